@@ -59,7 +59,9 @@ typedef enum {
   SA_ERR_CUDA = 4,          /* a CUDA runtime call failed (launch, copy, ...)     */
   SA_ERR_TIMEOUT = 5,       /* device: a bounded wait inside a kernel gave up    */
   SA_ERR_BAD_OFFSETS = 6,   /* device: offsets not a valid ragged partition      */
-  SA_ERR_NO_DEVICE = 7      /* no sm_100 device current                          */
+  SA_ERR_NO_DEVICE = 7,     /* no sm_100 device current                          */
+  SA_ERR_BAD_PAGES = 8      /* device: the free list ran out, a request does not fit its
+                               block table row, or a page id lies outside the cache */
 } sa_status;
 
 /* Limits. d must be 64 or 128. k may be 1..2048 for fp32 and bf16 alike; bf16
@@ -274,9 +276,9 @@ int sa_sketch_forward_grid(int k, int d, sa_dtype dt, int* clusters, int* cluste
 
 /*
  * Reads the device status word that the last call using `workspace` left behind.
- * It synchronises `stream` and returns SA_OK, SA_ERR_BAD_OFFSETS or SA_ERR_TIMEOUT,
- * or SA_ERR_CUDA if the copy itself failed. The word is cleared at the start of
- * every forward and backward call.
+ * It synchronises `stream` and returns SA_OK, SA_ERR_BAD_OFFSETS, SA_ERR_BAD_PAGES or
+ * SA_ERR_TIMEOUT, or SA_ERR_CUDA if the copy itself failed. Every call that has a
+ * workspace clears or overwrites the word.
  */
 int sa_sketch_get_device_status(const void* workspace, void* stream);
 
@@ -449,6 +451,143 @@ int sa_sketch_pack(const float* sketch, int64_t rows, int d, int format, void* c
                    float* scales, void* stream);
 int sa_sketch_unpack(const void* codes, const float* scales, int64_t rows, int d, int format,
                      float* sketch, void* stream);
+
+/*
+ * Multi-head cross attention from ragged queries to an encoder's states of other lengths.
+ * The pages' cross attention (sa_stca_keys_forward) has one head and reads one set of rows
+ * as keys and values; a ranker that stacks such layers ("100,000 videos in your pocket"
+ * blog, section "2. STCA reasons at two time scales") needs heads, keys apart from values,
+ * and its own projections around the attention. For user u, query row t in
+ * [q_offsets[u], q_offsets[u+1]) and head h, over the key rows j in [kv_offsets[u],
+ * kv_offsets[u+1]) that key_mask keeps, with key head h / (H / Hkv):
+ *   z_j = scale Q_th . K_jh,   out_th = sum_j softmax_j(z) V_jh,   lse_th = log sum_j exp z_j
+ * A row without any kept key gets out = 0 and lse = -inf.
+ *
+ *   Q          [n_q, H, d]    bf16, device; consecutive rows t are q_stride elements apart
+ *   K, V       [n_kv, Hkv, d] bf16, device; rows k_stride and v_stride elements apart (a
+ *              row's heads are contiguous: the two can be halves of one projection)
+ *   q_offsets, kv_offsets [R + 1] int64, device: 0 first, non-decreasing, the last one at
+ *              most n_q / n_kv. Rows at or past the last offset belong to no user: they are
+ *              not read, and the rows of out, lse and of the gradients there stay as they were.
+ *   key_mask   [n_kv] uint8, device, nullable: 0 drops the key row for every query. What a
+ *              dropped row holds is never used, not even as 0 times it (it may be NaN).
+ *   scale      > 0, finite (1 / sqrt(d) for scaled dot products)
+ *   out        [n_q, H, d] bf16, device   output (overwritten)
+ *   lse        [n_q, H]    fp32, device   output (overwritten); the backward needs it
+ * d in {64, 128}; 1 <= Hkv <= H <= 1024, H a multiple of Hkv; n_q, n_kv <= INT32_MAX;
+ * strides multiples of 8 and at least H d / Hkv d; pointers 16-byte aligned (key_mask: any).
+ * Outputs must not overlap inputs. Precision: products and sums in fp32; the weights enter
+ * the second product as bf16 relative to the row's running maximum; out is rounded once.
+ * Deterministic: two calls on the same inputs give bitwise-equal outputs. Workspace:
+ * sa_cross_attn_workspace_size(...) bytes, 256-aligned; errors follow sa_sketch_forward's
+ * conventions (bad offsets: SA_ERR_BAD_OFFSETS in the device status word, outputs
+ * unspecified). Enqueues on `stream`, never synchronises.
+ */
+size_t sa_cross_attn_workspace_size(int R, int64_t n_q, int64_t n_kv, int H, int Hkv, int d,
+                                    int backward);
+int sa_cross_attn_forward(const void* Q, int64_t q_stride, const int64_t* q_offsets, int R,
+                          int64_t n_q, int H, int d, const void* K, int64_t k_stride,
+                          const void* V, int64_t v_stride, const int64_t* kv_offsets,
+                          int64_t n_kv, int Hkv, const uint8_t* key_mask, float scale, void* out,
+                          float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of sa_cross_attn_forward given dout = dL/dout. With P the forward's weights:
+ *   dV_j = sum_t P_tj dout_t,  dS_tj = scale P_tj (dout_t . V_j - dout_t . out_t),
+ *   dQ_t = sum_j dS_tj K_j,    dK_j = sum_t dS_tj Q_t
+ * where the sums of dK and dV run over the user's query rows and the H / Hkv heads that
+ * share the key head. Rows no query attends to get 0 (dropped keys among them).
+ *
+ *   out, lse, dout   the forward's outputs for the same inputs; dL/dout [n_q, H, d] bf16
+ *   dQ [n_q, H, d], dK, dV [n_kv, Hkv, d]   bf16, device, contiguous, overwritten
+ * Everything else as for the forward; the weights and dS enter the products as bf16, the
+ * sums are fp32, each gradient is rounded once. Deterministic (no atomics).
+ */
+int sa_cross_attn_backward(const void* Q, int64_t q_stride, const int64_t* q_offsets, int R,
+                           int64_t n_q, int H, int d, const void* K, int64_t k_stride,
+                           const void* V, int64_t v_stride, const int64_t* kv_offsets,
+                           int64_t n_kv, int Hkv, const uint8_t* key_mask, float scale,
+                           const void* out, const float* lse, const void* dout, void* dQ, void* dK,
+                           void* dV, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The paged key-value cache that serves that attention one new token at a time. The cache
+ * holds K and V as [n_pages, Hkv, page_size, d] each (bf16, or SA_CODEC_FP8 codes with one
+ * fp32 scale per row in k_scales, v_scales [n_pages, Hkv, page_size], as sa_sketch_pack
+ * makes them). Request r's position p is row p mod page_size of page
+ * block_table[r][p / page_size]; its slot is page page_size + row. page_size is a power of
+ * two from 8 to 256. User-level caches reused across requests are the pages' subject
+ * ("100,000 videos in your pocket" blog, section "3. The system makes it cheap enough to
+ * matter", low-rank caching); their layout is not.
+ *
+ * sa_page_tables: block tables and slot maps from request lengths. Request r holds
+ * cached_lens[r] positions and gets new_lens[r] more. Pages for them are taken from
+ * free_pages[*free_used], free_pages[*free_used + 1], ... in request order (free_used
+ * null: from the start) and written to the request's row of block_table.
+ *   cached_lens, new_lens [R] int32, device, >= 0
+ *   free_pages  [n_free] int32, device     page ids not in use
+ *   free_used   int64, device, nullable    entries of free_pages taken by earlier calls
+ *   block_table [R, max_pages] int32, device, updated in place: the entries of the
+ *               ceil(cached / page_size) pages held are read, the new pages' are written,
+ *               all others stay as they were
+ *   slots       [n_slots] int64, device, written: the slot of every new position, requests
+ *               concatenated; -1 behind the last one, and where a held page's id is negative
+ *   new_offsets [R + 1] int64, device, written: prefix sums of new_lens
+ *   seq_lens    [R] int32, device, written: cached_lens + new_lens
+ *   free_used_out int64, device, written: *free_used + the pages taken
+ * All or nothing: a negative length, more new positions than n_slots or a length past
+ * INT32_MAX (SA_ERR_BAD_OFFSETS), a request longer than max_pages pages or too few free
+ * pages (SA_ERR_BAD_PAGES) are latched in the device status word; then no page is taken:
+ * slots are -1, new_offsets 0, seq_lens = cached_lens, free_used_out = *free_used, and
+ * block_table stays. R <= SA_MAX_USERS; n_slots, n_free <= INT32_MAX. block_table is the
+ * only argument that is both read and written; outputs must not overlap inputs. The
+ * workspace needs 256 bytes, 256-aligned. int32 arrays 4-byte, int64 arrays 8-byte aligned.
+ */
+int sa_page_tables(const int32_t* cached_lens, const int32_t* new_lens, int R, int page_size,
+                   const int32_t* free_pages, int64_t n_free, const int64_t* free_used,
+                   int32_t* block_table, int max_pages, int64_t n_slots, int64_t* slots,
+                   int64_t* new_offsets, int32_t* seq_lens, int64_t* free_used_out,
+                   void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * New rows into the cache: K, V [n, Hkv, d] bf16 (rows k_stride, v_stride elements apart,
+ * multiples of 8) go to slots[i]; a slot outside [0, n_pages page_size) is skipped (the
+ * padding of sa_page_tables is -1). SA_CODEC_BF16 copies the bits; SA_CODEC_FP8 stores
+ * s = max |row| / 448 (1 for a row of zeros) and the E4M3 codes of row / s as
+ * sa_sketch_pack does (finite rows). Slots named twice hold one of the rows, which one is
+ * not fixed. n_pages Hkv page_size <= INT32_MAX; d in {64, 128}; Hkv <= 1024; pointers
+ * 16-byte aligned (slots: 8). One kernel, no workspace.
+ */
+int sa_paged_append(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                    const int64_t* slots, int64_t n, int Hkv, int d, int format, void* k_cache,
+                    void* v_cache, float* k_scales, float* v_scales, int64_t n_pages,
+                    int page_size, void* stream);
+
+/*
+ * Attention of one new token per request over the paged cache: for request r and head h,
+ * over the positions p in [max(0, seq_lens[r] - window), seq_lens[r]) (window 0: all),
+ * with key head h / (H / Hkv):
+ *   z_p = scale Q_rh . K_p,   out_rh = sum_p softmax_p(z) V_p,   lse_rh = log sum_p exp z_p
+ * (sa_cross_attn_forward's computation with one query row; window = 10000 reads the recent
+ * branch's rows). A request of length 0 gets out = 0 and lse = -inf. The length is split
+ * over the GPU and the parts are joined in a fixed order: results are deterministic.
+ *   Q [R, H, d] bf16, rows q_stride elements apart (a multiple of 8); out [R, H, d] bf16;
+ *   lse [R, H] fp32, nullable
+ *   block_table [R, max_pages] int32, seq_lens [R] int32, device. A length outside
+ *   [0, max_pages page_size] (SA_ERR_BAD_OFFSETS) or a page id in reach outside [0, n_pages)
+ *   (SA_ERR_BAD_PAGES) is latched in the device status word and nothing outside the cache
+ *   is read; the outputs are then unspecified. Entries past the length are not read as ids.
+ * Rows past the length and before the window are never used, whatever they hold. d in
+ * {64, 128}; H / Hkv <= 64; H <= 1024; n_pages Hkv page_size <= INT32_MAX; R <=
+ * SA_MAX_USERS. Precision as for the forward above; FP8 codes are exact in bf16, their
+ * scales enter in fp32. Workspace: sa_paged_attn_workspace_size(...) bytes, 256-aligned.
+ */
+size_t sa_paged_attn_workspace_size(int R, int H, int Hkv, int d);
+int sa_paged_attn(const void* Q, int64_t q_stride, int R, int H, int d, const void* k_cache,
+                  const void* v_cache, const float* k_scales, const float* v_scales, int format,
+                  int64_t n_pages, int page_size, int Hkv, const int32_t* block_table,
+                  int max_pages, const int32_t* seq_lens, int64_t window, float scale, void* out,
+                  float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* Static, human-readable name of a status code. */
 const char* sa_status_string(int status);

@@ -27,6 +27,7 @@ SA_ERR_CUDA = 4
 SA_ERR_TIMEOUT = 5
 SA_ERR_BAD_OFFSETS = 6
 SA_ERR_NO_DEVICE = 7
+SA_ERR_BAD_PAGES = 8
 
 EXPORTED = ("sa_sketch_workspace_size", "sa_sketch_forward", "sa_sketch_backward",
             "sa_sketch_get_device_status", "sa_status_string", "sa_sketch_debug_wait_timeout",
@@ -36,7 +37,9 @@ EXPORTED = ("sa_sketch_workspace_size", "sa_sketch_forward", "sa_sketch_backward
             "sa_sketch_forward_host_buffer_size", "sa_sketch_forward_host",
             "sa_sketch_forward_host_status", "sa_sketch_host_parts", "sa_sketch_forward_grid",
             "sa_stca_keys_workspace_size", "sa_stca_keys_forward", "sa_stca_keys_backward",
-            "sa_stca_recent_ranges")
+            "sa_stca_recent_ranges", "sa_cross_attn_workspace_size", "sa_cross_attn_forward",
+            "sa_cross_attn_backward", "sa_page_tables", "sa_paged_append",
+            "sa_paged_attn_workspace_size", "sa_paged_attn")
 SA_CODEC_BF16 = 0
 SA_CODEC_FP8 = 1
 
@@ -108,6 +111,25 @@ def _load() -> ctypes.CDLL:
                                           vp, vp, i32, vp, vp, vp, vp, sz, vp]
     lib.sa_stca_recent_ranges.restype = i32
     lib.sa_stca_recent_ranges.argtypes = [vp, i32, i64, vp, vp, vp]
+    f32 = ctypes.c_float
+    lib.sa_cross_attn_workspace_size.restype = sz
+    lib.sa_cross_attn_workspace_size.argtypes = [i32, i64, i64, i32, i32, i32, i32]
+    cross = [vp, i64, vp, i32, i64, i32, i32, vp, i64, vp, i64, vp, i64, i32, vp, f32]
+    lib.sa_cross_attn_forward.restype = i32
+    lib.sa_cross_attn_forward.argtypes = cross + [vp, vp, vp, sz, vp]
+    lib.sa_cross_attn_backward.restype = i32
+    lib.sa_cross_attn_backward.argtypes = cross + [vp] * 7 + [sz, vp]
+    lib.sa_page_tables.restype = i32
+    lib.sa_page_tables.argtypes = [vp, vp, i32, i32, vp, i64, vp, vp, i32, i64, vp, vp, vp, vp, vp,
+                                   sz, vp]
+    lib.sa_paged_append.restype = i32
+    lib.sa_paged_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, i64,
+                                    i32, vp]
+    lib.sa_paged_attn_workspace_size.restype = sz
+    lib.sa_paged_attn_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.sa_paged_attn.restype = i32
+    lib.sa_paged_attn.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp, vp, i32, i64, i32, i32, vp,
+                                  i32, vp, i64, f32, vp, vp, vp, sz, vp]
     return lib
 
 
@@ -256,6 +278,52 @@ def sketch_unpack(packed: dict, stream=None) -> torch.Tensor:
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_unpack")
     return S
+
+
+def sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, backward) -> int:
+    return int(_lib.sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, int(backward)))
+
+
+def sa_cross_attn_forward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V, v_stride,
+                          kv_offsets, n_kv, Hkv, key_mask, scale, out, lse, workspace, ws_bytes,
+                          stream) -> int:
+    return int(_lib.sa_cross_attn_forward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V,
+                                          v_stride, kv_offsets, n_kv, Hkv, key_mask, scale, out,
+                                          lse, workspace, ws_bytes, stream))
+
+
+def sa_cross_attn_backward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V, v_stride,
+                           kv_offsets, n_kv, Hkv, key_mask, scale, out, lse, dout, dQ, dK, dV,
+                           workspace, ws_bytes, stream) -> int:
+    return int(_lib.sa_cross_attn_backward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V,
+                                           v_stride, kv_offsets, n_kv, Hkv, key_mask, scale, out,
+                                           lse, dout, dQ, dK, dV, workspace, ws_bytes, stream))
+
+
+def sa_page_tables(cached_lens, new_lens, R, page_size, free_pages, n_free, free_used, block_table,
+                   max_pages, n_slots, slots, new_offsets, seq_lens, free_used_out, workspace,
+                   ws_bytes, stream) -> int:
+    return int(_lib.sa_page_tables(cached_lens, new_lens, R, page_size, free_pages, n_free,
+                                   free_used, block_table, max_pages, n_slots, slots, new_offsets,
+                                   seq_lens, free_used_out, workspace, ws_bytes, stream))
+
+
+def sa_paged_append(K, k_stride, V, v_stride, slots, n, Hkv, d, fmt, k_cache, v_cache, k_scales,
+                    v_scales, n_pages, page_size, stream) -> int:
+    return int(_lib.sa_paged_append(K, k_stride, V, v_stride, slots, n, Hkv, d, fmt, k_cache,
+                                    v_cache, k_scales, v_scales, n_pages, page_size, stream))
+
+
+def sa_paged_attn_workspace_size(R, H, Hkv, d) -> int:
+    return int(_lib.sa_paged_attn_workspace_size(R, H, Hkv, d))
+
+
+def sa_paged_attn(Q, q_stride, R, H, d, k_cache, v_cache, k_scales, v_scales, fmt, n_pages,
+                  page_size, Hkv, block_table, max_pages, seq_lens, window, scale, out, lse,
+                  workspace, ws_bytes, stream) -> int:
+    return int(_lib.sa_paged_attn(Q, q_stride, R, H, d, k_cache, v_cache, k_scales, v_scales, fmt,
+                                  n_pages, page_size, Hkv, block_table, max_pages, seq_lens,
+                                  window, scale, out, lse, workspace, ws_bytes, stream))
 
 
 def sa_sketch_get_device_status(workspace, stream) -> int:
@@ -660,6 +728,268 @@ def stca_keys_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Te
                                    _ptr(ws), ws.nbytes, _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_keys_backward")
+    out["_ws"] = ws
+    return out
+
+
+def _rows_stride(where: str, name: str, x: torch.Tensor, heads: int, d: int) -> int:
+    """Elements between consecutive rows of x [n, heads, d], whose heads are contiguous (a
+    slice of a wider projection is fine)."""
+    _require((d == 1 or x.stride(2) == 1) and (heads == 1 or x.stride(1) == d), where,
+             f"{name}: a row's heads must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def _check_heads(where: str, name: str, x, n, d, dev, heads=None) -> None:
+    _require(isinstance(x, torch.Tensor) and x.dim() == 3, where, f"{name} must be [n, heads, d]")
+    _require(x.dtype == torch.bfloat16, where, f"{name} has dtype {x.dtype}, expected torch.bfloat16")
+    want = (n, x.shape[1] if heads is None else heads, d)
+    _require(tuple(x.shape) == want, where, f"{name} has shape {tuple(x.shape)}, expected {want}")
+    _require(x.device == dev, where, f"{name} is on {x.device}, expected {dev}")
+
+
+def _scale(scale, d: int) -> float:
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
+    _require(isinstance(Q, torch.Tensor) and Q.dim() == 3, where, "Q must be [n, heads, d]")
+    _require(isinstance(K, torch.Tensor) and K.dim() == 3, where, "K must be [n, heads, d]")
+    dev, (n_q, H, d), (n_kv, Hkv, _) = Q.device, Q.shape, K.shape
+    _check_heads(where, "Q", Q, n_q, d, dev)
+    _check_heads(where, "K", K, n_kv, d, dev)
+    _check_heads(where, "V", V, n_kv, d, dev, Hkv)
+    _require(Hkv >= 1 and H >= 1 and H % Hkv == 0, where,
+             f"{H} query heads cannot share {Hkv} key heads")
+    _require(isinstance(q_offsets, torch.Tensor) and q_offsets.dim() == 1
+             and q_offsets.numel() >= 1, where, "q_offsets must be a 1-D tensor with R + 1 entries")
+    R = q_offsets.numel() - 1
+    _check_tensor(where, "q_offsets", q_offsets, (R + 1,), torch.int64, dev)
+    _check_tensor(where, "kv_offsets", kv_offsets, (R + 1,), torch.int64, dev)
+    if key_mask is not None:
+        _require(isinstance(key_mask, torch.Tensor) and key_mask.dtype in (torch.bool, torch.uint8),
+                 where, "key_mask must be a bool or uint8 tensor")
+        _check_tensor(where, "key_mask", key_mask, (n_kv,), key_mask.dtype, dev)
+    _check_cuda(where, Q)
+    strides = tuple(_rows_stride(where, name, x, heads, d)
+                    for name, x, heads in (("Q", Q, H), ("K", K, Hkv), ("V", V, Hkv)))
+    return R, n_q, H, d, n_kv, Hkv, dev, strides
+
+
+def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
+                    kv_offsets: torch.Tensor, *, key_mask: torch.Tensor | None = None,
+                    scale: float | None = None, out: dict | None = None,
+                    ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Multi-head cross attention from user u's query rows Q[q_offsets[u]:q_offsets[u+1]] to its
+    key rows K, V[kv_offsets[u]:kv_offsets[u+1]] (sa_cross_attn_forward). Q [n_q, H, d], K and V
+    [n_kv, Hkv, d] bf16 (rows may be strided, a row's heads contiguous), offsets [R + 1] int64,
+    key_mask [n_kv] bool (False drops a key row), scale 1 / sqrt(d) by default. Returns out
+    [n_q, H, d] bf16 and lse [n_q, H] fp32, written into `out` ({"out", "lse"}) when given."""
+    where = "cross_attention"
+    R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
+                                                              key_mask)
+    if out is None:
+        out = {"out": torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16),
+               "lse": torch.empty(n_q, H, device=dev, dtype=torch.float32)}
+    else:
+        out = dict(out)
+        _check_tensor(where, "out", out.get("out"), (n_q, H, d), torch.bfloat16, dev)
+        _check_tensor(where, "lse", out.get("lse"), (n_q, H), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if ws is None:
+            nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 0)
+            if nb == 0:
+                raise SketchAttentionError(SA_ERR_UNSUPPORTED, "sa_cross_attn_workspace_size")
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        st = sa_cross_attn_forward(_ptr(Q), qs, _ptr(q_offsets), R, n_q, H, d, _ptr(K), ks, _ptr(V),
+                                   vs, _ptr(kv_offsets), n_kv, Hkv, _ptr(key_mask),
+                                   _scale(scale, d), _ptr(out["out"]), _ptr(out["lse"]), _ptr(ws),
+                                   ws.nbytes, _stream(stream, dev))
+    if st != SA_OK:
+        raise SketchAttentionError(st, "sa_cross_attn_forward")
+    out["_ws"] = ws
+    return out
+
+
+def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor,
+                             V: torch.Tensor, kv_offsets: torch.Tensor, fwd: dict,
+                             dout: torch.Tensor, *, key_mask: torch.Tensor | None = None,
+                             scale: float | None = None, out: dict | None = None,
+                             ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of cross_attention given its outputs `fwd` (out, lse) and dout = dL/dout
+    [n_q, H, d] bf16: dQ [n_q, H, d], dK and dV [n_kv, Hkv, d], bf16 (sa_cross_attn_backward),
+    written into `out` ({"dQ", "dK", "dV"}) when given. Other arguments as passed to the
+    forward."""
+    where = "cross_attention_backward"
+    R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
+                                                              key_mask)
+    bf = torch.bfloat16
+    _check_tensor(where, "out", fwd.get("out"), (n_q, H, d), bf, dev)
+    _check_tensor(where, "lse", fwd.get("lse"), (n_q, H), torch.float32, dev)
+    _check_tensor(where, "dout", dout, (n_q, H, d), bf, dev)
+    if out is None:
+        out = {"dQ": torch.empty(n_q, H, d, device=dev, dtype=bf),
+               "dK": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf),
+               "dV": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf)}
+    else:
+        out = dict(out)
+        _check_tensor(where, "dQ", out.get("dQ"), (n_q, H, d), bf, dev)
+        _check_tensor(where, "dK", out.get("dK"), (n_kv, Hkv, d), bf, dev)
+        _check_tensor(where, "dV", out.get("dV"), (n_kv, Hkv, d), bf, dev)
+    with torch.cuda.device(dev):
+        if ws is None:
+            nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 1)
+            if nb == 0:
+                raise SketchAttentionError(SA_ERR_UNSUPPORTED, "sa_cross_attn_workspace_size")
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        st = sa_cross_attn_backward(_ptr(Q), qs, _ptr(q_offsets), R, n_q, H, d, _ptr(K), ks,
+                                    _ptr(V), vs, _ptr(kv_offsets), n_kv, Hkv, _ptr(key_mask),
+                                    _scale(scale, d), _ptr(fwd["out"]), _ptr(fwd["lse"]),
+                                    _ptr(dout), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]),
+                                    _ptr(ws), ws.nbytes, _stream(stream, dev))
+    if st != SA_OK:
+        raise SketchAttentionError(st, "sa_cross_attn_backward")
+    out["_ws"] = ws
+    return out
+
+
+def paged_cache(n_pages: int, Hkv: int, page_size: int, d: int, *, fmt: int = SA_CODEC_BF16,
+                device="cuda") -> dict:
+    """A paged key-value cache: K and V [n_pages, Hkv, page_size, d] (bfloat16, or
+    float8_e4m3fn with k_scales and v_scales [n_pages, Hkv, page_size] fp32). The rows start
+    unwritten."""
+    where = "paged_cache"
+    _require(fmt in (SA_CODEC_BF16, SA_CODEC_FP8), where, f"unknown format {fmt}")
+    shape = (int(n_pages), int(Hkv), int(page_size), int(d))
+    _require(min(shape) >= 0, where, f"negative size in {shape}")
+    kind = torch.float8_e4m3fn if fmt == SA_CODEC_FP8 else torch.bfloat16
+    cache = {n: torch.empty(shape, dtype=kind, device=device) for n in ("K", "V")}
+    for n in ("k_scales", "v_scales"):
+        cache[n] = (torch.empty(shape[:3], dtype=torch.float32, device=device)
+                    if fmt == SA_CODEC_FP8 else None)
+    return cache
+
+
+def _check_cache(where: str, cache: dict, dev) -> tuple[int, int, int, int, int]:
+    """(format, n_pages, Hkv, page_size, d) of a paged_cache."""
+    K = cache.get("K") if isinstance(cache, dict) else None
+    _require(isinstance(K, torch.Tensor) and K.dim() == 4, where,
+             "cache must hold K [n_pages, Hkv, page_size, d]")
+    _require(K.dtype in (torch.bfloat16, torch.float8_e4m3fn), where,
+             f"cache K has dtype {K.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+    fp8 = K.dtype == torch.float8_e4m3fn
+    _check_tensor(where, "cache K", K, tuple(K.shape), K.dtype, dev)
+    _check_tensor(where, "cache V", cache.get("V"), tuple(K.shape), K.dtype, dev)
+    for n in ("k_scales", "v_scales"):
+        if fp8:
+            _check_tensor(where, f"cache {n}", cache.get(n), tuple(K.shape[:3]), torch.float32, dev)
+        else:
+            _require(cache.get(n) is None, where, f"cache {n} belongs to an FP8 cache")
+    return (SA_CODEC_FP8 if fp8 else SA_CODEC_BF16, *K.shape)
+
+
+def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                block_table: torch.Tensor, page_size: int, n_slots: int, *,
+                free_used: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                stream=None) -> dict:
+    """Pages and slots for new_lens [R] new positions of requests that hold cached_lens [R]
+    (int32; sa_page_tables): takes pages from free_pages (int32), from entry free_used (int64
+    [1]; None: 0) on, and writes them into block_table [R, max_pages] (int32) in place. n_slots:
+    room for the new positions (their number, or more: the rest is -1). Returns slots [n_slots]
+    and new_offsets [R + 1] int64, seq_lens [R] int32, free_used [1] int64. Too few pages and
+    the like are latched in the device status (device_status(result["_ws"])) and change
+    nothing."""
+    where = "page_tables"
+    _require(isinstance(cached_lens, torch.Tensor) and cached_lens.dim() == 1, where,
+             "cached_lens must be a 1-D tensor")
+    R, dev = cached_lens.numel(), cached_lens.device
+    i32, i64 = torch.int32, torch.int64
+    _check_tensor(where, "cached_lens", cached_lens, (R,), i32, dev)
+    _check_tensor(where, "new_lens", new_lens, (R,), i32, dev)
+    _require(isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1, where,
+             "free_pages must be a 1-D tensor")
+    _check_tensor(where, "free_pages", free_pages, (free_pages.numel(),), i32, dev)
+    _require(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, where,
+             "block_table must be [R, max_pages]")
+    _check_tensor(where, "block_table", block_table, (R, block_table.shape[1]), i32, dev)
+    _check_tensor(where, "free_used", free_used, (1,), i64, dev, optional=True)
+    _check_cuda(where, cached_lens)
+    _require(int(n_slots) >= 0, where, "n_slots must not be negative")
+    out = {"slots": torch.empty(int(n_slots), dtype=i64, device=dev),
+           "new_offsets": torch.empty(R + 1, dtype=i64, device=dev),
+           "seq_lens": torch.empty(R, dtype=i32, device=dev),
+           "free_used": torch.empty(1, dtype=i64, device=dev)}
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        st = sa_page_tables(_ptr(cached_lens), _ptr(new_lens), R, int(page_size), _ptr(free_pages),
+                            free_pages.numel(), _ptr(free_used), _ptr(block_table),
+                            block_table.shape[1], int(n_slots), _ptr(out["slots"]),
+                            _ptr(out["new_offsets"]), _ptr(out["seq_lens"]), _ptr(out["free_used"]),
+                            _ptr(ws), ws.nbytes, _stream(stream, dev))
+    if st != SA_OK:
+        raise SketchAttentionError(st, "sa_page_tables")
+    out["_ws"] = ws
+    return out
+
+
+def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: dict, *,
+                 stream=None) -> None:
+    """Writes rows K, V [n, Hkv, d] bf16 (rows may be strided) into the slots [n] int64 of a
+    paged_cache, quantised for an FP8 cache (sa_paged_append). Slots outside the cache, such as
+    the -1 of page_tables, are skipped."""
+    where = "paged_append"
+    _require(isinstance(K, torch.Tensor) and K.dim() == 3, where, "K must be [n, heads, d]")
+    dev = K.device
+    fmt, n_pages, Hkv, page_size, d = _check_cache(where, cache, dev)
+    _check_heads(where, "K", K, K.shape[0], d, dev, Hkv)
+    _check_heads(where, "V", V, K.shape[0], d, dev, Hkv)
+    _check_tensor(where, "slots", slots, (K.shape[0],), torch.int64, dev)
+    _check_cuda(where, K)
+    ks, vs = _rows_stride(where, "K", K, Hkv, d), _rows_stride(where, "V", V, Hkv, d)
+    with torch.cuda.device(dev):
+        st = sa_paged_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), K.shape[0], Hkv, d, fmt,
+                             _ptr(cache["K"]), _ptr(cache["V"]), _ptr(cache["k_scales"]),
+                             _ptr(cache["v_scales"]), n_pages, page_size, _stream(stream, dev))
+    if st != SA_OK:
+        raise SketchAttentionError(st, "sa_paged_append")
+
+
+def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
+                    seq_lens: torch.Tensor, *, window: int = 0, scale: float | None = None,
+                    ws: torch.Tensor | None = None, stream=None) -> dict:
+    """Attention of one new token per request, Q [R, H, d] bf16, over the last `window`
+    positions (0: all) of its seq_lens [R] int32 in a paged_cache, through block_table
+    [R, max_pages] int32 (sa_paged_attn). Returns out [R, H, d] bf16 and lse [R, H] fp32. Bad
+    lengths and page ids are latched in the device status (device_status(result["_ws"]))."""
+    where = "paged_attention"
+    _require(isinstance(Q, torch.Tensor) and Q.dim() == 3, where, "Q must be [n, heads, d]")
+    dev, (R, H, d) = Q.device, Q.shape
+    fmt, n_pages, Hkv, page_size, cd = _check_cache(where, cache, dev)
+    _check_heads(where, "Q", Q, R, cd, dev)
+    _require(Hkv >= 1 and H >= 1 and H % Hkv == 0, where,
+             f"{H} query heads cannot share {Hkv} key heads")
+    _require(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, where,
+             "block_table must be [R, max_pages]")
+    _check_tensor(where, "block_table", block_table, (R, block_table.shape[1]), torch.int32, dev)
+    _check_tensor(where, "seq_lens", seq_lens, (R,), torch.int32, dev)
+    _check_cuda(where, Q)
+    qs = _rows_stride(where, "Q", Q, H, d)
+    out = {"out": torch.empty(R, H, d, device=dev, dtype=torch.bfloat16),
+           "lse": torch.empty(R, H, device=dev, dtype=torch.float32)}
+    with torch.cuda.device(dev):
+        if ws is None:
+            nb = sa_paged_attn_workspace_size(R, H, Hkv, d)
+            if nb == 0:
+                raise SketchAttentionError(SA_ERR_UNSUPPORTED, "sa_paged_attn_workspace_size")
+            ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        st = sa_paged_attn(_ptr(Q), qs, R, H, d, _ptr(cache["K"]), _ptr(cache["V"]),
+                           _ptr(cache["k_scales"]), _ptr(cache["v_scales"]), fmt, n_pages,
+                           page_size, Hkv, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+                           int(window), _scale(scale, d), _ptr(out["out"]), _ptr(out["lse"]),
+                           _ptr(ws), ws.nbytes, _stream(stream, dev))
+    if st != SA_OK:
+        raise SketchAttentionError(st, "sa_paged_attn")
     out["_ws"] = ws
     return out
 

@@ -204,6 +204,14 @@ sa_status cuda_status(cudaError_t e) {
 }
 
 }  // namespace
+
+int device_sms(int* sms) {
+  Device dev;
+  const sa_status st = current_device(&dev);
+  if (st == SA_OK) *sms = dev.sms;
+  return st;
+}
+
 }  // namespace sa
 
 namespace sa {
@@ -769,6 +777,7 @@ const char* sa_status_string(int status) {
     case SA_ERR_CUDA: return "SA_ERR_CUDA: a CUDA call failed";
     case SA_ERR_TIMEOUT: return "SA_ERR_TIMEOUT: a bounded wait inside a kernel gave up";
     case SA_ERR_BAD_OFFSETS: return "SA_ERR_BAD_OFFSETS: offsets are not a ragged partition";
+    case SA_ERR_BAD_PAGES: return "SA_ERR_BAD_PAGES: no free page, a row too short or a page id outside the cache";
     case SA_ERR_NO_DEVICE: return "SA_ERR_NO_DEVICE: no sm_100 device is current";
     default: return "unknown sa_status";
   }

@@ -303,6 +303,100 @@ cudaError_t launch_sketch_pack(const float* S, long long rows, int d, int format
 cudaError_t launch_sketch_unpack(const void* codes, const float* scales, long long rows, int d,
                                  int format, float* S, cudaStream_t s);
 
+// ---- multi-head cross attention (sa_cross.cu)
+struct CrossPlan {  // workspace layout (byte offsets, 256-aligned)
+  size_t hdr = 0, delta = 0, total = 0;
+};
+size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, bool backward,
+                  int sms, CrossPlan* p);
+struct CrossArgs {
+  const void* Q;          // bf16 [n_q, H, d], rows q_stride elements apart
+  const void* K;          // bf16 [n_kv, Hkv, d]
+  const void* V;
+  long long q_stride, k_stride, v_stride;
+  const int64_t* qoff;    // [R + 1]
+  const int64_t* koff;
+  int R, H, Hkv, d;
+  long long n_q, n_kv;
+  const uint8_t* mask;    // [n_kv], nullable
+  float scale;
+  void* out;              // bf16 [n_q, H, d] (read by the backward)
+  float* lse;             // [n_q, H]
+  const void* dout;       // backward only
+  void *dQ, *dK, *dV;
+  void* workspace;
+  CrossPlan plan;
+  int sms;
+};
+cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s);
+cudaError_t launch_cross_backward(const CrossArgs& a, cudaStream_t s);
+
+// ---- paged key-value cache (sa_paged.cu)
+struct PageTablesArgs {
+  const int32_t* cached;
+  const int32_t* fresh;
+  int R, log2_page;
+  const int32_t* free_pages;
+  long long n_free;
+  const int64_t* free_used;   // nullable
+  int32_t* table;
+  int max_pages;
+  long long n_slots;
+  int64_t* slots;
+  int64_t* new_offsets;
+  int32_t* seq_lens;
+  int64_t* free_used_out;
+  WsHeader* hdr;
+  int sms;
+};
+cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t s);
+struct PagedAppendArgs {
+  const void* K;
+  const void* V;
+  long long k_stride, v_stride;
+  const int64_t* slots;
+  long long n, n_pages;
+  int Hkv, d, log2_page;
+  bool fp8;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;
+  float* v_scales;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+
+// ---- attention over the paged cache (sa_paged_attn.cu)
+struct PagedAttnPlan {
+  size_t hdr = 0, total = 0;
+};
+size_t paged_attn_plan(int R, int H, int Hkv, int d, int sms, PagedAttnPlan* p);
+struct PagedAttnArgs {
+  const void* Q;
+  long long q_stride;
+  int R, H, Hkv, d;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  bool fp8;
+  long long n_pages;
+  int log2_page;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* seq_lens;
+  long long window;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  PagedAttnPlan plan;
+  int sms;
+};
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
+
+// SM count of the current device (SA_OK, or SA_ERR_NO_DEVICE when it is no sm_100)
+int device_sms(int* sms);
+
 // the measurement hook's events (sa_sketch_profile_events) recorded around a main kernel
 extern thread_local cudaEvent_t g_prof_start;
 extern thread_local cudaEvent_t g_prof_stop;
