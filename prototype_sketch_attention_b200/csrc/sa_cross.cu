@@ -4,22 +4,82 @@
 #include <cmath>
 
 #include "sa_common.cuh"
+#include "sa_cross.cuh"
 #include "sa_internal.h"
 
 namespace sa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+using cross::kLog2e;
 
-__global__ void cross_check_kernel(const int64_t* qoff, const int64_t* koff, int R, long long n_q,
-                                   long long n_kv, WsHeader* hdr) {
+// Block 0 lists the query tiles (pairs of 128-row tiles: pair_tokens tokens), block 1 the key
+// tiles (128 rows). Both check both offset arrays; bad offsets leave no tiles.
+__global__ void __launch_bounds__(1024) cross_schedule_kernel(const int64_t* __restrict__ qoff,
+                                                              const int64_t* __restrict__ koff,
+                                                              int R, long long n_q, long long n_kv,
+                                                              int pair_tokens, WsHeader* hdr,
+                                                              cross::Tile* __restrict__ qtiles,
+                                                              cross::Tile* __restrict__ ktiles) {
+  griddep_launch_dependents();
+  __shared__ int first[1025], part[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool keys = blockIdx.x == 1;
+  const int64_t* off = keys ? koff : qoff;
+  cross::Tile* tiles = keys ? ktiles : qtiles;
+  const int per = keys ? 128 : pair_tokens;
   int bad = 0;
-  for (int u = threadIdx.x; u < R; u += blockDim.x)
+  for (int u = tid; u < R; u += 1024)
     if (qoff[u + 1] < qoff[u] || koff[u + 1] < koff[u]) bad = 1;
-  if (threadIdx.x == 0 && (qoff[0] != 0 || koff[0] != 0 || qoff[R] > n_q || koff[R] > n_kv)) bad = 1;
+  if (tid == 0 && (qoff[0] != 0 || koff[0] != 0 || qoff[R] > n_q || koff[R] > n_kv)) bad = 1;
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) hdr->status = bad ? SA_ERR_BAD_OFFSETS : 0;
+  int base = 0;
+  if (!bad) {
+    for (int u0 = 0; u0 < R; u0 += 1024) {
+      const int u = u0 + tid, nu = min(1024, R - u0);
+      const int n = u < R ? (int)((off[u + 1] - off[u] + per - 1) / per) : 0;
+      int x = n;  // inclusive prefix sum over the block
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) part[warp] = x;
+      __syncthreads();
+      if (warp == 0) {
+        int y = part[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int z = __shfl_up_sync(0xffffffffu, y, o);
+          if (lane >= o) y += z;
+        }
+        part[lane] = y;
+      }
+      __syncthreads();
+      x += warp ? part[warp - 1] : 0;
+      first[tid + 1] = x;
+      if (tid == 0) first[0] = 0;
+      __syncthreads();
+      const int total = first[nu];
+      for (int i = tid; i < total; i += 1024) {
+        int lo = 0, hi = nu;  // first[lo] <= i < first[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first[mid] <= i) lo = mid; else hi = mid;
+        }
+        tiles[base + i] = cross::Tile{u0 + lo, i - first[lo]};
+      }
+      base += total;
+      __syncthreads();
+    }
+  }
+  if (tid == 0) {
+    if (keys) {
+      hdr->pad[0] = base;
+    } else {
+      hdr->total_tiles = base;
+      hdr->status = bad ? SA_ERR_BAD_OFFSETS : SA_OK;
+    }
+  }
 }
 
 // the user whose rows [off[u], off[u + 1]) hold row t, or -1
@@ -47,40 +107,6 @@ __device__ __forceinline__ float dot_row(const float (&a)[N], const float (&b)[N
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
-}
-
-template <int N>
-__global__ void __launch_bounds__(128) cross_fwd_kernel(CrossArgs a, const WsHeader* hdr) {
-  if (read_status(&hdr->status) != 0) return;
-  constexpr int D = 32 * N;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
-  const long long t = w / a.H;
-  const int h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  if (t >= a.n_q) return;
-  const int u = user_of_row(a.qoff, a.R, t);
-  if (u < 0) return;
-  float q[N], o[N], k[N];
-  load_row<N>((const __nv_bfloat16*)a.Q + t * a.q_stride + h * D, lane, q);
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (long long j = a.koff[u]; j < a.koff[u + 1]; ++j) {
-    if (a.mask && !a.mask[j]) continue;
-    load_row<N>((const __nv_bfloat16*)a.K + j * a.k_stride + hk * D, lane, k);
-    const float z = dot_row<N>(q, k) * a.scale * kLog2e;
-    const float mn = fmaxf(m, z), f = ex2_approx(m - mn), p = ex2_approx(z - mn);
-    load_row<N>((const __nv_bfloat16*)a.V + j * a.v_stride + hk * D, lane, k);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * k[i];
-    l = l * f + p;
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = (__nv_bfloat16*)a.out + (t * a.H + h) * D;
-#pragma unroll
-  for (int i = 0; i < N; ++i) out[lane + 32 * i] = __float2bfloat16(o[i] * inv);
-  if (lane == 0) a.lse[t * a.H + h] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
 }
 
 // dQ of one (row, head), and delta = dout . out
@@ -168,8 +194,45 @@ cudaError_t backward_t(const CrossArgs& a, WsHeader* hdr, float* delta, cudaStre
 
 }  // namespace
 
+namespace {
+
+cross::CrossGeo geometry(int R, long long n_q, long long n_kv, int H, int Hkv, int sms) {
+  cross::CrossGeo g;
+  const int G = H / Hkv;
+  g.pg = G & -G;
+  if (g.pg > 128) g.pg = 128;
+  const long long pair = 256 / g.pg, some = R < n_q ? R : n_q;
+  g.pair_tiles = n_q / pair + some;
+  g.key_tiles = n_kv / 128 + (R < n_kv ? R : n_kv);
+  // With fewer CTAs than SMs (about one per user and head group, or per full tile), the
+  // keys are split so that the SMs fill up, down to four key tiles a split.
+  const long long full = (n_q + pair - 1) / pair;
+  const long long ctas = (full > some ? full : some) * (H / g.pg);
+  long long s = ctas > 0 ? sms / ctas : 1;
+  const long long most = R > 0 ? n_kv / R / 512 : 1;
+  if (s > most) s = most;
+  g.splits = s < 1 ? 1 : (int)s;
+  return g;
+}
+
+}  // namespace
+
+bool cross::tmap_heads(CUtensorMap* m, const void* base, long long n, int heads, int d,
+                       long long stride, int box_heads, int box_rows) {
+  auto fn = tmap_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)(n > 0 ? n : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, bool backward,
                   int sms, CrossPlan* p) {
+  const cross::CrossGeo g = geometry(R, n_q, n_kv, H, Hkv, sms);
   CrossPlan q;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -178,28 +241,45 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
     return at;
   };
   q.hdr = take(sizeof(WsHeader));
-  if (backward) q.delta = take((size_t)n_q * H * sizeof(float));
+  q.qtiles = take((size_t)g.pair_tiles * sizeof(cross::Tile));
+  q.ktiles = take((size_t)g.key_tiles * sizeof(cross::Tile));
+  if (backward) {
+    q.delta = take((size_t)n_q * H * sizeof(float));
+  } else if (g.splits > 1) {
+    q.part_o = take((size_t)g.splits * n_q * H * d * sizeof(float));
+    q.part_lse = take((size_t)g.splits * n_q * H * sizeof(float));
+  }
   q.total = o;
   if (p) *p = q;
   return q.total;
 }
 
-cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
-  WsHeader* hdr = reinterpret_cast<WsHeader*>(static_cast<uint8_t*>(a.workspace) + a.plan.hdr);
-  cross_check_kernel<<<1, 256, 0, s>>>(a.qoff, a.koff, a.R, a.n_q, a.n_kv, hdr);
-  const long long n = (a.n_q * a.H + 3) / 4;
-  if (n > 0) {
-    if (a.d == 64) cross_fwd_kernel<2><<<(unsigned)n, 128, 0, s>>>(a, hdr);
-    else cross_fwd_kernel<4><<<(unsigned)n, 128, 0, s>>>(a, hdr);
-  }
+namespace {
+cudaError_t launch_schedule(const CrossArgs& a, const cross::CrossGeo& g, cudaStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  cross_schedule_kernel<<<2, 1024, 0, s>>>(
+      a.qoff, a.koff, a.R, a.n_q, a.n_kv, 256 / g.pg, reinterpret_cast<WsHeader*>(ws + a.plan.hdr),
+      reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
+      reinterpret_cast<cross::Tile*>(ws + a.plan.ktiles));
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
+  CrossArgs b = a;
+  if (b.n_kv == 0) b.K = b.V = b.Q;  // nothing is read through their tensor maps
+  const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
+  const cudaError_t e = launch_schedule(a, g, s);
+  return e != cudaSuccess || g.pair_tiles == 0 ? e : cross::launch_fwd(b, g, s);
 }
 
 cudaError_t launch_cross_backward(const CrossArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws + a.plan.hdr);
   float* delta = reinterpret_cast<float*>(ws + a.plan.delta);
-  cross_check_kernel<<<1, 256, 0, s>>>(a.qoff, a.koff, a.R, a.n_q, a.n_kv, hdr);
+  const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
+  const cudaError_t e = launch_schedule(a, g, s);
+  if (e != cudaSuccess) return e;
   return a.d == 64 ? backward_t<2>(a, hdr, delta, s) : backward_t<4>(a, hdr, delta, s);
 }
 

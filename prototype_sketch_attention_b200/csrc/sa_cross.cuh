@@ -1,0 +1,139 @@
+// Device helpers shared by the multi-head cross attention's kernels (sm_100a).
+//
+// Rows. The G = H / Hkv query heads that share a key head are packed into the rows of a tile:
+// with PG the largest power of two that divides G (at most 128), row r of a tile is token
+// t0 + r / PG and head hu PG + r mod PG of head group hu < H / PG, so a key tile is read once
+// for PG heads. A tile has 128 rows, 128 / PG tokens.
+#pragma once
+
+#include <cuda.h>
+
+#include "sa_common.cuh"
+#include "sa_internal.h"
+
+namespace sa {
+namespace cross {
+
+constexpr int kBox = 16384;  // 128 rows x 128 bytes (64 bf16), 128B swizzle
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 3-D tiled load of one box.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]: A is [128 lanes] x bf16 pairs along the columns.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+      " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Byte offset >> 4 of K step ks (16 of 128 or 64 columns) within a K-major operand made of
+// 64-column boxes.
+__device__ __forceinline__ uint64_t kstep(int ks) {
+  return (uint64_t)((((ks >> 2) * kBox) + (ks & 3) * 32) >> 4);
+}
+
+// The keep bits of 128 rows from row0 on: rows at or past `end` and rows whose mask byte is 0
+// are dropped. The load half can run ahead of the vote; both are called by whole warps.
+struct MaskBytes {
+  uint32_t b[4];
+  __device__ __forceinline__ void load(const uint8_t* mask, long long row0, long long end,
+                                       int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long r = row0 + 32 * i + lane;
+      b[i] = r < end ? (mask ? mask[r] : 1u) : 0u;
+    }
+  }
+  __device__ __forceinline__ void vote(uint32_t (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ballot_sync(0xffffffffu, b[i] != 0u);
+  }
+};
+
+// A whole warp zeroes the rows whose bit is 0 in a tile of `boxes` 128-row boxes: a dropped
+// row meets weight 0 in a product, and 0 times what it holds must not be NaN.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, const uint32_t (&w)[4],
+                                          int lane) {
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    uint32_t gone = ~w[i];
+    while (gone) {
+      const int r = 32 * i + __ffs(gone) - 1;
+      gone &= gone - 1;
+      for (int c = lane; c < boxes * 8; c += 32)  // 16-byte pieces; the swizzle stays in the row
+        *reinterpret_cast<uint4*>(tile + (c >> 3) * kBox + r * 128 + (c & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// A tile of the schedule: its user, and its place among the user's tiles.
+struct Tile {
+  int user, index;
+};
+
+// Launch geometry, from the sizes that the host knows (lengths live on the device).
+struct CrossGeo {
+  int pg;                // heads packed into a tile
+  long long pair_tiles;  // bound on the 256-row query tiles of all users
+  long long key_tiles;   // bound on the 128-row key tiles of all users
+  int splits;            // forward: CTAs that share a query tile's keys
+};
+
+// 3-D tensor map over bf16 rows of heads [n, heads, d], rows `stride` elements apart: boxes of
+// 64 columns x box_heads x box_rows, 128B swizzle. n = 0 (nothing will be read): one row.
+bool tmap_heads(CUtensorMap* m, const void* base, long long n, int heads, int d, long long stride,
+                int box_heads, int box_rows);
+
+// A launch that may start while the grid before it in the stream drains: the kernel calls
+// griddep_wait() before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+cudaError_t launch_fwd(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s);
+
+}  // namespace cross
+}  // namespace sa
