@@ -26,8 +26,8 @@ LIB = os.path.join(PKG, "libsa_sketch.so")
 SOURCES = ["sa_host.cu", "sa_prep.cu", "sa_fwd_sm100.cu", "sa_fwd_simt.cu", "sa_bwd_simt.cu",
            "sa_gemm_sm100.cu", "sa_bwd_tc.cu",
            "sa_noalloc.cu", "sa_stca.cu", "sa_codec.cu", "sa_forward_host.cu", "sa_bwd_fused.cu",
-           "sa_stca_keys.cu", "sa_stca_keys_bwd.cu", "sa_cross.cu", "sa_cross_fwd.cu", "sa_paged.cu",
-           "sa_paged_attn.cu", "sa_attn_host.cu"]
+           "sa_stca_keys.cu", "sa_stca_keys_bwd.cu", "sa_cross.cu", "sa_cross_fwd.cu",
+           "sa_cross_bwd.cu", "sa_paged.cu", "sa_paged_attn.cu", "sa_attn_host.cu"]
 HEADERS = ["sa_common.cuh", "sa_internal.h", "sa_cross.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

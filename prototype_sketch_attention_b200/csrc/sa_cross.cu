@@ -1,6 +1,6 @@
-// Multi-head cross attention over ragged users, forward and backward: the plain kernels.
-// One warp per output row, every sum in fp32, one pass over the keys (or queries) with the
-// running maximum and sum of the softmax. Bound by the warps' shuffles.
+// Multi-head cross attention over ragged users: the schedule of tiles, the backward's row
+// statistics, workspace plans and launch sequences. The tensor-core kernels are in
+// sa_cross_fwd.cu and sa_cross_bwd.cu.
 #include <cmath>
 
 #include "sa_common.cuh"
@@ -13,14 +13,12 @@ namespace {
 using cross::kLog2e;
 
 // Block 0 lists the query tiles (pairs of 128-row tiles: pair_tokens tokens), block 1 the key
-// tiles (128 rows). Both check both offset arrays; bad offsets leave no tiles.
-__global__ void __launch_bounds__(1024) cross_schedule_kernel(const int64_t* __restrict__ qoff,
-                                                              const int64_t* __restrict__ koff,
-                                                              int R, long long n_q, long long n_kv,
-                                                              int pair_tokens, WsHeader* hdr,
-                                                              cross::Tile* __restrict__ qtiles,
-                                                              cross::Tile* __restrict__ ktiles) {
-  griddep_launch_dependents();
+// tiles (128 rows). Both check both offset arrays; bad offsets leave no tiles. 1024 threads.
+__device__ __forceinline__ void schedule_block(const int64_t* __restrict__ qoff,
+                                               const int64_t* __restrict__ koff, int R,
+                                               long long n_q, long long n_kv, int pair_tokens,
+                                               WsHeader* hdr, cross::Tile* __restrict__ qtiles,
+                                               cross::Tile* __restrict__ ktiles) {
   __shared__ int first[1025], part[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool keys = blockIdx.x == 1;
@@ -82,114 +80,61 @@ __global__ void __launch_bounds__(1024) cross_schedule_kernel(const int64_t* __r
   }
 }
 
-// the user whose rows [off[u], off[u + 1]) hold row t, or -1
-__device__ __forceinline__ int user_of_row(const int64_t* off, int R, long long t) {
-  if (t >= off[R]) return -1;
-  int lo = 0, hi = R;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
-template <int N>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int lane, float (&v)[N]) {
+// (lse2, delta = dout . out) of every query row of a user, at [head group][row][head of the group], where
+// the backward's tiles find them contiguous. A row without kept keys gets lse2 = +inf: weight 0.
+// LANES = d / 8 lanes per row and head, 16 bytes each.
+template <int LANES>
+__device__ __forceinline__ void stats_rows(const CrossArgs& a, int pg, long long first, long long step,
+                                           float2* __restrict__ stats) {
+  const long long rows = min((long long)a.qoff[a.R], a.n_q) * a.H;
+  const int lane = threadIdx.x & (LANES - 1);
+  const long long bound = (rows + 31) / 32 * 32;  // whole warps take part in the shuffles
+  for (long long i = first; i < bound; i += step) {
+    float s = 0.f;
+    if (i < rows) {
+      const uint4 x = reinterpret_cast<const uint4*>(a.dout)[i * LANES + lane];
+      const uint4 y = reinterpret_cast<const uint4*>(a.out)[i * LANES + lane];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __bfloat162float(p[lane + 32 * i]);
-}
-
-template <int N>
-__device__ __forceinline__ float dot_row(const float (&a)[N], const float (&b)[N]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// dQ of one (row, head), and delta = dout . out
-template <int N>
-__global__ void __launch_bounds__(128) cross_dq_kernel(CrossArgs a, const WsHeader* hdr, float* delta) {
-  if (read_status(&hdr->status) != 0) return;
-  constexpr int D = 32 * N;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
-  const long long t = w / a.H;
-  const int h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  if (t >= a.n_q) return;
-  const int u = user_of_row(a.qoff, a.R, t);
-  if (u < 0) return;
-  float q[N], g[N], dq[N], k[N], v[N];
-  load_row<N>((const __nv_bfloat16*)a.Q + t * a.q_stride + h * D, lane, q);
-  load_row<N>((const __nv_bfloat16*)a.dout + (t * a.H + h) * D, lane, g);
-  load_row<N>((const __nv_bfloat16*)a.out + (t * a.H + h) * D, lane, k);
-  const float dl = dot_row<N>(g, k), lse = a.lse[t * a.H + h];
-  if (lane == 0) delta[t * a.H + h] = dl;
-#pragma unroll
-  for (int i = 0; i < N; ++i) dq[i] = 0.f;
-  for (long long j = a.koff[u]; j < a.koff[u + 1]; ++j) {
-    if (a.mask && !a.mask[j]) continue;
-    load_row<N>((const __nv_bfloat16*)a.K + j * a.k_stride + hk * D, lane, k);
-    load_row<N>((const __nv_bfloat16*)a.V + j * a.v_stride + hk * D, lane, v);
-    const float p = ex2_approx((dot_row<N>(q, k) * a.scale - lse) * kLog2e);
-    const float ds = p * (dot_row<N>(g, v) - dl) * a.scale;
-#pragma unroll
-    for (int i = 0; i < N; ++i) dq[i] = fmaf(ds, k[i], dq[i]);
-  }
-  __nv_bfloat16* out = (__nv_bfloat16*)a.dQ + (t * a.H + h) * D;
-#pragma unroll
-  for (int i = 0; i < N; ++i) out[lane + 32 * i] = __float2bfloat16(dq[i]);
-}
-
-// dK and dV of one (key row, key head): over the user's query rows and the heads that share it
-template <int N>
-__global__ void __launch_bounds__(128) cross_dkv_kernel(CrossArgs a, const WsHeader* hdr,
-                                                        const float* delta) {
-  if (read_status(&hdr->status) != 0) return;
-  constexpr int D = 32 * N;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
-  const long long j = w / a.Hkv;
-  const int hk = (int)(w % a.Hkv), G = a.H / a.Hkv;
-  if (j >= a.n_kv) return;
-  const int u = user_of_row(a.koff, a.R, j);
-  if (u < 0) return;
-  float q[N], g[N], dk[N], dv[N], k[N], v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) dk[i] = dv[i] = 0.f;
-  if (!a.mask || a.mask[j]) {
-    load_row<N>((const __nv_bfloat16*)a.K + j * a.k_stride + hk * D, lane, k);
-    load_row<N>((const __nv_bfloat16*)a.V + j * a.v_stride + hk * D, lane, v);
-    for (long long t = a.qoff[u]; t < a.qoff[u + 1]; ++t) {
-      for (int h = hk * G; h < (hk + 1) * G; ++h) {
-        load_row<N>((const __nv_bfloat16*)a.Q + t * a.q_stride + h * D, lane, q);
-        load_row<N>((const __nv_bfloat16*)a.dout + (t * a.H + h) * D, lane, g);
-        const float p = ex2_approx((dot_row<N>(q, k) * a.scale - a.lse[t * a.H + h]) * kLog2e);
-        const float ds = p * (dot_row<N>(g, v) - delta[t * a.H + h]) * a.scale;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          dk[i] = fmaf(ds, q[i], dk[i]);
-          dv[i] = fmaf(p, g[i], dv[i]);
-        }
+      for (int z = 0; z < 4; ++z) {
+        s = fmaf(__uint_as_float(u[z] << 16), __uint_as_float(v[z] << 16), s);
+        s = fmaf(__uint_as_float(u[z] & 0xffff0000u), __uint_as_float(v[z] & 0xffff0000u), s);
       }
     }
-  }
-  const long long at = (j * a.Hkv + hk) * D;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    ((__nv_bfloat16*)a.dK)[at + lane + 32 * i] = __float2bfloat16(dk[i]);
-    ((__nv_bfloat16*)a.dV)[at + lane + 32 * i] = __float2bfloat16(dv[i]);
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (i < rows && lane == 0) {
+      const long long t = i / a.H;
+      const int h = (int)(i - t * a.H), hu = h / pg;
+      const float lse = a.lse[i];
+      stats[((long long)hu * a.n_q + t) * pg + (h - hu * pg)] =
+          make_float2(lse == -INFINITY ? INFINITY : lse * kLog2e, s);
+    }
   }
 }
 
-template <int N>
-cudaError_t backward_t(const CrossArgs& a, WsHeader* hdr, float* delta, cudaStream_t s) {
-  const long long nq = (a.n_q * a.H + 3) / 4, nk = (a.n_kv * a.Hkv + 3) / 4;
-  if (nq > 0) cross_dq_kernel<N><<<(unsigned)nq, 128, 0, s>>>(a, hdr, delta);
-  if (nk > 0) cross_dkv_kernel<N><<<(unsigned)nk, 128, 0, s>>>(a, hdr, delta);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(1024) cross_schedule_kernel(const int64_t* qoff, const int64_t* koff, int R,
+                                                              long long n_q, long long n_kv, int pair_tokens,
+                                                              WsHeader* hdr, cross::Tile* qtiles,
+                                                              cross::Tile* ktiles) {
+  griddep_launch_dependents();
+  schedule_block(qoff, koff, R, n_q, n_kv, pair_tokens, hdr, qtiles, ktiles);
+}
+
+// The backward's: blocks 0 and 1 the schedule, the others lse2 and delta.
+__global__ void __launch_bounds__(1024) cross_prep_kernel(CrossArgs a, int pg, WsHeader* hdr,
+                                                          cross::Tile* qtiles, cross::Tile* ktiles,
+                                                          float2* stats) {
+  griddep_launch_dependents();
+  if (blockIdx.x < 2) {
+    schedule_block(a.qoff, a.koff, a.R, a.n_q, a.n_kv, 256 / pg, hdr, qtiles, ktiles);
+    return;
+  }
+  const int lanes = a.d / 8;
+  const long long first = ((blockIdx.x - 2) * 1024LL + threadIdx.x) / lanes;
+  const long long step = (gridDim.x - 2) * (1024LL / lanes);
+  if (a.d == 64) stats_rows<8>(a, pg, first, step, stats);
+  else stats_rows<16>(a, pg, first, step, stats);
 }
 
 }  // namespace
@@ -243,44 +188,47 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
   q.hdr = take(sizeof(WsHeader));
   q.qtiles = take((size_t)g.pair_tiles * sizeof(cross::Tile));
   q.ktiles = take((size_t)g.key_tiles * sizeof(cross::Tile));
-  if (backward) {
-    q.delta = take((size_t)n_q * H * sizeof(float));
-  } else if (g.splits > 1) {
+  if (backward) q.stats = take((size_t)n_q * H * sizeof(float2));
+  if (g.splits > 1) {
     q.part_o = take((size_t)g.splits * n_q * H * d * sizeof(float));
-    q.part_lse = take((size_t)g.splits * n_q * H * sizeof(float));
+    if (!backward) q.part_lse = take((size_t)g.splits * n_q * H * sizeof(float));
   }
   q.total = o;
   if (p) *p = q;
   return q.total;
 }
 
-namespace {
-cudaError_t launch_schedule(const CrossArgs& a, const cross::CrossGeo& g, cudaStream_t s) {
+cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
   cross_schedule_kernel<<<2, 1024, 0, s>>>(
       a.qoff, a.koff, a.R, a.n_q, a.n_kv, 256 / g.pg, reinterpret_cast<WsHeader*>(ws + a.plan.hdr),
       reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
       reinterpret_cast<cross::Tile*>(ws + a.plan.ktiles));
-  return cudaGetLastError();
-}
-}  // namespace
-
-cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || g.pair_tiles == 0) return e;
   CrossArgs b = a;
   if (b.n_kv == 0) b.K = b.V = b.Q;  // nothing is read through their tensor maps
-  const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
-  const cudaError_t e = launch_schedule(a, g, s);
-  return e != cudaSuccess || g.pair_tiles == 0 ? e : cross::launch_fwd(b, g, s);
+  return cross::launch_fwd(b, g, s);
 }
 
 cudaError_t launch_cross_backward(const CrossArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  WsHeader* hdr = reinterpret_cast<WsHeader*>(ws + a.plan.hdr);
-  float* delta = reinterpret_cast<float*>(ws + a.plan.delta);
   const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
-  const cudaError_t e = launch_schedule(a, g, s);
+  long long grid = 2 + (a.n_q * a.H * (a.d / 8) + 1023) / 1024;
+  if (grid > 4LL * a.sms) grid = 4LL * a.sms;
+  cross_prep_kernel<<<(unsigned)grid, 1024, 0, s>>>(
+      a, g.pg, reinterpret_cast<WsHeader*>(ws + a.plan.hdr),
+      reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
+      reinterpret_cast<cross::Tile*>(ws + a.plan.ktiles),
+      reinterpret_cast<float2*>(ws + a.plan.stats));
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return a.d == 64 ? backward_t<2>(a, hdr, delta, s) : backward_t<4>(a, hdr, delta, s);
+  CrossArgs b = a;
+  if (b.n_kv == 0) b.K = b.V = b.Q;  // nothing is read through the empty side's tensor maps
+  if (b.n_q == 0) b.Q = b.dout = b.K;
+  if (a.n_kv == 0 && a.n_q == 0) return cudaSuccess;
+  return cross::launch_bwd(b, g, s);
 }
 
 }  // namespace sa

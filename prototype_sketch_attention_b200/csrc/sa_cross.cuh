@@ -134,6 +134,7 @@ cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t s
 }
 
 cudaError_t launch_fwd(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s);
+cudaError_t launch_bwd(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s);
 
 }  // namespace cross
 }  // namespace sa

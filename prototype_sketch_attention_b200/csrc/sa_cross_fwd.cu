@@ -492,7 +492,8 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.part_lse = reinterpret_cast<float*>(ws + a.plan.part_lse);
   p.n_q = a.n_q;
   p.budget = kDefaultWaitBudget;
-  const size_t smem = 1024 + FSmem<D>::oBars + sizeof(FBars);
+  constexpr size_t smem = 1024 + FSmem<D>::oBars + sizeof(FBars);
+  static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
