@@ -63,20 +63,31 @@ __device__ __forceinline__ uint64_t kstep(int ks) {
 }
 
 // The keep bits of 128 rows from row0 on: rows at or past `end` and rows whose mask byte is 0
-// are dropped. The load half can run ahead of the vote; both are called by whole warps.
+// are dropped. The load can run ahead of the vote; both are called by whole warps. Without
+// a mask only a range's last tile needs a vote.
 struct MaskBytes {
   uint32_t b[4];
-  __device__ __forceinline__ void load(const uint8_t* mask, long long row0, long long end,
-                                       int lane) {
+  __device__ __forceinline__ void load(const uint8_t* mask, int row0, int end, int lane) {
+    if (mask) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long r = row0 + 32 * i + lane;
-      b[i] = r < end ? (mask ? mask[r] : 1u) : 0u;
+      for (int i = 0; i < 4; ++i)
+        b[i] = 32 * i + lane < end - row0 ? mask[(long long)row0 + 32 * i + lane] : 0u;
     }
   }
-  __device__ __forceinline__ void vote(uint32_t (&w)[4]) const {
+  // false: every row is kept (w unset)
+  __device__ __forceinline__ bool vote(const uint8_t* mask, int row0, int end, int lane,
+                                       uint32_t (&w)[4]) const {
+    if (mask) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __ballot_sync(0xffffffffu, b[i] != 0u);
+      for (int i = 0; i < 4; ++i) w[i] = __ballot_sync(0xffffffffu, b[i] != 0u);
+      return (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu;
+    }
+    const int n = end - row0;
+    if (n >= 128) return false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = n >= 32 * i + 32 ? ~0u : n > 32 * i ? (1u << (n - 32 * i)) - 1u : 0u;
+    return true;
   }
 };
 
@@ -84,13 +95,18 @@ struct MaskBytes {
 // row meets weight 0 in a product, and 0 times what it holds must not be NaN.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, const uint32_t (&w)[4],
                                           int lane) {
+  const int pieces = boxes * 8;  // 16-byte pieces of a row; the swizzle stays within the row
+  const int per = 32 / pieces, sub = lane / pieces, c = lane % pieces;  // rows at once
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     uint32_t gone = ~w[i];
     while (gone) {
-      const int r = 32 * i + __ffs(gone) - 1;
-      gone &= gone - 1;
-      for (int c = lane; c < boxes * 8; c += 32)  // 16-byte pieces; the swizzle stays in the row
+      int r = -1;
+      for (int x = 0; x < per; ++x) {
+        if (x == sub && gone) r = 32 * i + __ffs(gone) - 1;
+        gone &= gone - 1;
+      }
+      if (r >= 0)
         *reinterpret_cast<uint4*>(tile + (c >> 3) * kBox + r * 128 + (c & 7) * 16) =
             make_uint4(0, 0, 0, 0);
     }

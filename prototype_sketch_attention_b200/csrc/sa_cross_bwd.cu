@@ -438,11 +438,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap* tmap_q, const CUtensor
     if (n > 0) mb.load(a.mask, k0, k1, lane);
     for (int j = 0; j < n; ++j) {
       uint32_t keep[4];
-      mb.vote(keep);
-      if (j + 1 < n) mb.load(a.mask, k0 + 128LL * (j + 1), k1, lane);
+      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
+      if (j + 1 < n) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
       const int x = 2 * j;
       if (!mbar_wait_warp(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), status, a.budget)) break;
-      if ((keep[0] & keep[1] & keep[2] & keep[3]) != 0xffffffffu) {
+      if (drop) {
         zero_rows(smem + L::oRing + (x % NS) * L::kTile, L::kBoxes, keep, lane);
         fence_proxy_async_smem();
       }
@@ -471,8 +471,8 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap* tmap_q, const CUtensor
     if (n > 0) mb.load(a.mask, k0, k1, lane);
     for (int j = 0; j < n; ++j) {
       uint32_t keep[4];
-      mb.vote(keep);
-      if (j + 1 < n) mb.load(a.mask, k0 + 128LL * (j + 1), k1, lane);
+      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
+      if (j + 1 < n) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
       const uint32_t kw[2] = {w ? keep[2] : keep[0], w ? keep[3] : keep[1]};
       const uint32_t ts = tmem + lane_off + 128 * (j & 1) + 64 * w;
       if (!mbar_wait_warp(smem_u32(&bars->s_full[j & 1]), (uint32_t)((j >> 1) & 1), status, a.budget)) {
@@ -494,7 +494,6 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap* tmap_q, const CUtensor
       }
       tc_fence_after();
       uint32_t pk[32];
-      const bool all = (kw[0] & kw[1]) == 0xffffffffu;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t dp[32];
@@ -503,7 +502,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap* tmap_q, const CUtensor
 #pragma unroll
         for (int x = 0; x < 32; ++x)
           dp[x] = __float_as_uint(__uint_as_float(s[h][x]) * (__uint_as_float(dp[x]) - delta));
-        if (!all) {
+        if (drop) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (!((kw[h] >> x) & 1u)) dp[x] = 0u;

@@ -55,7 +55,8 @@ struct FSmem {
 struct FBars {
   uint64_t q_full, full[8], empty[8];
   uint64_t v_ready[8];  // by key tile mod 8: fewer V tiles than that fit in the ring
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t s_full[2], o_done[2];
+  uint64_t p_full[2][2];  // [tile][half of the keys]: the second product starts on the first half
   uint64_t merge, drain;
   uint32_t tmem_base;
 };
@@ -110,7 +111,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->v_ready[s]), 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&bars->s_full[w]), 1);
-      mbar_init(smem_u32(&bars->p_full[w]), 4);
+      mbar_init(smem_u32(&bars->p_full[w][0]), 4);
+      mbar_init(smem_u32(&bars->p_full[w][1]), 4);
       mbar_init(smem_u32(&bars->o_done[w]), 1);
     }
     mbar_init(smem_u32(&bars->merge), 4);
@@ -200,15 +202,18 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       };
       auto output = [&](int w, int j, int n) {  // O_w += P_w V_j; n: this tile's n-th key tile
         const int i = 2 * j + 1, st = i % NS;
-        ok = ok && mbar_wait(smem_u32(&bars->v_ready[j & 7]), (uint32_t)((j >> 3) & 1), status, a.budget) &&
-             mbar_wait(smem_u32(&bars->p_full[w]), (uint32_t)(n & 1), status, a.budget);
-        if (!ok) return;
-        tc_fence_after();
+        ok = ok && mbar_wait(smem_u32(&bars->v_ready[j & 7]), (uint32_t)((j >> 3) & 1), status, a.budget);
         const uint64_t dv = smem_desc(sbase + L::oKV + st * L::kTile, kBox, 1024, kSwizzle128B);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_f16_ts(tmem + col_o(w), tmem + col_s(w) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), id_o,
-                        (n > 0 || ks > 0) ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && mbar_wait(smem_u32(&bars->p_full[w][h]), (uint32_t)(n & 1), status, a.budget);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+            tc_mma_f16_ts(tmem + col_o(w), tmem + col_s(w) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4),
+                          id_o, (n > 0 || ks > 0) ? 1u : 0u);
+        }
         tc_commit(smem_u32(&bars->o_done[w]));
         if (!two || w == 1) tc_commit(smem_u32(&bars->empty[st]));
       };
@@ -239,10 +244,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int j = 0; j < nkt; ++j) {
       const int i = 2 * j + 1, st = i % NS;
       uint32_t keep[4];
-      mb.vote(keep);
-      if (j + 1 < nkt) mb.load(a.mask, k0 + 128LL * (j + 1), k1, lane);
+      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
+      if (j + 1 < nkt) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
       if (!mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget)) break;
-      if ((keep[0] & keep[1] & keep[2] & keep[3]) != 0xffffffffu) {
+      if (drop) {
         zero_rows(smem + L::oKV + st * L::kTile, L::kBoxes, keep, lane);
         fence_proxy_async_smem();
       }
@@ -265,11 +270,11 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     bool ok = true;
     int n = 0;
     MaskBytes mb;
-    if (first < nkt) mb.load(a.mask, k0 + 128LL * first, k1, lane);
+    if (first < nkt) mb.load(a.mask, k0 + 128 * first, k1, lane);
     for (int j = first; j < nkt; j += step, ++n) {
       uint32_t keep[4];
-      mb.vote(keep);
-      if (j + step < nkt) mb.load(a.mask, k0 + 128LL * (j + step), k1, lane);
+      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
+      if (j + step < nkt) mb.load(a.mask, k0 + 128 * (j + step), k1, lane);
       if (!mbar_wait_warp(smem_u32(&bars->s_full[w]), (uint32_t)(n & 1), status, a.budget)) {
         ok = false;
         break;
@@ -277,17 +282,22 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       tc_fence_after();
       uint32_t s[4][32];
       load_scores(st, s);
-      if ((keep[0] & keep[1] & keep[2] & keep[3]) != 0xffffffffu) {
+      if (drop) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (!((keep[i] >> x) & 1u)) s[i][x] = 0xff800000u;  // -inf
       }
-      float mt = fmaxf(__uint_as_float(s[0][0]), __uint_as_float(s[0][1]));
+      float mx[4];  // four chains: the maximum is on the way to everything else
 #pragma unroll
-      for (int x = 2; x < 128; x += 2)
-        mt = fmax3(mt, __uint_as_float(s[x >> 5][x & 31]), __uint_as_float(s[x >> 5][(x & 31) + 1]));
+      for (int i = 0; i < 4; ++i) {
+        mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+#pragma unroll
+        for (int x = 2; x < 32; x += 2)
+          mx[i] = fmax3(mx[i], __uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1]));
+      }
+      const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
       const bool raise = (mt - m) * c > kRaise;  // false for -inf - -inf
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? ex2_approx((m - mt) * c) : 1.f;  // 0 for the first maximum
@@ -324,12 +334,12 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           pk[x] = cvt_bf16x2(p0, p1);
         }
         tmem_st32(st + 32 * h, pk);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w][h]));
       }
       l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w]));
     }
     // ---- this tile's (or half's) accumulator is complete
     if (ok && n > 0)
