@@ -1,99 +1,895 @@
-// Attention of one new token per request over the paged cache: the plain kernel. One warp
-// per (request, head), one pass over the positions with the softmax's running maximum and sum.
-#include <cuda_fp8.h>
-
+// Attention of one new token per request over the paged key-value cache (sm_100a).
+//
+// Bound by reading the cache once: 4 H operations a cached value pair against 2 or 4 bytes, so
+// the products stay on mma.sync, whose operands come straight from the copied pages (16 query heads
+// at most share a key head's rows; tcgen05 would pad them to 128). Keys are the rows of the products:
+//   S^T [keys x heads] = K Q^T,   P = 2^(c S^T - m),   O^T [d x heads] += V^T P^T,   c = scale log2 e,
+// so that 8 heads fill one n-tile, the running maximum and sum of a head stay in one lane column
+// of S^T and O^T alike, and P^T becomes the next operand by an 8 x 8 transpose in registers.
+//
+// Work. A (request, key head, up to 16 of its query heads) is an item; its positions from the
+// window on are cut into tiles of T keys (16 KB of K and V). All items' tiles in order are split
+// evenly over the CTAs (one per SM) and within a CTA over its warps, each of which runs on its
+// own: it copies its pages by TMA into a ring of two tiles and keeps the softmax state of its
+// current item in registers. An item that one warp sees whole is written at once. Else the warps'
+// parts are put together in the CTA, in order, and what spans CTAs by paged_join_kernel, in
+// order: the result does not depend on timing. The 12 to 16 tiles in flight on an SM, 144 to
+// 224 KB, are more than the 45 KB that the memory's latency times its rate needs.
+//
+// FP8 codes go to bf16 exactly: exponent and mantissa moved to bf16's fields, times 2^120; a
+// row's scale multiplies its scores, and its weights, in fp32.
 #include <cmath>
 
-#include "sa_common.cuh"
-#include "sa_internal.h"
+#include "sa_cross.cuh"
 
 namespace sa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+using cross::kLn2;
+using cross::kLog2e;
+constexpr float kRaise = 8.f;  // raise the running maximum only when passed by this (log2 units)
+constexpr int kMaxWarps = 8;
+
+template <int D, bool FP8>
+struct Geo {
+  static constexpr int T = FP8 || D == 64 ? 64 : 32;      // keys per tile
+  static constexpr int kRow = FP8 ? D : 128;              // bytes of a shared-memory row
+  static constexpr int kHalves = FP8 ? 1 : D / 64;        // a bf16 row of 128 is two 128-byte halves
+  static constexpr int kMat = T * D * (FP8 ? 1 : 2);      // bytes of K or of V
+  static constexpr int kSlot = 2 * kMat + (FP8 ? 1024 : 0);  // and the scales (1024-aligned slots)
+  static constexpr int kWarps = !FP8 ? 7 : D == 128 ? 6 : 8;  // as many as fit with two slots each
+  static constexpr int oBars = kWarps * 2 * kSlot;
+  static constexpr size_t kSmem = 1024 + oBars + kWarps * 2 * 8;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 block of 16-bit values
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// E4M3 to bf16, exactly, for the low (bytes 0 and 2) and high (1 and 3) bytes of a word:
+// s eeee mmm moved to s 0000eeee mmm0000 is 2^-120 times the value, subnormal codes included.
+__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7B807B80u));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) {
+  return times_2_120(((w << 8) & 0x80008000u) | ((w << 4) & 0x07F007F0u));
+}
+__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) {
+  return times_2_120((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u));
+}
+
+struct PagedParams {
+  const __nv_bfloat16* Q;
+  long long q_stride;
+  int R, H, Hkv, G;
+  int subs, heads;        // items per request (key heads x chunks of heads), heads of a chunk
+  int chunks;
+  const float* k_scales;
+  const float* v_scales;
+  int n_pages, log2_page, max_pages;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  long long window;
+  float c;
+  __nv_bfloat16* out;
+  float* lse;
+  float* parts;           // partial results: [CTAs][kMaxWarps][2], then [CTAs][2]
+  int* flags;             // [CTAs] errors seen
+  int* status;
+  int ctas;
+  long long budget;
+};
+
+// Tiles of one item of request r (all items of a request have as many), and its first tile.
+__device__ __forceinline__ int request_tiles(const PagedParams& a, int len, int T, int* first_tile,
+                                             int* first) {
+  const int f = a.window > 0 && len > a.window ? (int)(len - a.window) : 0;
+  *first = f;
+  *first_tile = f / T;
+  return (len + T - 1) / T - f / T;
+}
+__device__ __forceinline__ int checked_len(const PagedParams& a, int r, int* bad) {
+  const int len = a.seq_lens[r];
+  if (len < 0 || len > ((long long)a.max_pages << a.log2_page)) {
+    *bad = SA_ERR_BAD_OFFSETS;
+    return 0;
+  }
+  return len;
+}
+
+// The tile lists of the requests, seen by one warp: lane l owns the requests [l C, (l + 1) C).
+struct Ranges {
+  long long before;  // tiles (per item) before this lane's requests
+  long long total;   // tiles of all items
+  int C;
+  __device__ void init(const PagedParams& a, int T, int lane, int* bad) {
+    C = (a.R + 31) / 32;
+    long long n = 0;
+    const int r1 = min(a.R, (lane + 1) * C);
+    for (int r = lane * C; r < r1; ++r) {
+      int ft, f;
+      n += request_tiles(a, checked_len(a, r, bad), T, &ft, &f);
+    }
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    before = incl - n;
+    total = __shfl_sync(0xffffffffu, incl, 31) * a.subs;
+  }
+  // the request whose items hold tile x (x < total), and the tiles before it; whole warp
+  __device__ int find(const PagedParams& a, int T, int lane, long long x, long long* base) const {
+    const unsigned le = __ballot_sync(0xffffffffu, before * a.subs <= x);
+    int src = 31 - __clz(le);  // the last lane that starts at or before x
+    long long b = __shfl_sync(0xffffffffu, before, src);
+    int bad = 0;
+    for (int r0 = src * C;; r0 += 32) {
+      int n = 0, ft, f;
+      if (r0 + lane < a.R) n = request_tiles(a, checked_len(a, r0 + lane, &bad), T, &ft, &f);
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, (b + incl) * a.subs > x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        *base = (b + __shfl_sync(0xffffffffu, incl - n, l)) * a.subs;
+        return r0 + l;
+      }
+      b += __shfl_sync(0xffffffffu, incl, 31);
+      if (r0 + 32 >= a.R) {  // not reached for x < total
+        *base = b * a.subs;
+        return a.R - 1;
+      }
+    }
+  }
+};
+
+// A place in the list of tiles: item (r, sub), tile t of [t0, t1).
+struct Cursor {
+  int r, sub, t, t0, t1, len, first;
+  __device__ void request(const PagedParams& a, int T) {
+    int bad;
+    len = checked_len(a, r, &bad);
+    t1 = request_tiles(a, len, T, &t0, &first);
+    t1 += t0;
+  }
+  __device__ void next(const PagedParams& a, int T) {
+    if (++t < t1) return;
+    if (++sub == a.subs) {
+      sub = 0;
+      do {
+        if (++r >= a.R) return;
+        request(a, T);
+      } while (t1 == t0);
+    }
+    t = t0;
+  }
+};
+
+// A part of an item: running maximum and sum of every head, and the raw O^T fragments.
+template <int D, int NT>
+struct Part {
+  static constexpr int kO = NT * D / 16 * 128;  // floats of O^T
+  static constexpr int kStride = kO + 2 * 8 * NT;
+};
+
+template <int D, int NT>
+struct State {
+  float o[D / 16][NT][4];
+  float m[NT][2], l[NT][2];  // heads 8 nt + 2 (lane mod 4) and the next; l summed over this lane's keys
+  __device__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    }
+  }
+  __device__ void sum_l() {  // over the lanes that hold other keys of the same head
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+  }
+  __device__ void store(float* p, int lane) const {  // after sum_l
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        reinterpret_cast<float4*>(p)[(i * NT + n) * 32 + lane] =
+            make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+    if (lane < 4) {
+      float* q = p + Part<D, NT>::kO;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          q[n * 8 + 2 * lane + e] = m[n][e];
+          q[8 * NT + n * 8 + 2 * lane + e] = l[n][e];
+        }
+    }
+  }
+  __device__ void merge(const float* p, int lane) {  // both summed over lanes
+    const float* q = p + Part<D, NT>::kO;
+    float f[NT][2], g[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float pm = q[n * 8 + 2 * (lane & 3) + e], pl = q[8 * NT + n * 8 + 2 * (lane & 3) + e];
+        const float mm = fmaxf(m[n][e], pm);
+        f[n][e] = l[n][e] > 0.f ? ex2_approx(m[n][e] - mm) : 0.f;
+        g[n][e] = pl > 0.f ? ex2_approx(pm - mm) : 0.f;
+        m[n][e] = mm;
+        l[n][e] = l[n][e] * f[n][e] + pl * g[n][e];
+      }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 v = reinterpret_cast<const float4*>(p)[(i * NT + n) * 32 + lane];
+        o[i][n][0] = o[i][n][0] * f[n][0] + v.x * g[n][0];
+        o[i][n][1] = o[i][n][1] * f[n][1] + v.y * g[n][1];
+        o[i][n][2] = o[i][n][2] * f[n][0] + v.z * g[n][0];
+        o[i][n][3] = o[i][n][3] * f[n][1] + v.w * g[n][1];
+      }
+  }
+};
+
+// out and lse of an item from its finished state (l summed over lanes).
+template <int D, bool FP8, int NT>
+__device__ __forceinline__ void write_item(const PagedParams& a, const State<D, NT>& st, int r, int sub,
+                                           int lane) {
+  const int hk = sub / a.chunks, h0 = hk * a.G + (sub % a.chunks) * a.heads;
+  const int nh = min(a.heads, (hk + 1) * a.G - h0);
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float i0 = st.l[n][0] > 0.f ? 1.f / st.l[n][0] : 0.f;
+    const float i1 = st.l[n][1] > 0.f ? 1.f / st.l[n][1] : 0.f;
+    __nv_bfloat16* row = a.out + ((long long)r * a.H + h0 + 8 * n + g) * D;
+    const bool w = 8 * n + g < nh;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      // (d, heads) to (head g, d pairs)
+      const uint32_t lo = transpose8(cvt_bf16x2(st.o[i][n][0] * i0, st.o[i][n][1] * i1));
+      const uint32_t hi = transpose8(cvt_bf16x2(st.o[i][n][2] * i0, st.o[i][n][3] * i1));
+      if (w) {
+        if (FP8) {  // fragment rows 0-7 are d = 0, 2, .., 14 and rows 8-15 are d = 1, 3, .., 15
+          *reinterpret_cast<uint2*>(row + 16 * i + 4 * t) =
+              make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+        } else {
+          *reinterpret_cast<uint32_t*>(row + 16 * i + 2 * t) = lo;
+          *reinterpret_cast<uint32_t*>(row + 16 * i + 8 + 2 * t) = hi;
+        }
+      }
+    }
+    if (a.lse && g == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (8 * n + 2 * t + e < nh)
+          a.lse[(long long)r * a.H + h0 + 8 * n + 2 * t + e] =
+              st.l[n][e] > 0.f ? (st.m[n][e] + lg2_approx(st.l[n][e])) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+// Where a warp's (or CTA's) parts go: at most one that starts inside an item (its first) and one
+// that ends inside an item it saw the start of (its last).
+enum : int { kNone = 0, kOpen = 1, kEnds = 2 };  // kEnds: reaches the item's end
+
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(Geo<D, FP8>::kWarps * 32, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                  const __grid_constant__ PagedParams a) {
+  using L = Geo<D, FP8>;
+  constexpr int T = L::T, MT = T / 16, KS = D / 16, kWarps = L::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ int head_kind[kWarps], tail_kind[kWarps], errors;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+  griddep_launch_dependents();  // the join reads its inputs only after this grid has ended
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::oBars) + 2 * warp;
+  const uint32_t slot0 = smem_u32(smem) + warp * 2 * L::kSlot;
+  if (threadIdx.x == 0) errors = 0;
+  if (lane == 0) {
+    mbar_init(smem_u32(&bars[0]), 1);
+    mbar_init(smem_u32(&bars[1]), 1);
+    fence_mbar_init();
+    head_kind[warp] = tail_kind[warp] = kNone;
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  __syncthreads();
+  int bad = 0;
+
+  Ranges rg;
+  rg.init(a, T, lane, &bad);
+  const long long W = rg.total;
+  const long long ca = W * blockIdx.x / a.ctas, cb = W * (blockIdx.x + 1) / a.ctas;
+  const long long xa = ca + (cb - ca) * warp / kWarps, xb = ca + (cb - ca) * (warp + 1) / kWarps;
+  float* parts = a.parts + ((long long)blockIdx.x * kMaxWarps + warp) * 2 * Part<D, NT>::kStride;
+  int last_r = 0, last_sub = 0;
+  bool dead = false;
+  if (xa < xb) {
+    long long base;
+    Cursor cur;
+    cur.r = rg.find(a, T, lane, xa, &base);
+    cur.request(a, T);
+    const int nt = cur.t1 - cur.t0;
+    cur.sub = (int)((xa - base) / nt);
+    cur.t = cur.t0 + (int)((xa - base) % nt);
+    Cursor ahead = cur;
+
+    // copies of one tile: lane -> (page, K or V, half); scales by the first lanes
+    const int ps = 1 << a.log2_page, box = min(ps, T), np = T / box;
+    const int kinds = 2 * L::kHalves;
+    auto copy = [&](int slot) {
+      const int hk = ahead.sub / a.chunks;
+      const int p0 = ahead.t * T, pos = p0 + (lane / kinds) * box;  // this lane's first position
+      const bool mine = lane < np * kinds && pos < ahead.len && pos + box > ahead.first;
+      int page = -1;
+      if (mine) {
+        page = a.table[(long long)ahead.r * a.max_pages + (pos >> a.log2_page)];
+        if (page < 0 || page >= a.n_pages) {
+          bad = SA_ERR_BAD_PAGES;
+          page = -1;
+        }
+      }
+      const int copies = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      const uint32_t bar = smem_u32(&bars[slot]);
+      const uint32_t dst = slot0 + slot * L::kSlot;
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar, copies * box * L::kRow + (FP8 ? copies * box * 4 : 0));
+      __syncwarp();
+      if (page >= 0) {
+        const int kind = lane % kinds, v = kind / L::kHalves, half = kind % L::kHalves;
+        const int row = ((page * a.Hkv + hk) << a.log2_page) + (pos & (ps - 1));
+        const uint32_t to = dst + v * L::kMat + half * T * 128 + (pos - p0) * L::kRow;
+        tma_load_2d(to, v ? &tmap_v : &tmap_k, half * 64, row, bar);
+        if (FP8)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+              ::"r"(dst + 2 * L::kMat + v * T * 4 + (pos - p0) * 4),
+                "l"((v ? a.v_scales : a.k_scales) + row), "r"(box * 4), "r"(bar)
+              : "memory");
+      }
+      ahead.next(a, T);
+    };
+    const int n_tiles = (int)(xb - xa);
+    copy(0);
+    if (n_tiles > 1) copy(1);
+
+    State<D, NT> st;
+    uint32_t qf[KS][NT][2];
+    bool fresh = true, from_start = false;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int slot = i & 1;
+      if (fresh) {  // a new item: its queries as the products' right operand
+        st.clear();
+        from_start = cur.t == cur.t0;
+        const int hk = cur.sub / a.chunks, h0 = hk * a.G + (cur.sub % a.chunks) * a.heads;
+        const int nh = min(a.heads, (hk + 1) * a.G - h0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const __nv_bfloat16* qr = a.Q + cur.r * a.q_stride + (h0 + 8 * n + g) * D;
+          const bool w = 8 * n + g < nh;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            if (FP8) {
+              const uint2 v = w ? *reinterpret_cast<const uint2*>(qr + 16 * ks + 4 * q4) : make_uint2(0, 0);
+              qf[ks][n][0] = __byte_perm(v.x, v.y, 0x5410);  // even and odd values apart, as the
+              qf[ks][n][1] = __byte_perm(v.x, v.y, 0x7632);  // codes of a word are taken
+            } else {
+              qf[ks][n][0] = w ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * q4) : 0u;
+              qf[ks][n][1] = w ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * q4) : 0u;
+            }
+          }
+        }
+        fresh = false;
+      }
+      if (!mbar_wait_warp(smem_u32(&bars[slot]), (uint32_t)((i >> 1) & 1), &errors, a.budget)) {
+        dead = true;
+        break;
+      }
+      const uint32_t kb = slot0 + slot * L::kSlot, vb = kb + L::kMat;
+      const float* ksc = reinterpret_cast<const float*>(smem + (kb - smem_u32(smem)) + 2 * L::kMat);
+      const int p0 = cur.t * T;
+      const bool edge = p0 < cur.first || p0 + T > cur.len;
+      if (edge) {  // weight 0 meets these rows of V: they must not hold NaN
+        uint8_t* vs = smem + (vb - smem_u32(smem));
+        for (int x = lane; x < T * (L::kRow / 16) * L::kHalves; x += 32) {
+          const int y = x % (L::kRow / 16), z = x / (L::kRow / 16), half = z / T, p = p0 + z % T;
+          if (p < cur.first || p >= cur.len)
+            *reinterpret_cast<uint4*>(vs + half * T * 128 + (z % T) * L::kRow + y * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      // ---- S^T = K Q^T
+      float s[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+        const int row = mt * 16 + (lane & 15);
+        if (FP8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += 2) {  // a 16-byte piece is 16 values: two steps a load
+            const int ch = ks + (lane >> 4);
+            uint32_t w[4];
+            ldsm4(kb + row * L::kRow + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // bytes 4t .. 4t + 3 of a piece: k = 2t, 2t + 1 take bytes 0, 2 and k = 2t + 8, 2t + 9
+              // bytes 1, 3
+              const uint32_t a0 = e4m3_even(w[2 * h]), a2 = e4m3_odd(w[2 * h]);
+              const uint32_t a1 = e4m3_even(w[2 * h + 1]), a3 = e4m3_odd(w[2 * h + 1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816(s[mt][n], a0, a1, a2, a3, qf[ks + h][n][0], qf[ks + h][n][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const int ch = 2 * ks + (lane >> 4);
+            uint32_t w[4];
+            ldsm4(kb + (ch >> 3) * T * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(s[mt][n], w[0], w[1], w[2], w[3], qf[ks][n][0], qf[ks][n][1]);
+          }
+        }
+      }
+      // ---- softmax along the keys: lane column = heads 2 q4 and 2 q4 + 1, rows g and g + 8
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const int key = mt * 16 + g + 8 * hi;
+          const float f = FP8 ? a.c * ksc[key] : a.c;
+          const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = in ? s[mt][n][2 * hi + e] * f : -INFINITY;
+              s[mt][n][2 * hi + e] = z;
+              mx[n][e] = fmaxf(mx[n][e], z);
+            }
+        }
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], x));
+          raise = raise || mx[n][e] - st.m[n][e] > kRaise;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mm = fmaxf(st.m[n][e], mx[n][e]);
+            f[e] = st.m[n][e] > -INFINITY ? ex2_approx(st.m[n][e] - mm) : 0.f;
+            st.m[n][e] = mm;
+            st.l[n][e] *= f[e];
+          }
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            st.o[y][n][0] *= f[0];
+            st.o[y][n][1] *= f[1];
+            st.o[y][n][2] *= f[0];
+            st.o[y][n][3] *= f[1];
+          }
+        }
+      }
+      uint32_t pf[MT][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float m0 = st.m[n][0] == -INFINITY ? 0.f : st.m[n][0];
+        const float m1 = st.m[n][1] == -INFINITY ? 0.f : st.m[n][1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            float e0 = ex2_approx(s[mt][n][2 * hi] - m0), e1 = ex2_approx(s[mt][n][2 * hi + 1] - m1);
+            st.l[n][0] += e0;
+            st.l[n][1] += e1;
+            if (FP8) {
+              const int key = mt * 16 + g + 8 * hi;
+              const float vs = ksc[T + key];
+              const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
+              e0 = in ? e0 * vs : 0.f;
+              e1 = in ? e1 * vs : 0.f;
+            }
+            pf[mt][n][hi] = transpose8(cvt_bf16x2(e0, e1));
+          }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int kk = 0; kk < MT; ++kk) {
+        if (FP8) {
+          const int row = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+          for (int dm = 0; dm < KS; dm += 2) {
+            const int ch = dm + (lane >> 4);
+            uint32_t w[4];
+            ldsm4_t(vb + row * L::kRow + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = e4m3_even(w[2 * h]), a1 = e4m3_odd(w[2 * h]);
+              const uint32_t a2 = e4m3_even(w[2 * h + 1]), a3 = e4m3_odd(w[2 * h + 1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816(st.o[dm + h][n], a0, a1, a2, a3, pf[kk][n][0], pf[kk][n][1]);
+            }
+          }
+        } else {
+          const int row = kk * 16 + (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+          for (int dm = 0; dm < KS; ++dm) {
+            const int ch = 2 * dm + ((lane >> 3) & 1);
+            uint32_t w[4];
+            ldsm4_t(vb + (ch >> 3) * T * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4), w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(st.o[dm][n], w[0], w[1], w[2], w[3], pf[kk][n][0], pf[kk][n][1]);
+          }
+        }
+      }
+      if (edge) fence_proxy_async_smem();  // the zeros, before the next copy into this slot
+      __syncwarp();
+      if (i + 2 < n_tiles) copy(slot);
+      // ---- the end of the item, or of this warp's tiles
+      const bool ends = cur.t + 1 == cur.t1;
+      if (ends || i + 1 == n_tiles) {
+        st.sum_l();
+        if (ends && from_start) {
+          write_item<D, FP8, NT>(a, st, cur.r, cur.sub, lane);
+        } else if (!from_start) {
+          st.store(parts, lane);
+          if (lane == 0) head_kind[warp] = ends ? kEnds : kOpen;
+        } else {
+          st.store(parts + Part<D, NT>::kStride, lane);
+          if (lane == 0) tail_kind[warp] = kOpen;
+          last_r = cur.r;
+          last_sub = cur.sub;
+        }
+        fresh = true;
+      }
+      cur.next(a, T);
+    }
+    if (dead) {  // let the copies in flight land before the block leaves
+      for (int x = 0; x < 2; ++x)
+        for (int ph = 0; ph < 2; ++ph) mbar_wait_drain(smem_u32(&bars[x]), (uint32_t)ph, 2000000LL);
+    }
+  }
+  const int any_bad = __reduce_max_sync(0xffffffffu, (unsigned)bad);
+  if (lane == 0 && any_bad) atomicMax(&errors, any_bad);
+  __syncthreads();  // the warps' parts are written
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = errors;
+
+  // ---- parts that belong together, in order: a warp whose last item goes on in later warps
+  // (or the first warp with tiles, when the CTA starts inside an item) adds them to its own
+  int lead = -1;  // 0: this warp's first part leads (the CTA's first), 1: its last part does
+  if (tail_kind[warp] != kNone) lead = 1;
+  if (head_kind[warp] != kNone) {
+    int w = 0;
+    while (w < warp && ca + (cb - ca) * w / kWarps == ca + (cb - ca) * (w + 1) / kWarps) ++w;
+    if (w == warp) {  // (a warp may lead twice: its first part may end, and its last start, an item)
+      State<D, NT> st;
+      st.clear();
+      st.merge(parts, lane);
+      bool end = head_kind[warp] == kEnds;
+      for (int x = warp + 1; x < kWarps && !end; ++x)
+        if (head_kind[x] != kNone) {
+          st.merge(parts + (x - warp) * 2 * Part<D, NT>::kStride, lane);
+          end = head_kind[x] == kEnds;
+        }
+      // the CTA started inside this item: its part 0
+      st.store(a.parts + ((long long)a.ctas * kMaxWarps * 2 + blockIdx.x * 2) * Part<D, NT>::kStride, lane);
+    }
+  }
+  if (lead == 1) {
+    State<D, NT> st;
+    st.clear();
+    st.merge(parts + Part<D, NT>::kStride, lane);
+    bool end = false;
+    for (int x = warp + 1; x < kWarps && !end; ++x)
+      if (head_kind[x] != kNone) {
+        st.merge(parts + (x - warp) * 2 * Part<D, NT>::kStride, lane);
+        end = head_kind[x] == kEnds;
+      }
+    if (end) write_item<D, FP8, NT>(a, st, last_r, last_sub, lane);
+    else  // goes on in the next CTA: this CTA's part 1
+      st.store(a.parts + ((long long)a.ctas * kMaxWarps * 2 + blockIdx.x * 2 + 1) * Part<D, NT>::kStride, lane);
+  }
+}
+
+// Items that span CTAs: the CTAs' parts in order. One block per item; its four groups of threads
+// take every fourth part each and are then put together. Also: items without positions, and the
+// device status.
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(512)
+paged_join_kernel(const __grid_constant__ PagedParams a) {
+  constexpr int T = Geo<D, FP8>::T, kV = NT * D / 16 * 32;  // float4 of a part
+  constexpr int kGroups = 512 / 128, kPer = kV / 128;
+  __shared__ float wgt[kGroups][8 * NT][2];
+  __shared__ long long bounds[2];
+  __shared__ float red_l[kGroups][8 * NT], red_m[kGroups][8 * NT];
+  __shared__ float4 acc_s[kGroups][kV];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long item = blockIdx.x;
+  const int r = (int)(item / a.subs), sub = (int)(item % a.subs);
+  __shared__ long long Wt;
+  __shared__ int bad_s;
+  if (tid == 0) bad_s = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int bad = 0;
+    Ranges rg;
+    rg.init(a, T, lane, &bad);
+    // tiles before request r: the owning lane's, plus those of the requests between
+    const int src = rg.C ? r / rg.C : 0;
+    long long b = __shfl_sync(0xffffffffu, rg.before, src);
+    long long part = 0;
+    int ft, f, dummy = 0, mine = 0;
+    if (r < a.R) {
+      for (int x = src * rg.C + lane; x < r; x += 32)
+        part += request_tiles(a, checked_len(a, x, &dummy), T, &ft, &f);
+      mine = request_tiles(a, checked_len(a, r, &dummy), T, &ft, &f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) {
+      bounds[0] = (b + part) * a.subs + (long long)sub * mine;
+      bounds[1] = bounds[0] + mine;
+      Wt = rg.total;
+    }
+    if (blockIdx.x == 0) {
+      const int any = __reduce_max_sync(0xffffffffu, (unsigned)bad);
+      if (lane == 0) bad_s = any;
+    }
+  }
+  griddep_wait();
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    int bad = 0;
+    for (int x = tid; x < a.ctas; x += 512) bad = max(bad, a.flags[x]);
+    if (bad) atomicMax(&bad_s, bad);
+    __syncthreads();
+    if (tid == 0) *a.status = bad_s;
+  }
+  if (r >= a.R) return;
+  const long long T0 = bounds[0], T1 = bounds[1], W = Wt;
+  const int hk = sub / a.chunks, h0 = hk * a.G + (sub % a.chunks) * a.heads;
+  const int nh = min(a.heads, (hk + 1) * a.G - h0);
+  if (T0 == T1) {  // no positions
+    for (int x = tid; x < nh * D; x += 512) a.out[((long long)r * a.H + h0) * D + x] = __float2bfloat16(0.f);
+    if (a.lse && tid < nh) a.lse[(long long)r * a.H + h0 + tid] = -INFINITY;
+    return;
+  }
+  // the CTAs that hold tiles T0 and T1 - 1: CTA b has [W b / ctas, W (b + 1) / ctas)
+  auto owner = [&](long long x) {
+    int b = (int)(x * a.ctas / W);
+    while (b + 1 < a.ctas && W * (b + 1) / a.ctas <= x) ++b;
+    while (b > 0 && W * b / a.ctas > x) --b;
+    return b;
+  };
+  const int b0 = owner(T0), b1 = owner(T1 - 1);
+  if (b0 == b1) return;  // written by its CTA
+  auto part_of = [&](int b) -> const float* {  // null: a CTA without tiles
+    const long long ca = W * b / a.ctas, cb = W * (b + 1) / a.ctas;
+    if (ca == cb) return nullptr;
+    return a.parts + ((long long)a.ctas * kMaxWarps * 2 + b * 2 + (ca > T0 ? 0 : 1)) * Part<D, NT>::kStride;
+  };
+  const int grp = tid >> 7, t = tid & 127;
+  // every group's own maximum and sum first
+  float m = -INFINITY, l = 0.f;
+  const int h = t;  // head, for t < 8 NT
+  if (t < 8 * NT) {
+    for (int b = b0 + grp; b <= b1; b += kGroups) {
+      const float* p = part_of(b);
+      if (!p) continue;
+      const float pm = p[Part<D, NT>::kO + h], pl = p[Part<D, NT>::kO + 8 * NT + h];
+      if (!(pl > 0.f)) continue;
+      const float mm = fmaxf(m, pm);
+      l = l * (m > -INFINITY ? ex2_approx(m - mm) : 0.f) + pl * ex2_approx(pm - mm);
+      m = mm;
+    }
+    red_m[grp][h] = m;
+    red_l[grp][h] = l;
+  }
+  __syncthreads();
+  float mt = -INFINITY;
+  if (t < 8 * NT) {
+    for (int x = 0; x < kGroups; ++x) mt = fmaxf(mt, red_m[x][h]);
+    wgt[grp][h][0] = mt;  // the item's maximum
+  }
+  __syncthreads();
+  float4 acc[kPer];
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // thread t holds float4 t + 128 y of the raw fragments: n-tile (i / 32) mod NT, heads 2 (lane mod 4) + e
+#pragma unroll 4
+  for (int b = b0 + grp; b <= b1; b += kGroups) {
+    const float* p = part_of(b);
+    if (!p) continue;
+#pragma unroll
+    for (int y = 0; y < kPer; ++y) {
+      const int i = t + 128 * y, hh = ((i >> 5) % NT) * 8 + 2 * (i & 3);
+      const float4 v = reinterpret_cast<const float4*>(p)[i];
+      const float* ml = p + Part<D, NT>::kO;
+      const float w0 = ml[8 * NT + hh] > 0.f ? ex2_approx(ml[hh] - wgt[grp][hh][0]) : 0.f;
+      const float w1 = ml[8 * NT + hh + 1] > 0.f ? ex2_approx(ml[hh + 1] - wgt[grp][hh + 1][0]) : 0.f;
+      acc[y].x = fmaf(v.x, w0, acc[y].x);
+      acc[y].y = fmaf(v.y, w1, acc[y].y);
+      acc[y].z = fmaf(v.z, w0, acc[y].z);
+      acc[y].w = fmaf(v.w, w1, acc[y].w);
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kPer; ++y) acc_s[grp][t + 128 * y] = acc[y];
+  __syncthreads();
+  if (tid < 32) {  // one warp writes the item, as the main kernel's warps do
+    State<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hh = n * 8 + 2 * (lane & 3) + e;
+        float ls = 0.f;
+        const float mm = wgt[0][hh][0];
+        for (int x = 0; x < kGroups; ++x)
+          if (red_l[x][hh] > 0.f) ls += red_l[x][hh] * ex2_approx(red_m[x][hh] - mm);
+        st.m[n][e] = mm;
+        st.l[n][e] = ls;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        float4 v = acc_s[0][(i * NT + n) * 32 + lane];
+        for (int x = 1; x < kGroups; ++x) {
+          const float4 u = acc_s[x][(i * NT + n) * 32 + lane];
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        st.o[i][n][0] = v.x;
+        st.o[i][n][1] = v.y;
+        st.o[i][n][2] = v.z;
+        st.o[i][n][3] = v.w;
+      }
+    }
+    write_item<D, FP8, NT>(a, st, r, sub, lane);
+  }
+}
+
+// 2-D tensor map over the cache's rows, boxes of one row width x box_rows.
+bool tmap_cache(CUtensorMap* m, const void* base, uint64_t rows, int d, bool fp8, int box_rows) {
+  auto fn = tmap_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * (fp8 ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(fp8 ? d : 64), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            fp8 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool FP8, int NT>
+cudaError_t launch_t(const PagedAttnArgs& a, PagedParams& p, cudaStream_t s) {
+  using L = Geo<D, FP8>;
+  const int ps = 1 << a.log2_page, box = ps < L::T ? ps : L::T;
+  CUtensorMap tk, tv;
+  const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * ps;
+  if (!tmap_cache(&tk, rows ? a.k_cache : a.Q, rows ? rows : 1, D, FP8, box) ||
+      !tmap_cache(&tv, rows ? a.v_cache : a.Q, rows ? rows : 1, D, FP8, box))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, FP8, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_attn_kernel<D, FP8, NT><<<p.ctas, L::kWarps * 32, L::kSmem, s>>>(tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return cross::launch_dependent(paged_join_kernel<D, FP8, NT>, dim3((unsigned)((long long)a.R * p.subs)),
+                                 dim3(512), 0, s, p);
+}
 
 __global__ void paged_clear_kernel(WsHeader* hdr) { hdr->status = 0; }
-
-template <int N, bool FP8>
-__device__ __forceinline__ void cache_row(const void* cache, const float* scales, long long row,
-                                          int lane, float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const long long at = row * (32 * N) + lane + 32 * i;
-    if (FP8) v[i] = float(static_cast<const __nv_fp8_e4m3*>(cache)[at]) * scales[row];
-    else v[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(cache)[at]);
-  }
-}
-
-template <int N, bool FP8>
-__global__ void __launch_bounds__(128) paged_attn_kernel(PagedAttnArgs a, WsHeader* hdr) {
-  constexpr int D = 32 * N;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4LL + (threadIdx.x >> 5);
-  const int r = (int)(w / a.H), h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  if (r >= a.R) return;
-  long long len = a.seq_lens[r];
-  if (len < 0 || len > ((long long)a.max_pages << a.log2_page)) {
-    latch_status(&hdr->status, SA_ERR_BAD_OFFSETS);
-    len = 0;
-  }
-  float q[N], o[N], k[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = __bfloat162float(((const __nv_bfloat16*)a.Q)[r * a.q_stride + h * D + lane + 32 * i]);
-    o[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (long long p = a.window > 0 && len > a.window ? len - a.window : 0; p < len; ++p) {
-    const long long pg = a.table[(long long)r * a.max_pages + (p >> a.log2_page)];
-    if (pg < 0 || pg >= a.n_pages) {
-      latch_status(&hdr->status, SA_ERR_BAD_PAGES);
-      continue;
-    }
-    const long long row = ((pg * a.Hkv + hk) << a.log2_page) + (p & ((1 << a.log2_page) - 1));
-    cache_row<N, FP8>(a.k_cache, a.k_scales, row, lane, k);
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) z = fmaf(q[i], k[i], z);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-    z *= a.scale * kLog2e;
-    const float mn = fmaxf(m, z), f = ex2_approx(m - mn), e = ex2_approx(z - mn);
-    cache_row<N, FP8>(a.v_cache, a.v_scales, row, lane, k);
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * f + e * k[i];
-    l = l * f + e;
-    m = mn;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    ((__nv_bfloat16*)a.out)[((long long)r * a.H + h) * D + lane + 32 * i] = __float2bfloat16(o[i] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[(long long)r * a.H + h] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
-}
 
 }  // namespace
 
 size_t paged_attn_plan(int R, int H, int Hkv, int d, int sms, PagedAttnPlan* p) {
   PagedAttnPlan q;
-  q.total = sizeof(WsHeader);
+  const int nt = H / Hkv > 8 ? 2 : 1;
+  q.flags = sizeof(WsHeader);
+  q.parts = (q.flags + (size_t)sms * 4 + 255) / 256 * 256;
+  const size_t part = ((size_t)nt * d / 16 * 128 + 16 * nt) * sizeof(float);
+  q.total = q.parts + (size_t)sms * (2 * kMaxWarps + 2) * part;
   if (p) *p = q;
   return q.total;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   WsHeader* hdr = static_cast<WsHeader*>(a.workspace);
-  paged_clear_kernel<<<1, 1, 0, s>>>(hdr);
-  const long long n = ((long long)a.R * a.H + 3) / 4;
-  if (n > 0) {
-    if (a.d == 64 && a.fp8) paged_attn_kernel<2, true><<<(unsigned)n, 128, 0, s>>>(a, hdr);
-    else if (a.d == 64) paged_attn_kernel<2, false><<<(unsigned)n, 128, 0, s>>>(a, hdr);
-    else if (a.fp8) paged_attn_kernel<4, true><<<(unsigned)n, 128, 0, s>>>(a, hdr);
-    else paged_attn_kernel<4, false><<<(unsigned)n, 128, 0, s>>>(a, hdr);
+  if (a.R == 0) {
+    paged_clear_kernel<<<1, 1, 0, s>>>(hdr);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  const int G = a.H / a.Hkv, nt = G > 8 ? 2 : 1;
+  PagedParams p = {};
+  p.Q = static_cast<const __nv_bfloat16*>(a.Q);
+  p.q_stride = a.q_stride;
+  p.R = a.R;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.G = G;
+  p.heads = 8 * nt;
+  p.chunks = (G + p.heads - 1) / p.heads;
+  p.subs = a.Hkv * p.chunks;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.n_pages = (int)a.n_pages;
+  p.log2_page = a.log2_page;
+  p.max_pages = a.max_pages;
+  p.table = a.table;
+  p.seq_lens = a.seq_lens;
+  p.window = a.window;
+  p.c = a.scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.flags = reinterpret_cast<int*>(ws + a.plan.flags);
+  p.parts = reinterpret_cast<float*>(ws + a.plan.parts);
+  p.status = &hdr->status;
+  p.ctas = a.sms;
+  p.budget = kDefaultWaitBudget;
+  if (a.d == 64) {
+    if (a.fp8) return nt == 1 ? launch_t<64, true, 1>(a, p, s) : launch_t<64, true, 2>(a, p, s);
+    return nt == 1 ? launch_t<64, false, 1>(a, p, s) : launch_t<64, false, 2>(a, p, s);
+  }
+  if (a.fp8) return nt == 1 ? launch_t<128, true, 1>(a, p, s) : launch_t<128, true, 2>(a, p, s);
+  return nt == 1 ? launch_t<128, false, 1>(a, p, s) : launch_t<128, false, 2>(a, p, s);
 }
 
 }  // namespace sa
