@@ -367,7 +367,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
 
 // ---- attention over the paged cache (sa_paged_attn.cu)
 struct PagedAttnPlan {
-  size_t flags = 0, parts = 0, total = 0;
+  size_t info = 0, parts = 0, total = 0;
 };
 size_t paged_attn_plan(int R, int H, int Hkv, int d, int sms, PagedAttnPlan* p);
 struct PagedAttnArgs {

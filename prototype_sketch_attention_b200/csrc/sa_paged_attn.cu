@@ -79,6 +79,13 @@ __device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) {
   return times_2_120((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u));
 }
 
+// What a CTA leaves for the join: errors seen, and the item (request, sub) that it saw the start
+// of and that goes on in later CTAs, up to tile `end` of the `total` tiles.
+struct CtaInfo {
+  long long end, total;
+  int error, open, r, sub;
+};
+
 struct PagedParams {
   const __nv_bfloat16* Q;
   long long q_stride;
@@ -95,7 +102,7 @@ struct PagedParams {
   __nv_bfloat16* out;
   float* lse;
   float* parts;           // partial results: [CTAs][kMaxWarps][2], then [CTAs][2]
-  int* flags;             // [CTAs] errors seen
+  CtaInfo* info;          // [CTAs]
   int* status;
   int ctas;
   long long budget;
@@ -340,6 +347,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   const long long xa = ca + (cb - ca) * warp / kWarps, xb = ca + (cb - ca) * (warp + 1) / kWarps;
   float* parts = a.parts + ((long long)blockIdx.x * kMaxWarps + warp) * 2 * Part<D, NT>::kStride;
   int last_r = 0, last_sub = 0;
+  long long last_end = 0;  // the tile behind the last item
   bool dead = false;
   if (xa < xb) {
     long long base;
@@ -592,6 +600,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
           if (lane == 0) tail_kind[warp] = kOpen;
           last_r = cur.r;
           last_sub = cur.sub;
+          last_end = xb + (cur.t1 - cur.t - 1);
         }
         fresh = true;
       }
@@ -602,10 +611,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int ph = 0; ph < 2; ++ph) mbar_wait_drain(smem_u32(&bars[x]), (uint32_t)ph, 2000000LL);
     }
   }
+  // requests without positions: CTA b's are b, b + CTAs, ..., 32 a warp
+  for (int r0 = blockIdx.x + a.ctas * 32 * warp; r0 < a.R; r0 += a.ctas * 32 * kWarps) {
+    const int r = r0 + a.ctas * lane;
+    int dummy;
+    unsigned none = __ballot_sync(0xffffffffu, r < a.R && checked_len(a, r, &dummy) == 0);
+    while (none) {
+      const long long row = (long long)(r0 + a.ctas * (__ffs(none) - 1)) * a.H;
+      none &= none - 1;
+      for (int x = lane; x < a.H * D / 8; x += 32)
+        reinterpret_cast<uint4*>(a.out + row * D)[x] = make_uint4(0, 0, 0, 0);
+      for (int x = lane; a.lse && x < a.H; x += 32) a.lse[row + x] = -INFINITY;
+    }
+  }
   const int any_bad = __reduce_max_sync(0xffffffffu, (unsigned)bad);
   if (lane == 0 && any_bad) atomicMax(&errors, any_bad);
+  if (threadIdx.x == 0) a.info[blockIdx.x].open = 0;
   __syncthreads();  // the warps' parts are written
-  if (threadIdx.x == 0) a.flags[blockIdx.x] = errors;
+  if (threadIdx.x == 0) a.info[blockIdx.x].error = errors;
 
   // ---- parts that belong together, in order: a warp whose last item goes on in later warps
   // (or the first warp with tiles, when the CTA starts inside an item) adds them to its own
@@ -639,131 +662,99 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         end = head_kind[x] == kEnds;
       }
     if (end) write_item<D, FP8, NT>(a, st, last_r, last_sub, lane);
-    else  // goes on in the next CTA: this CTA's part 1
+    else {  // goes on in the next CTA: this CTA's part 1
       st.store(a.parts + ((long long)a.ctas * kMaxWarps * 2 + blockIdx.x * 2 + 1) * Part<D, NT>::kStride, lane);
+      if (lane == 0) {
+        CtaInfo& in = a.info[blockIdx.x];
+        in.end = last_end;
+        in.total = W;
+        in.r = last_r;
+        in.sub = last_sub;
+        in.open = 1;
+      }
+    }
   }
 }
 
-// Items that span CTAs: the CTAs' parts in order. One block per item; its four groups of threads
-// take every fourth part each and are then put together. Also: items without positions, and the
-// device status.
+// An item that spans CTAs: block b joins the one that starts in CTA b and goes on, from the parts
+// of CTAs b .. b1 in order (four groups of threads take every fourth part each and are then
+// put together). Block 0 also writes the device status.
 template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(512)
 paged_join_kernel(const __grid_constant__ PagedParams a) {
-  constexpr int T = Geo<D, FP8>::T, kV = NT * D / 16 * 32;  // float4 of a part
-  constexpr int kGroups = 512 / 128, kPer = kV / 128;
-  __shared__ float wgt[kGroups][8 * NT][2];
-  __shared__ long long bounds[2];
-  __shared__ float red_l[kGroups][8 * NT], red_m[kGroups][8 * NT];
+  constexpr int kV = NT * D / 16 * 32, kHeads = 8 * NT;  // float4 and heads of a part
+  constexpr int kGroups = 4, kPer = kV / 128;
+  extern __shared__ float ml[];  // [2][CTAs][kHeads]: maxima, then weights; sums (-1: no part)
+  __shared__ float tot_m[kHeads], tot_l[kHeads];
   __shared__ float4 acc_s[kGroups][kV];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long item = blockIdx.x;
-  const int r = (int)(item / a.subs), sub = (int)(item % a.subs);
-  __shared__ long long Wt;
-  __shared__ int bad_s;
-  if (tid == 0) bad_s = 0;
-  __syncthreads();
-  if (warp == 0) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = blockIdx.x;
+  griddep_wait();
+  if (b0 == 0) {
     int bad = 0;
-    Ranges rg;
-    rg.init(a, T, lane, &bad);
-    // tiles before request r: the owning lane's, plus those of the requests between
-    const int src = rg.C ? r / rg.C : 0;
-    long long b = __shfl_sync(0xffffffffu, rg.before, src);
-    long long part = 0;
-    int ft, f, dummy = 0, mine = 0;
-    if (r < a.R) {
-      for (int x = src * rg.C + lane; x < r; x += 32)
-        part += request_tiles(a, checked_len(a, x, &dummy), T, &ft, &f);
-      mine = request_tiles(a, checked_len(a, r, &dummy), T, &ft, &f);
+    for (int x = tid; x < a.ctas; x += 512) bad = max(bad, a.info[x].error);
+    bad = __syncthreads_or(bad == SA_ERR_TIMEOUT) ? SA_ERR_TIMEOUT
+          : __syncthreads_or(bad == SA_ERR_BAD_PAGES) ? SA_ERR_BAD_PAGES
+          : __syncthreads_or(bad == SA_ERR_BAD_OFFSETS) ? SA_ERR_BAD_OFFSETS : SA_OK;
+    if (tid == 0) *a.status = bad;
+  }
+  const CtaInfo in = a.info[b0];
+  if (!in.open) return;
+  const long long W = in.total;
+  int b1 = (int)((in.end - 1) * a.ctas / W);  // the CTA that holds the item's last tile
+  while (b1 + 1 < a.ctas && W * (b1 + 1) / a.ctas <= in.end - 1) ++b1;
+  while (W * b1 / a.ctas > in.end - 1) --b1;
+  const int nb = b1 - b0 + 1;
+  auto part_of = [&](int x) {  // the first CTA's last part, then the others' first parts
+    return a.parts + ((long long)a.ctas * kMaxWarps * 2 + (b0 + x) * 2 + (x == 0 ? 1 : 0)) * Part<D, NT>::kStride;
+  };
+  float* ms = ml;
+  float* ls = ml + a.ctas * kHeads;
+  for (int i = tid; i < nb * kHeads; i += 512) {
+    const int x = i / kHeads, h = i % kHeads;
+    const bool some = W * (b0 + x) / a.ctas < W * (b0 + x + 1) / a.ctas;  // else a CTA without tiles
+    const float* q = part_of(x) + Part<D, NT>::kO;
+    ms[i] = some ? q[h] : -INFINITY;
+    ls[i] = some ? q[kHeads + h] : -1.f;
+  }
+  __syncthreads();
+  if (warp < kHeads) {  // 16 warps: one head each
+    float m = -INFINITY, l = 0.f;
+    for (int x = lane; x < nb; x += 32)
+      if (ls[x * kHeads + warp] > 0.f) m = fmaxf(m, ms[x * kHeads + warp]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int x = lane; x < nb; x += 32) {
+      const int i = x * kHeads + warp;
+      const float w = ls[i] > 0.f ? ex2_approx(ms[i] - m) : 0.f;
+      l += w > 0.f ? w * ls[i] : 0.f;
+      ms[i] = w;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      bounds[0] = (b + part) * a.subs + (long long)sub * mine;
-      bounds[1] = bounds[0] + mine;
-      Wt = rg.total;
-    }
-    if (blockIdx.x == 0) {
-      const int any = __reduce_max_sync(0xffffffffu, (unsigned)bad);
-      if (lane == 0) bad_s = any;
+      tot_m[warp] = m;
+      tot_l[warp] = l;
     }
   }
-  griddep_wait();
   __syncthreads();
-  if (blockIdx.x == 0) {
-    int bad = 0;
-    for (int x = tid; x < a.ctas; x += 512) bad = max(bad, a.flags[x]);
-    if (bad) atomicMax(&bad_s, bad);
-    __syncthreads();
-    if (tid == 0) *a.status = bad_s;
-  }
-  if (r >= a.R) return;
-  const long long T0 = bounds[0], T1 = bounds[1], W = Wt;
-  const int hk = sub / a.chunks, h0 = hk * a.G + (sub % a.chunks) * a.heads;
-  const int nh = min(a.heads, (hk + 1) * a.G - h0);
-  if (T0 == T1) {  // no positions
-    for (int x = tid; x < nh * D; x += 512) a.out[((long long)r * a.H + h0) * D + x] = __float2bfloat16(0.f);
-    if (a.lse && tid < nh) a.lse[(long long)r * a.H + h0 + tid] = -INFINITY;
-    return;
-  }
-  // the CTAs that hold tiles T0 and T1 - 1: CTA b has [W b / ctas, W (b + 1) / ctas)
-  auto owner = [&](long long x) {
-    int b = (int)(x * a.ctas / W);
-    while (b + 1 < a.ctas && W * (b + 1) / a.ctas <= x) ++b;
-    while (b > 0 && W * b / a.ctas > x) --b;
-    return b;
-  };
-  const int b0 = owner(T0), b1 = owner(T1 - 1);
-  if (b0 == b1) return;  // written by its CTA
-  auto part_of = [&](int b) -> const float* {  // null: a CTA without tiles
-    const long long ca = W * b / a.ctas, cb = W * (b + 1) / a.ctas;
-    if (ca == cb) return nullptr;
-    return a.parts + ((long long)a.ctas * kMaxWarps * 2 + b * 2 + (ca > T0 ? 0 : 1)) * Part<D, NT>::kStride;
-  };
+  // thread t holds float4 t + 128 y of the raw fragments: n-tile (i / 32) mod NT, heads 2 (lane mod 4) + e
   const int grp = tid >> 7, t = tid & 127;
-  // every group's own maximum and sum first
-  float m = -INFINITY, l = 0.f;
-  const int h = t;  // head, for t < 8 NT
-  if (t < 8 * NT) {
-    for (int b = b0 + grp; b <= b1; b += kGroups) {
-      const float* p = part_of(b);
-      if (!p) continue;
-      const float pm = p[Part<D, NT>::kO + h], pl = p[Part<D, NT>::kO + 8 * NT + h];
-      if (!(pl > 0.f)) continue;
-      const float mm = fmaxf(m, pm);
-      l = l * (m > -INFINITY ? ex2_approx(m - mm) : 0.f) + pl * ex2_approx(pm - mm);
-      m = mm;
-    }
-    red_m[grp][h] = m;
-    red_l[grp][h] = l;
-  }
-  __syncthreads();
-  float mt = -INFINITY;
-  if (t < 8 * NT) {
-    for (int x = 0; x < kGroups; ++x) mt = fmaxf(mt, red_m[x][h]);
-    wgt[grp][h][0] = mt;  // the item's maximum
-  }
-  __syncthreads();
   float4 acc[kPer];
 #pragma unroll
   for (int y = 0; y < kPer; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // thread t holds float4 t + 128 y of the raw fragments: n-tile (i / 32) mod NT, heads 2 (lane mod 4) + e
 #pragma unroll 4
-  for (int b = b0 + grp; b <= b1; b += kGroups) {
-    const float* p = part_of(b);
-    if (!p) continue;
+  for (int x = grp; x < nb; x += kGroups) {
+    if (ls[x * kHeads] < 0.f) continue;
+    const float4* p = reinterpret_cast<const float4*>(part_of(x));
 #pragma unroll
     for (int y = 0; y < kPer; ++y) {
       const int i = t + 128 * y, hh = ((i >> 5) % NT) * 8 + 2 * (i & 3);
-      const float4 v = reinterpret_cast<const float4*>(p)[i];
-      const float* ml = p + Part<D, NT>::kO;
-      const float w0 = ml[8 * NT + hh] > 0.f ? ex2_approx(ml[hh] - wgt[grp][hh][0]) : 0.f;
-      const float w1 = ml[8 * NT + hh + 1] > 0.f ? ex2_approx(ml[hh + 1] - wgt[grp][hh + 1][0]) : 0.f;
-      acc[y].x = fmaf(v.x, w0, acc[y].x);
-      acc[y].y = fmaf(v.y, w1, acc[y].y);
-      acc[y].z = fmaf(v.z, w0, acc[y].z);
-      acc[y].w = fmaf(v.w, w1, acc[y].w);
+      const float4 v = p[i];
+      const float2 w = *reinterpret_cast<const float2*>(ms + x * kHeads + hh);
+      acc[y].x = fmaf(v.x, w.x, acc[y].x);
+      acc[y].y = fmaf(v.y, w.y, acc[y].y);
+      acc[y].z = fmaf(v.z, w.x, acc[y].z);
+      acc[y].w = fmaf(v.w, w.y, acc[y].w);
     }
   }
 #pragma unroll
@@ -775,17 +766,13 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int hh = n * 8 + 2 * (lane & 3) + e;
-        float ls = 0.f;
-        const float mm = wgt[0][hh][0];
-        for (int x = 0; x < kGroups; ++x)
-          if (red_l[x][hh] > 0.f) ls += red_l[x][hh] * ex2_approx(red_m[x][hh] - mm);
-        st.m[n][e] = mm;
-        st.l[n][e] = ls;
+        st.m[n][e] = tot_m[n * 8 + 2 * (lane & 3) + e];
+        st.l[n][e] = tot_l[n * 8 + 2 * (lane & 3) + e];
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         float4 v = acc_s[0][(i * NT + n) * 32 + lane];
+#pragma unroll
         for (int x = 1; x < kGroups; ++x) {
           const float4 u = acc_s[x][(i * NT + n) * 32 + lane];
           v.x += u.x;
@@ -799,7 +786,7 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
         st.o[i][n][3] = v.w;
       }
     }
-    write_item<D, FP8, NT>(a, st, r, sub, lane);
+    write_item<D, FP8, NT>(a, st, in.r, in.sub, lane);
   }
 }
 
@@ -831,8 +818,11 @@ cudaError_t launch_t(const PagedAttnArgs& a, PagedParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, FP8, NT><<<p.ctas, L::kWarps * 32, L::kSmem, s>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return cross::launch_dependent(paged_join_kernel<D, FP8, NT>, dim3((unsigned)((long long)a.R * p.subs)),
-                                 dim3(512), 0, s, p);
+  const size_t join = (size_t)p.ctas * 2 * 8 * NT * sizeof(float);
+  if ((e = cudaFuncSetAttribute(paged_join_kernel<D, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)join)) != cudaSuccess)
+    return e;
+  return cross::launch_dependent(paged_join_kernel<D, FP8, NT>, dim3((unsigned)p.ctas), dim3(512), join, s, p);
 }
 
 __global__ void paged_clear_kernel(WsHeader* hdr) { hdr->status = 0; }
@@ -842,8 +832,8 @@ __global__ void paged_clear_kernel(WsHeader* hdr) { hdr->status = 0; }
 size_t paged_attn_plan(int R, int H, int Hkv, int d, int sms, PagedAttnPlan* p) {
   PagedAttnPlan q;
   const int nt = H / Hkv > 8 ? 2 : 1;
-  q.flags = sizeof(WsHeader);
-  q.parts = (q.flags + (size_t)sms * 4 + 255) / 256 * 256;
+  q.info = sizeof(WsHeader);
+  q.parts = (q.info + (size_t)sms * sizeof(CtaInfo) + 255) / 256 * 256;
   const size_t part = ((size_t)nt * d / 16 * 128 + 16 * nt) * sizeof(float);
   q.total = q.parts + (size_t)sms * (2 * kMaxWarps + 2) * part;
   if (p) *p = q;
@@ -879,7 +869,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s) {
   p.c = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.flags = reinterpret_cast<int*>(ws + a.plan.flags);
+  p.info = reinterpret_cast<CtaInfo*>(ws + a.plan.info);
   p.parts = reinterpret_cast<float*>(ws + a.plan.parts);
   p.status = &hdr->status;
   p.ctas = a.sms;
