@@ -16,8 +16,13 @@
 // order: the result does not depend on timing. The 12 to 16 tiles in flight on an SM, 144 to
 // 224 KB, are more than the 45 KB that the memory's latency times its rate needs.
 //
-// FP8 codes go to bf16 exactly: exponent and mantissa moved to bf16's fields, times 2^120; a
-// row's scale multiplies its scores, and its weights, in fp32.
+// FP8 codes go to fp16 exactly (one conversion instruction a pair), and the products run in fp16.
+// A head's query is brought to [2^8, 2^9) by a power of two, which costs nothing that fp32 sums
+// would keep (what falls below fp16's steps is 2^-33 of the largest value); the weights are
+// p v_scale / 2^e with 2^e the power of two above the largest v_scale so far, so they stay
+// below 2^8 and are rounded to 2^-12 of their value, or to 2^-25 where they are below 2^-14.
+// (The same steps through bf16 took 9 integer instructions a word in place of 2 or 3: 0.39 against
+// see below.) A key's scale multiplies its scores in fp32.
 #include <cmath>
 
 #include "sa_cross.cuh"
@@ -65,19 +70,28 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// E4M3 to bf16, exactly, for the low (bytes 0 and 2) and high (1 and 3) bytes of a word:
-// s eeee mmm moved to s 0000eeee mmm0000 is 2^-120 times the value, subnormal codes included.
-__device__ __forceinline__ uint32_t times_2_120(uint32_t x) {
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four E4M3 codes to two pairs of fp16, in order.
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7B807B80u));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) {
-  return times_2_120(((w << 8) & 0x80008000u) | ((w << 4) & 0x07F007F0u));
-}
-__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) {
-  return times_2_120((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u));
-}
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // What a CTA leaves for the join: errors seen, and the item (request, sub) that it saw the start
 // of and that goes on in later CTAs, up to tile `end` of the `total` tiles.
@@ -209,8 +223,10 @@ struct Part {
 template <int D, int NT>
 struct State {
   float o[D / 16][NT][4];
+  int ve;  // FP8: o is in units of 2^ve
   float m[NT][2], l[NT][2];  // heads 8 nt + 2 (lane mod 4) and the next; l summed over this lane's keys
   __device__ void clear() {
+    ve = -126;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
@@ -218,6 +234,15 @@ struct State {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
+  }
+  __device__ void plain_units() {
+    const float f = pow2i(ve);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[i][n][x] *= f;
   }
   __device__ void sum_l() {  // over the lanes that hold other keys of the same head
 #pragma unroll
@@ -400,6 +425,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
     State<D, NT> st;
     uint32_t qf[KS][NT][2];
+    float qc[NT][2];  // FP8: c times what the query's power of two took away
     bool fresh = true, from_start = false;
     for (int i = 0; i < n_tiles; ++i) {
       const int slot = i & 1;
@@ -412,16 +438,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int n = 0; n < NT; ++n) {
           const __nv_bfloat16* qr = a.Q + cur.r * a.q_stride + (h0 + 8 * n + g) * D;
           const bool w = 8 * n + g < nh;
+          uint32_t top = 0;  // FP8: the row's largest magnitude (bits of a float)
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             if (FP8) {
               const uint2 v = w ? *reinterpret_cast<const uint2*>(qr + 16 * ks + 4 * q4) : make_uint2(0, 0);
-              qf[ks][n][0] = __byte_perm(v.x, v.y, 0x5410);  // even and odd values apart, as the
-              qf[ks][n][1] = __byte_perm(v.x, v.y, 0x7632);  // codes of a word are taken
+              qf[ks][n][0] = v.x;
+              qf[ks][n][1] = v.y;
+              top = max(top, max((v.x << 16) & 0x7fffffffu, v.x & 0x7fff0000u));
+              top = max(top, max((v.y << 16) & 0x7fffffffu, v.y & 0x7fff0000u));
             } else {
               qf[ks][n][0] = w ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 2 * q4) : 0u;
               qf[ks][n][1] = w ? *reinterpret_cast<const uint32_t*>(qr + 16 * ks + 8 + 2 * q4) : 0u;
             }
+          }
+          if (FP8) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max((int)(top >> 23), 10) - 135;  // row max in [2^(e + 8), 2^(e + 9))
+            const float down = pow2i(-e);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t v = qf[ks][n][x];
+                qf[ks][n][x] = cvt_f16x2(__uint_as_float(v << 16) * down,
+                                         __uint_as_float(v & 0xffff0000u) * down);
+              }
+            const float up = pow2i(e) * a.c;  // row g's; this lane's score columns are heads 2 q4, + 1
+            qc[n][0] = __shfl_sync(0xffffffffu, up, 8 * q4);
+            qc[n][1] = __shfl_sync(0xffffffffu, up, 8 * q4 + 4);
           }
         }
         fresh = false;
@@ -459,13 +505,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             ldsm4(kb + row * L::kRow + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4), w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              // bytes 4t .. 4t + 3 of a piece: k = 2t, 2t + 1 take bytes 0, 2 and k = 2t + 8, 2t + 9
-              // bytes 1, 3
-              const uint32_t a0 = e4m3_even(w[2 * h]), a2 = e4m3_odd(w[2 * h]);
-              const uint32_t a1 = e4m3_even(w[2 * h + 1]), a3 = e4m3_odd(w[2 * h + 1]);
+              // bytes 4t .. 4t + 3 of a piece: k = 2t, 2t + 1 and k = 2t + 8, 2t + 9
+              uint32_t a0, a1, a2, a3;
+              e4m3x4(w[2 * h], a0, a2);
+              e4m3x4(w[2 * h + 1], a1, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816(s[mt][n], a0, a1, a2, a3, qf[ks + h][n][0], qf[ks + h][n][1]);
+                mma16816_f16(s[mt][n], a0, a1, a2, a3, qf[ks + h][n][0], qf[ks + h][n][1]);
             }
           }
         } else {
@@ -489,18 +535,38 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
           const int key = mt * 16 + g + 8 * hi;
-          const float f = FP8 ? a.c * ksc[key] : a.c;
+          const float f = FP8 ? ksc[key] : a.c;
           const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float z = in ? s[mt][n][2 * hi + e] * f : -INFINITY;
+              const float z = in ? s[mt][n][2 * hi + e] * (FP8 ? f * qc[n][e] : f) : -INFINITY;
               s[mt][n][2 * hi + e] = z;
               mx[n][e] = fmaxf(mx[n][e], z);
             }
         }
       bool raise = false;
+      float fv = 1.f;  // FP8: the change of o's unit
+      if (FP8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            const int key = mt * 16 + g + 8 * hi;
+            if (!edge || (p0 + key >= cur.first && p0 + key < cur.len))
+              top = max(top, __float_as_uint(ksc[T + key]) & 0x7fffffffu);
+          }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const int e = min((int)(top >> 23) - 126, 126);  // 2^e is above every scale
+        if (e > st.ve) {
+          fv = pow2i(max(st.ve - e, -126));
+          st.ve = e;
+          raise = true;
+        }
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -519,6 +585,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             f[e] = st.m[n][e] > -INFINITY ? ex2_approx(st.m[n][e] - mm) : 0.f;
             st.m[n][e] = mm;
             st.l[n][e] *= f[e];
+            if (FP8) f[e] *= fv;
           }
 #pragma unroll
           for (int y = 0; y < KS; ++y) {
@@ -530,6 +597,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
       }
       uint32_t pf[MT][NT][2];
+      const float vdown = FP8 ? pow2i(-st.ve) : 1.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0 = st.m[n][0] == -INFINITY ? 0.f : st.m[n][0];
@@ -543,12 +611,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             st.l[n][1] += e1;
             if (FP8) {
               const int key = mt * 16 + g + 8 * hi;
-              const float vs = ksc[T + key];
+              const float vs = ksc[T + key] * vdown;
               const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
               e0 = in ? e0 * vs : 0.f;
               e1 = in ? e1 * vs : 0.f;
             }
-            pf[mt][n][hi] = transpose8(cvt_bf16x2(e0, e1));
+            pf[mt][n][hi] = transpose8(FP8 ? cvt_f16x2(e0, e1) : cvt_bf16x2(e0, e1));
           }
       }
       // ---- O^T += V^T P^T
@@ -563,11 +631,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             ldsm4_t(vb + row * L::kRow + ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4), w);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = e4m3_even(w[2 * h]), a1 = e4m3_odd(w[2 * h]);
-              const uint32_t a2 = e4m3_even(w[2 * h + 1]), a3 = e4m3_odd(w[2 * h + 1]);
+              // a word is (key 2t: d, d + 1), (key 2t + 1: d, d + 1): pairs of keys instead
+              uint32_t a0, a1, a2, a3;
+              e4m3x4(__byte_perm(w[2 * h], 0, 0x3120), a0, a1);
+              e4m3x4(__byte_perm(w[2 * h + 1], 0, 0x3120), a2, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816(st.o[dm + h][n], a0, a1, a2, a3, pf[kk][n][0], pf[kk][n][1]);
+                mma16816_f16(st.o[dm + h][n], a0, a1, a2, a3, pf[kk][n][0], pf[kk][n][1]);
             }
           }
         } else {
@@ -590,6 +660,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const bool ends = cur.t + 1 == cur.t1;
       if (ends || i + 1 == n_tiles) {
         st.sum_l();
+        if (FP8) st.plain_units();
         if (ends && from_start) {
           write_item<D, FP8, NT>(a, st, cur.r, cur.sub, lane);
         } else if (!from_start) {
