@@ -33,16 +33,18 @@ namespace {
 using cross::kLn2;
 using cross::kLog2e;
 constexpr float kRaise = 8.f;  // raise the running maximum only when passed by this (log2 units)
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 12;
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NT>
 struct Geo {
-  static constexpr int T = FP8 || D == 64 ? 64 : 32;      // keys per tile
+  static constexpr int T = D == 64 ? 64 : 32;             // keys per tile
   static constexpr int kRow = FP8 ? D : 128;              // bytes of a shared-memory row
   static constexpr int kHalves = FP8 ? 1 : D / 64;        // a bf16 row of 128 is two 128-byte halves
   static constexpr int kMat = T * D * (FP8 ? 1 : 2);      // bytes of K or of V
   static constexpr int kSlot = 2 * kMat + (FP8 ? 1024 : 0);  // and the scales (1024-aligned slots)
-  static constexpr int kWarps = !FP8 ? 7 : D == 128 ? 6 : 8;  // as many as fit with two slots each
+  // As many warps as fit with two slots each: 7 of 32 KB, or 12 of 18 KB; with 16 heads a warp needs
+  // more registers than 12 leave it (8 against 9 with spills: 0.61 and 0.48 of the copy rate).
+  static constexpr int kWarps = !FP8 ? 7 : NT == 1 ? 12 : 8;
   static constexpr int oBars = kWarps * 2 * kSlot;
   static constexpr size_t kSmem = 1024 + oBars + kWarps * 2 * 8;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -340,10 +342,10 @@ __device__ __forceinline__ void write_item(const PagedParams& a, const State<D, 
 enum : int { kNone = 0, kOpen = 1, kEnds = 2 };  // kEnds: reaches the item's end
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(Geo<D, FP8>::kWarps * 32, 1)
+__global__ void __launch_bounds__(Geo<D, FP8, NT>::kWarps * 32, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   const __grid_constant__ PagedParams a) {
-  using L = Geo<D, FP8>;
+  using L = Geo<D, FP8, NT>;
   constexpr int T = L::T, MT = T / 16, KS = D / 16, kWarps = L::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -477,7 +479,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         break;
       }
       const uint32_t kb = slot0 + slot * L::kSlot, vb = kb + L::kMat;
-      const float* ksc = reinterpret_cast<const float*>(smem + (kb - smem_u32(smem)) + 2 * L::kMat);
+      float* ksc = reinterpret_cast<float*>(smem + (kb - smem_u32(smem)) + 2 * L::kMat);
       const int p0 = cur.t * T;
       const bool edge = p0 < cur.first || p0 + T > cur.len;
       if (edge) {  // weight 0 meets these rows of V: they must not hold NaN
@@ -488,6 +490,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             *reinterpret_cast<uint4*>(vs + half * T * 128 + (z % T) * L::kRow + y * 16) =
                 make_uint4(0, 0, 0, 0);
         }
+        if (FP8)
+          for (int x = lane; x < T; x += 32)
+            if (p0 + x < cur.first || p0 + x >= cur.len) ksc[T + x] = 0.f;
         __syncwarp();
       }
       // ---- S^T = K Q^T
@@ -527,24 +532,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
       }
       // ---- softmax along the keys: lane column = heads 2 q4 and 2 q4 + 1, rows g and g + 8
-      float mx[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
-          const int key = mt * 16 + g + 8 * hi;
-          const float f = FP8 ? ksc[key] : a.c;
-          const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
+          const float f = FP8 ? ksc[mt * 16 + g + 8 * hi] : a.c;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float z = in ? s[mt][n][2 * hi + e] * (FP8 ? f * qc[n][e] : f) : -INFINITY;
-              s[mt][n][2 * hi + e] = z;
-              mx[n][e] = fmaxf(mx[n][e], z);
+            for (int e = 0; e < 2; ++e) s[mt][n][2 * hi + e] *= FP8 ? f * qc[n][e] : f;
+        }
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            const int p = p0 + mt * 16 + g + 8 * hi;
+            if (p < cur.first || p >= cur.len) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n) s[mt][n][2 * hi] = s[mt][n][2 * hi + 1] = -INFINITY;
             }
+          }
+      }
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+          for (int mt = 1; mt < MT; ++mt) mx[n][e] = fmax3(mx[n][e], s[mt][n][e], s[mt][n][2 + e]);
         }
       bool raise = false;
       float fv = 1.f;  // FP8: the change of o's unit
@@ -553,11 +570,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            const int key = mt * 16 + g + 8 * hi;
-            if (!edge || (p0 + key >= cur.first && p0 + key < cur.len))
-              top = max(top, __float_as_uint(ksc[T + key]) & 0x7fffffffu);
-          }
+          for (int hi = 0; hi < 2; ++hi)
+            top = max(top, __float_as_uint(ksc[T + mt * 16 + g + 8 * hi]) & 0x7fffffffu);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
         const int e = min((int)(top >> 23) - 126, 126);  // 2^e is above every scale
@@ -610,11 +624,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             st.l[n][0] += e0;
             st.l[n][1] += e1;
             if (FP8) {
-              const int key = mt * 16 + g + 8 * hi;
-              const float vs = ksc[T + key] * vdown;
-              const bool in = !edge || (p0 + key >= cur.first && p0 + key < cur.len);
-              e0 = in ? e0 * vs : 0.f;
-              e1 = in ? e1 * vs : 0.f;
+              const float vs = ksc[T + mt * 16 + g + 8 * hi] * vdown;
+              e0 *= vs;
+              e1 *= vs;
             }
             pf[mt][n][hi] = transpose8(FP8 ? cvt_f16x2(e0, e1) : cvt_bf16x2(e0, e1));
           }
@@ -877,7 +889,7 @@ bool tmap_cache(CUtensorMap* m, const void* base, uint64_t rows, int d, bool fp8
 
 template <int D, bool FP8, int NT>
 cudaError_t launch_t(const PagedAttnArgs& a, PagedParams& p, cudaStream_t s) {
-  using L = Geo<D, FP8>;
+  using L = Geo<D, FP8, NT>;
   const int ps = 1 << a.log2_page, box = ps < L::T ? ps : L::T;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * ps;
