@@ -299,6 +299,23 @@ struct State {
   }
 };
 
+// out of 16 columns of d (fragment i) and 8 heads, from (d, heads) to (head g, pairs of d).
+template <bool FP8>
+__device__ __forceinline__ void write_fragment(const float (&o)[4], float inv0, float inv1, bool write,
+                                               __nv_bfloat16* row, int q4) {
+  const uint32_t lo = transpose8(cvt_bf16x2(o[0] * inv0, o[1] * inv1));
+  const uint32_t hi = transpose8(cvt_bf16x2(o[2] * inv0, o[3] * inv1));
+  if (write) {
+    if (FP8) {  // fragment rows 0-7 are d = 0, 2, .., 14 and rows 8-15 are d = 1, 3, .., 15
+      *reinterpret_cast<uint2*>(row + 4 * q4) =
+          make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    } else {
+      *reinterpret_cast<uint32_t*>(row + 2 * q4) = lo;
+      *reinterpret_cast<uint32_t*>(row + 8 + 2 * q4) = hi;
+    }
+  }
+}
+
 // out and lse of an item from its finished state (l summed over lanes).
 template <int D, bool FP8, int NT>
 __device__ __forceinline__ void write_item(const PagedParams& a, const State<D, NT>& st, int r, int sub,
@@ -311,22 +328,9 @@ __device__ __forceinline__ void write_item(const PagedParams& a, const State<D, 
     const float i0 = st.l[n][0] > 0.f ? 1.f / st.l[n][0] : 0.f;
     const float i1 = st.l[n][1] > 0.f ? 1.f / st.l[n][1] : 0.f;
     __nv_bfloat16* row = a.out + ((long long)r * a.H + h0 + 8 * n + g) * D;
-    const bool w = 8 * n + g < nh;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      // (d, heads) to (head g, d pairs)
-      const uint32_t lo = transpose8(cvt_bf16x2(st.o[i][n][0] * i0, st.o[i][n][1] * i1));
-      const uint32_t hi = transpose8(cvt_bf16x2(st.o[i][n][2] * i0, st.o[i][n][3] * i1));
-      if (w) {
-        if (FP8) {  // fragment rows 0-7 are d = 0, 2, .., 14 and rows 8-15 are d = 1, 3, .., 15
-          *reinterpret_cast<uint2*>(row + 16 * i + 4 * t) =
-              make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-        } else {
-          *reinterpret_cast<uint32_t*>(row + 16 * i + 2 * t) = lo;
-          *reinterpret_cast<uint32_t*>(row + 16 * i + 8 + 2 * t) = hi;
-        }
-      }
-    }
+    for (int i = 0; i < D / 16; ++i)
+      write_fragment<FP8>(st.o[i][n], i0, i1, 8 * n + g < nh, row + 16 * i, t);
     if (a.lse && g == 0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
@@ -760,19 +764,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 }
 
 // An item that spans CTAs: block b joins the one that starts in CTA b and goes on, from the parts
-// of CTAs b .. b1 in order (four groups of threads take every fourth part each and are then
-// put together). Block 0 also writes the device status.
-template <int D, bool FP8, int NT>
+// of CTAs b .. b1 in order (groups of threads take every kGroups-th part each and are then put
+// together). SLICED: the blocks (b, i) join 16 columns i of d each, for few items of many parts
+// (one block took 20 us for the 148 parts of a lone request of 100K, the slices 10; with many items,
+// of few parts each, the slices' blocks cost 3 to 5 us). Block (0, 0) also writes the device status.
+template <int D, bool FP8, int NT, bool SLICED>
 __global__ void __launch_bounds__(512)
 paged_join_kernel(const __grid_constant__ PagedParams a) {
-  constexpr int kV = NT * D / 16 * 32, kHeads = 8 * NT;  // float4 and heads of a part
-  constexpr int kGroups = 4, kPer = kV / 128;
+  constexpr int kFrags = SLICED ? NT : NT * D / 16;  // fragments (16 columns x 8 heads) of a block
+  constexpr int kV = kFrags * 32, kHeads = 8 * NT, kGroups = 512 / kV;
   extern __shared__ float ml[];  // [2][CTAs][kHeads]: maxima, then weights; sums (-1: no part)
   __shared__ float tot_m[kHeads], tot_l[kHeads];
   __shared__ float4 acc_s[kGroups][kV];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = blockIdx.x, ci = blockIdx.y;
   griddep_wait();
-  if (b0 == 0) {
+  if (b0 == 0 && ci == 0) {
     int bad = 0;
     for (int x = tid; x < a.ctas; x += 512) bad = max(bad, a.info[x].error);
     bad = __syncthreads_or(bad == SA_ERR_TIMEOUT) ? SA_ERR_TIMEOUT
@@ -820,56 +826,41 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
     }
   }
   __syncthreads();
-  // thread t holds float4 t + 128 y of the raw fragments: n-tile (i / 32) mod NT, heads 2 (lane mod 4) + e
-  const int grp = tid >> 7, t = tid & 127;
-  float4 acc[kPer];
-#pragma unroll
-  for (int y = 0; y < kPer; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // thread t of a group holds float4 t: n-tile (t / 32) mod NT, heads 2 (t mod 4) + e
+  const int grp = tid / kV, t = tid % kV, hh = (t >> 5) % NT * 8 + 2 * (t & 3);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int x = grp; x < nb; x += kGroups) {
-    if (ls[x * kHeads] < 0.f) continue;
-    const float4* p = reinterpret_cast<const float4*>(part_of(x));
-#pragma unroll
-    for (int y = 0; y < kPer; ++y) {
-      const int i = t + 128 * y, hh = ((i >> 5) % NT) * 8 + 2 * (i & 3);
-      const float4 v = p[i];
-      const float2 w = *reinterpret_cast<const float2*>(ms + x * kHeads + hh);
-      acc[y].x = fmaf(v.x, w.x, acc[y].x);
-      acc[y].y = fmaf(v.y, w.y, acc[y].y);
-      acc[y].z = fmaf(v.z, w.x, acc[y].z);
-      acc[y].w = fmaf(v.w, w.y, acc[y].w);
-    }
+    const float4* p = reinterpret_cast<const float4*>(part_of(x)) + ci * kV;
+    const float4 v = ls[x * kHeads] < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : p[t];
+    const float2 w = *reinterpret_cast<const float2*>(ms + x * kHeads + hh);
+    acc.x = fmaf(v.x, w.x, acc.x);
+    acc.y = fmaf(v.y, w.y, acc.y);
+    acc.z = fmaf(v.z, w.x, acc.z);
+    acc.w = fmaf(v.w, w.y, acc.w);
   }
-#pragma unroll
-  for (int y = 0; y < kPer; ++y) acc_s[grp][t + 128 * y] = acc[y];
+  acc_s[grp][t] = acc;
   __syncthreads();
-  if (tid < 32) {  // one warp writes the item, as the main kernel's warps do
-    State<D, NT> st;
+  if (warp < kFrags) {  // a warp per fragment writes, as the main kernel's warps do
+    const int g = lane >> 2, q4 = lane & 3, hk = in.sub / a.chunks, n = warp % NT, i = ci + warp / NT;
+    const int h0 = hk * a.G + (in.sub % a.chunks) * a.heads, nh = min(a.heads, (hk + 1) * a.G - h0);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        st.m[n][e] = tot_m[n * 8 + 2 * (lane & 3) + e];
-        st.l[n][e] = tot_l[n * 8 + 2 * (lane & 3) + e];
-      }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        float4 v = acc_s[0][(i * NT + n) * 32 + lane];
-#pragma unroll
-        for (int x = 1; x < kGroups; ++x) {
-          const float4 u = acc_s[x][(i * NT + n) * 32 + lane];
-          v.x += u.x;
-          v.y += u.y;
-          v.z += u.z;
-          v.w += u.w;
-        }
-        st.o[i][n][0] = v.x;
-        st.o[i][n][1] = v.y;
-        st.o[i][n][2] = v.z;
-        st.o[i][n][3] = v.w;
-      }
+    for (int x = 0; x < kGroups; ++x) {
+      const float4 u = acc_s[x][warp * 32 + lane];
+      o[0] += u.x;
+      o[1] += u.y;
+      o[2] += u.z;
+      o[3] += u.w;
     }
-    write_item<D, FP8, NT>(a, st, in.r, in.sub, lane);
+    const float l0 = tot_l[n * 8 + 2 * q4], l1 = tot_l[n * 8 + 2 * q4 + 1];
+    write_fragment<FP8>(o, l0 > 0.f ? 1.f / l0 : 0.f, l1 > 0.f ? 1.f / l1 : 0.f, 8 * n + g < nh,
+                        a.out + ((long long)in.r * a.H + h0 + 8 * n + g) * D + 16 * i, q4);
+    if (a.lse && i == 0 && lane < 8 && 8 * n + lane < nh) {
+      const float l = tot_l[n * 8 + lane];
+      a.lse[(long long)in.r * a.H + h0 + 8 * n + lane] =
+          l > 0.f ? (tot_m[n * 8 + lane] + lg2_approx(l)) * kLn2 : -INFINITY;
+    }
   }
 }
 
@@ -901,11 +892,14 @@ cudaError_t launch_t(const PagedAttnArgs& a, PagedParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, FP8, NT><<<p.ctas, L::kWarps * 32, L::kSmem, s>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const size_t join = (size_t)p.ctas * 2 * 8 * NT * sizeof(float);
-  if ((e = cudaFuncSetAttribute(paged_join_kernel<D, FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)join)) != cudaSuccess)
+  const bool sliced = (long long)a.R * p.subs * 8 <= p.ctas;  // items of more than eight parts
+  auto join = sliced ? paged_join_kernel<D, FP8, NT, true> : paged_join_kernel<D, FP8, NT, false>;
+  const size_t join_smem = (size_t)p.ctas * 2 * 8 * NT * sizeof(float);
+  if ((e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join_smem)) !=
+      cudaSuccess)
     return e;
-  return cross::launch_dependent(paged_join_kernel<D, FP8, NT>, dim3((unsigned)p.ctas), dim3(512), join, s, p);
+  return cross::launch_dependent(join, dim3((unsigned)p.ctas, sliced ? D / 16 : 1), dim3(512), join_smem, s,
+                                 p);
 }
 
 __global__ void paged_clear_kernel(WsHeader* hdr) { hdr->status = 0; }
