@@ -185,6 +185,7 @@ int sa_page_tables(const int32_t* cached_lens, const int32_t* new_lens, int R, i
   a.seq_lens = seq_lens;
   a.free_used_out = free_used_out;
   a.hdr = static_cast<WsHeader*>(workspace);
+  a.wide = on16(slots);
   return status_of(launch_page_tables(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -209,8 +210,7 @@ int sa_paged_append(const void* K, int64_t k_stride, const void* V, int64_t v_st
     return SA_ERR_INVALID_ARG;
   if (k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d || k_stride % 8 || v_stride % 8)
     return SA_ERR_INVALID_ARG;
-  int sms = 0;
-  if ((st = device_sms(&sms)) != SA_OK) return st;
+  if ((st = device_sms(&a.sms)) != SA_OK) return st;
   a.K = K;
   a.V = V;
   a.k_stride = k_stride;

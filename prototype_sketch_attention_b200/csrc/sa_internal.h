@@ -347,6 +347,7 @@ struct PageTablesArgs {
   int32_t* seq_lens;
   int64_t* free_used_out;
   WsHeader* hdr;
+  bool wide;                  // slots is 16-byte aligned
   int sms;
 };
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t s);
@@ -362,6 +363,7 @@ struct PagedAppendArgs {
   void* v_cache;
   float* k_scales;
   float* v_scales;
+  int sms;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
 

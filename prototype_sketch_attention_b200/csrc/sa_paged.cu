@@ -10,10 +10,13 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 
-// Inclusive prefix sums over the block (up to 1024 threads) of two counts at once.
-__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long (&part)[2][32],
+constexpr int kUsers = 512;  // requests per chunk, one a thread
+
+// Exclusive prefix sums over the block of two counts at once, and their totals.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long (&part)[2][kUsers / 32],
                                             long long& total_a, long long& total_b) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long a0 = a, b0 = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
@@ -22,67 +25,92 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& b, long lon
       b += y;
     }
   }
-  __syncthreads();
+  __syncthreads();  // the last use of `part`
   if (lane == 31) {
     part[0][warp] = a;
     part[1][warp] = b;
   }
   __syncthreads();
-  long long ba = 0, bb = 0;
-  total_a = total_b = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w < warp) {
-      ba += part[0][w];
-      bb += part[1][w];
+  long long x = part[0][lane & 15], y = part[1][lane & 15];  // every warp sums the warps' totals
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o, 16), v = __shfl_up_sync(0xffffffffu, y, o, 16);
+    if ((lane & 15) >= o) {
+      x += u;
+      y += v;
     }
-    total_a += part[0][w];
-    total_b += part[1][w];
   }
-  a += ba;
-  b += bb;
+  total_a = __shfl_sync(0xffffffffu, x, 15);
+  total_b = __shfl_sync(0xffffffffu, y, 15);
+  const long long ba = __shfl_sync(0xffffffffu, x, (warp + 15) & 15), bb = __shfl_sync(0xffffffffu, y, (warp + 15) & 15);
+  a += (warp ? ba : 0) - a0;
+  b += (warp ? bb : 0) - b0;
 }
 
-// Every block first adds up all requests (the verdict is needed before anything is
-// written), then walks the requests again, kUsers at a time, keeping their prefix sums in
-// shared memory, and writes the slots of its own share [s0, s1) of the new positions. Block 0
-// also writes the tables, offsets and lengths.
-constexpr int kUsers = 512;
-constexpr int kTableThreads = 512;
+// One request's counts; bad: bit 0 lengths, bit 1 pages.
+struct Request {
+  int cached, fresh, have, need;  // positions held and new; pages held and to be taken
+  __device__ void load(const PageTablesArgs& a, int r, int* bad) {
+    cached = fresh = have = need = 0;
+    if (r >= a.R) return;
+    const int c = a.cached[r], n = a.fresh[r];
+    const long long end = (long long)c + n;
+    if (c < 0 || n < 0 || end > 0x7fffffffLL) {
+      *bad |= 1;
+      return;
+    }
+    const int ps = 1 << a.log2_page;
+    have = (int)(((long long)c + ps - 1) >> a.log2_page);
+    const int want = (int)((end + ps - 1) >> a.log2_page);
+    if (want > a.max_pages) *bad |= 2;
+    cached = c;
+    fresh = n;
+    need = want - have;
+  }
+};
 
-__global__ void __launch_bounds__(kTableThreads) page_tables_kernel(PageTablesArgs a) {
-  __shared__ long long part[2][32];
-  __shared__ long long off[kUsers + 1], pg[kUsers];
+// One launch. A verdict over all requests is needed before anything is written, so every block
+// adds all of them up (two 4-byte reads a request), then walks them 512 at a time with
+// their prefix sums in shared memory and writes its own share [s0, s1) of the slots, V a thread:
+// one search for the request, then a walk; the thread of a new page's first position writes its table entry. V = 8
+// when there are many slots (bound: 8 bytes written a slot), else 1 (bound: the chain of loads).
+// Block 0 also writes offsets and lengths.
+template <int V>
+__global__ void __launch_bounds__(kUsers) page_tables_kernel(PageTablesArgs a) {
+  __shared__ long long part[2][kUsers / 32];
+  __shared__ int off[kUsers + 1], pg[kUsers], held[kUsers];  // first slot, free entry; positions held
   const int tid = threadIdx.x, ps = 1 << a.log2_page;
   const long long used = a.free_used ? *a.free_used : 0;
-  // verdict
-  long long toks = 0, pages = 0;
-  int bad = 0;  // bit 0: lengths, bit 1: pages
-  for (int r = tid; r < a.R; r += blockDim.x) {
-    const long long c = a.cached[r], n = a.fresh[r];
-    if (c < 0 || n < 0 || c + n > 0x7fffffffLL) { bad |= 1; continue; }
-    const long long have = (c + ps - 1) >> a.log2_page, want = (c + n + ps - 1) >> a.log2_page;
-    if (want > a.max_pages) bad |= 2;
-    toks += n;
-    pages += want - have;
+  const bool lead = blockIdx.x == 0;
+  int bad = 0;
+  Request q;
+  q.load(a, tid, &bad);
+  long long it = q.fresh, ip = q.need, tt, tp;
+  if (a.R > kUsers) {
+    Request x;
+    for (int r = tid + kUsers; r < a.R; r += kUsers) {
+      x.load(a, r, &bad);
+      it += x.fresh;
+      ip += x.need;
+    }
   }
-  long long tt, tp;
-  block_scan2(toks, pages, part, tt, tp);
+  block_scan2(it, ip, part, tt, tp);
   if (tt > a.n_slots) bad |= 1;
   if (used < 0 || used + tp > a.n_free) bad |= 2;
   const int bad1 = __syncthreads_or(bad & 1), bad2 = __syncthreads_or(bad & 2);
   const bool stop = bad1 || bad2;
-  const bool lead = blockIdx.x == 0;
-  const long long per = (a.n_slots + gridDim.x - 1) / gridDim.x;
-  const long long s0 = min((long long)a.n_slots, blockIdx.x * per), s1 = min((long long)a.n_slots, s0 + per);
+  // slots, entries of the free list and positions are below 2^31
+  const long long per = ((a.n_slots + gridDim.x - 1) / gridDim.x + 32 * V - 1) / (32 * V) * (32 * V);
+  const int s0 = (int)min(a.n_slots, blockIdx.x * per), s1 = (int)min(a.n_slots, s0 + per);
   if (lead && tid == 0) {
     a.hdr->status = bad1 ? SA_ERR_BAD_OFFSETS : bad2 ? SA_ERR_BAD_PAGES : SA_OK;
     *a.free_used_out = stop ? used : used + tp;
     a.new_offsets[a.R] = stop ? 0 : tt;
   }
-  for (long long i = max(s0, stop ? 0 : tt) + tid; i < s1; i += blockDim.x) a.slots[i] = -1;
+  for (long long i = max((long long)s0, stop ? 0 : tt) + tid; i < s1; i += kUsers) a.slots[i] = -1;
   if (stop) {
     if (lead)
-      for (int r = tid; r < a.R; r += blockDim.x) {
+      for (int r = tid; r < a.R; r += kUsers) {
         a.new_offsets[r] = 0;
         a.seq_lens[r] = a.cached[r];
       }
@@ -90,47 +118,68 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(PageTablesAr
   }
   long long base_t = 0, base_p = used;
   for (int r0 = 0; r0 < a.R; r0 += kUsers) {
-    const int r = r0 + tid, nu = min(kUsers, a.R - r0);
-    long long c = 0, n = 0, have = 0, need = 0;
-    if (tid < nu) {
-      c = a.cached[r];
-      n = a.fresh[r];
-      have = (c + ps - 1) >> a.log2_page;
-      need = ((c + n + ps - 1) >> a.log2_page) - have;
+    const int nu = min(kUsers, a.R - r0);
+    long long ct = tt, cp = tp;
+    if (r0 > 0) q.load(a, r0 + tid, &bad);
+    if (a.R > kUsers) {  // else the verdict's sums are this chunk's
+      it = q.fresh;
+      ip = q.need;
+      block_scan2(it, ip, part, ct, cp);
     }
-    long long it = n, ip = need, ct, cp;
-    block_scan2(it, ip, part, ct, cp);
     if (tid < nu) {
-      off[tid] = base_t + it - n;
-      pg[tid] = base_p + ip - need;
+      off[tid] = (int)(base_t + it);
+      pg[tid] = (int)(base_p + ip);
+      held[tid] = q.cached;
       if (lead) {
-        a.new_offsets[r] = base_t + it - n;
-        a.seq_lens[r] = (int)(c + n);
+        a.new_offsets[r0 + tid] = base_t + it;
+        a.seq_lens[r0 + tid] = q.cached + q.fresh;
       }
     }
-    if (tid == 0) off[nu] = base_t + ct;
+    if (tid == 0) off[nu] = (int)(base_t + ct);
     __syncthreads();
-    if (lead) {
-      for (int x = tid >> 5; x < nu; x += blockDim.x >> 5) {
-        const long long cx = a.cached[r0 + x], nx = a.fresh[r0 + x];
-        const long long hx = (cx + ps - 1) >> a.log2_page;
-        const int nd = (int)(((cx + nx + ps - 1) >> a.log2_page) - hx);
-        int32_t* row = a.table + (long long)(r0 + x) * a.max_pages + hx;
-        for (int i = tid & 31; i < nd; i += 32) row[i] = a.free_pages[pg[x] + i];
-      }
-    }
-    const long long e1 = min(s1, base_t + ct);
-    for (long long i = max(s0, base_t) + tid; i < e1; i += blockDim.x) {
-      int lo = 0, hi = nu;
+    // A warp has 32 V slots at a time: lane l the pairs (V > 1) at 2 l + 64 k, so that a store
+    // instruction covers 512 contiguous bytes
+    constexpr int P = V > 1 ? 2 : 1;
+    const int b0 = (int)base_t, e1 = (int)min((long long)s1, base_t + ct), lane = tid & 31;
+    for (long long x = max(s0, b0) / (32 * V) * (32 * V) + 32LL * V * (tid >> 5); x < e1; x += V * kUsers) {
+      int lo = 0, hi = nu;  // off[lo] <= the first slot < off[hi]
+      const int f = max((int)x + P * lane, b0);
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (off[mid] <= i) lo = mid; else hi = mid;
+        if (off[mid] <= f) lo = mid; else hi = mid;
       }
-      const long long cx = a.cached[r0 + lo], pos = cx + i - off[lo];
-      const long long hx = (cx + ps - 1) >> a.log2_page, p = pos >> a.log2_page;
-      const long long id = p < hx ? a.table[(long long)(r0 + lo) * a.max_pages + p]
-                                  : a.free_pages[pg[lo] + p - hx];
-      a.slots[i] = id < 0 ? -1 : (id << a.log2_page) + (pos & (ps - 1));
+#pragma unroll
+      for (int k = 0; k < V / P; ++k) {
+        const int i0 = (int)x + 32 * P * k + P * lane;
+        long long v[P];
+        int pos = 0;
+#pragma unroll
+        for (int y = 0; y < P; ++y) {
+          const int i = i0 + y;
+          const bool mine = i >= b0 && i < e1 && i >= s0;
+          v[y] = -1;
+          if (!mine) continue;
+          const bool go = y > 0 && mine && i - 1 >= b0 && i - 1 >= s0 && i < off[lo + 1];
+          while (off[lo + 1] <= i) ++lo;
+          pos = held[lo] + (i - off[lo]);
+          if (go && (pos & (ps - 1)) != 0) {  // the same page as the pair's first slot
+            v[y] = v[0] < 0 ? -1 : v[0] + 1;
+            continue;
+          }
+          const int p = pos >> a.log2_page, hx = (int)((held[lo] + (long long)ps - 1) >> a.log2_page);
+          int32_t* entry = a.table + (long long)(r0 + lo) * a.max_pages + p;
+          const int id = p < hx ? *entry : a.free_pages[pg[lo] + p - hx];
+          if (p >= hx && (pos & (ps - 1)) == 0) *entry = id;
+          v[y] = id < 0 ? -1 : ((long long)id << a.log2_page) + (pos & (ps - 1));
+        }
+        if (P == 2 && a.wide && i0 >= b0 && i0 >= s0 && i0 + 1 < e1) {
+          *reinterpret_cast<longlong2*>(a.slots + i0) = make_longlong2(v[0], v[P - 1]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < P; ++y)
+            if (i0 + y >= b0 && i0 + y >= s0 && i0 + y < e1) a.slots[i0 + y] = v[y];
+        }
+      }
     }
     base_t += ct;
     base_p += cp;
@@ -143,67 +192,88 @@ __device__ __forceinline__ uint32_t e4m3_code(float y) {
   return (c & 0x7Fu) == 0 ? 0u : c;  // +0 for zero
 }
 
-// One row of K or V per LANES lanes (LANES = d / 8, 16 bytes a lane).
-template <int LANES, bool FP8>
+// Eight bf16 values to E4M3 codes with the row's scale (LANES lanes hold the row).
+template <int LANES>
+__device__ __forceinline__ uint2 quantise(uint4 w, unsigned mask, float* scale) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  float f[8], m = 0.f;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    f[2 * y] = __uint_as_float(u[y] << 16);
+    f[2 * y + 1] = __uint_as_float(u[y] & 0xFFFF0000u);
+    m = fmaxf(m, fmaxf(fabsf(f[2 * y]), fabsf(f[2 * y + 1])));
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o, LANES));
+  const float sc = m > 0.f ? __fdiv_rn(m, kE4m3Max) : 1.0f;
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int y = 0; y < 8; ++y) c[y >> 2] |= e4m3_code(__fdiv_rn(f[y], sc)) << (8 * (y & 3));
+  *scale = sc;
+  return make_uint2(c[0], c[1]);
+}
+
+// One (new position, key head) per LANES = d / 8 lanes, 16 bytes of K and of V each. Bound by
+// reading the rows and writing the cache once; IDX is 32 bits where the rows fit (a 64-bit
+// division a row costs more than its bytes).
+template <int LANES, bool FP8, typename IDX>
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
-  const int lane = threadIdx.x & (LANES - 1);
-  const long long g0 = (blockIdx.x * 256LL + threadIdx.x) / LANES, gs = gridDim.x * (256LL / LANES);
-  const long long rows = a.n * a.Hkv * 2, cap = a.n_pages << a.log2_page;
+  const int lane = threadIdx.x & (LANES - 1), ps = 1 << a.log2_page;
+  const IDX rows = (IDX)a.n * (IDX)a.Hkv, step = (IDX)gridDim.x * (256 / LANES);
+  const long long cap = a.n_pages << a.log2_page;
   const unsigned mask = (LANES == 16 ? 0xffffu : 0xffu) << (threadIdx.x & 31 & ~(LANES - 1));
-  for (long long g = g0; g < rows; g += gs) {
-    const long long i = g / (2 * a.Hkv);
-    const int x = (int)(g - i * (2 * a.Hkv)), v = x >= a.Hkv, h = v ? x - a.Hkv : x;
+  for (IDX x = (IDX)blockIdx.x * (256 / LANES) + threadIdx.x / LANES; x < rows; x += step) {
+    const IDX i = x / (IDX)a.Hkv;
+    const int h = (int)(x - i * (IDX)a.Hkv);
     const long long slot = a.slots[i];
+    const uint4 kw = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.K + (long long)i * a.k_stride + h * (LANES * 8))[lane];
+    const uint4 vw = reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.V + (long long)i * a.v_stride + h * (LANES * 8))[lane];
     if (slot < 0 || slot >= cap) continue;
-    const __nv_bfloat16* src = (v ? (const __nv_bfloat16*)a.V + i * a.v_stride
-                                  : (const __nv_bfloat16*)a.K + i * a.k_stride) + h * (LANES * 8);
-    const uint4 w = reinterpret_cast<const uint4*>(src)[lane];
-    const long long row = ((((slot >> a.log2_page) * a.Hkv) + h) << a.log2_page) +
-                          (slot & ((1 << a.log2_page) - 1));
+    const long long row = (((slot >> a.log2_page) * a.Hkv + h) << a.log2_page) + (slot & (ps - 1));
     if (!FP8) {
-      reinterpret_cast<uint4*>(v ? a.v_cache : a.k_cache)[row * LANES + lane] = w;
+      reinterpret_cast<uint4*>(a.k_cache)[row * LANES + lane] = kw;
+      reinterpret_cast<uint4*>(a.v_cache)[row * LANES + lane] = vw;
     } else {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      float f[8], m = 0.f;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        f[2 * y] = __uint_as_float(u[y] << 16);
-        f[2 * y + 1] = __uint_as_float(u[y] & 0xFFFF0000u);
-        m = fmaxf(m, fmaxf(fabsf(f[2 * y]), fabsf(f[2 * y + 1])));
+      float ks, vs;
+      reinterpret_cast<uint2*>(a.k_cache)[row * LANES + lane] = quantise<LANES>(kw, mask, &ks);
+      reinterpret_cast<uint2*>(a.v_cache)[row * LANES + lane] = quantise<LANES>(vw, mask, &vs);
+      if (lane == 0) {
+        a.k_scales[row] = ks;
+        a.v_scales[row] = vs;
       }
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o, LANES));
-      const float sc = m > 0.f ? __fdiv_rn(m, kE4m3Max) : 1.0f;
-      uint32_t c[2] = {0, 0};
-#pragma unroll
-      for (int y = 0; y < 8; ++y) c[y >> 2] |= e4m3_code(__fdiv_rn(f[y], sc)) << (8 * (y & 3));
-      reinterpret_cast<uint2*>(v ? a.v_cache : a.k_cache)[row * LANES + lane] = make_uint2(c[0], c[1]);
-      if (lane == 0) (v ? a.v_scales : a.k_scales)[row] = sc;
     }
   }
+}
+
+template <int LANES, bool FP8>
+void append_t(const PagedAppendArgs& a, cudaStream_t s) {
+  const long long rows = a.n * a.Hkv;
+  long long g = (rows * LANES + 255) / 256;
+  if (g > a.sms * 32LL) g = a.sms * 32LL;
+  if (rows + g * 256 < (1LL << 32)) paged_append_kernel<LANES, FP8, uint32_t><<<(unsigned)g, 256, 0, s>>>(a);
+  else paged_append_kernel<LANES, FP8, long long><<<(unsigned)g, 256, 0, s>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t s) {
-  long long g = (a.n_slots + 4095) / 4096;
+  const int v = a.n_slots > 4LL * a.sms * kUsers ? 8 : 1;
+  long long g = (a.n_slots + v * kUsers - 1) / (v * kUsers);  // at most one pass of the threads each
   if (g < 1) g = 1;
-  if (g > a.sms) g = a.sms;
-  page_tables_kernel<<<(unsigned)g, kTableThreads, 0, s>>>(a);
+  if (g > 4LL * a.sms) g = 4LL * a.sms;
+  if (v == 8) page_tables_kernel<8><<<(unsigned)g, kUsers, 0, s>>>(a);
+  else page_tables_kernel<1><<<(unsigned)g, kUsers, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   if (a.n == 0 || a.n_pages == 0) return cudaSuccess;
-  const int lanes = a.d / 8;
-  long long g = (a.n * a.Hkv * 2 * lanes + 255) / 256;
-  if (g > 148LL * 32) g = 148LL * 32;
   if (a.d == 128) {
-    if (a.fp8) paged_append_kernel<16, true><<<(unsigned)g, 256, 0, s>>>(a);
-    else paged_append_kernel<16, false><<<(unsigned)g, 256, 0, s>>>(a);
+    if (a.fp8) append_t<16, true>(a, s);
+    else append_t<16, false>(a, s);
   } else {
-    if (a.fp8) paged_append_kernel<8, true><<<(unsigned)g, 256, 0, s>>>(a);
-    else paged_append_kernel<8, false><<<(unsigned)g, 256, 0, s>>>(a);
+    if (a.fp8) append_t<8, true>(a, s);
+    else append_t<8, false>(a, s);
   }
   return cudaGetLastError();
 }
