@@ -10,6 +10,7 @@ fallback: if the library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -368,9 +369,21 @@ def _stream(stream, device=None) -> int:
     return s.cuda_stream
 
 
+def _fail(where: str, what: str):
+    raise SketchAttentionError(SA_ERR_INVALID_ARG, f"{where}: {what}")
+
+
 def _require(cond: bool, where: str, what: str) -> None:
     if not cond:
-        raise SketchAttentionError(SA_ERR_INVALID_ARG, f"{where}: {what}")
+        _fail(where, what)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _device(dev: torch.device):
+    """Makes `dev` current for a call; nothing to do when it is (the guard costs microseconds)."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _check_tensor(where: str, name: str, t: torch.Tensor | None, shape: tuple, dtype,
@@ -379,6 +392,10 @@ def _check_tensor(where: str, name: str, t: torch.Tensor | None, shape: tuple, d
     caller's promise, so the torch conveniences check them here."""
     if t is None:
         _require(optional, where, f"{name} is required")
+        return
+    # the usual case first: the messages below cost more than a small call
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.is_contiguous()
+            and (device is None or t.device == device)):
         return
     _require(isinstance(t, torch.Tensor), where, f"{name} must be a tensor")
     _require(tuple(t.shape) == tuple(shape), where,
@@ -390,7 +407,8 @@ def _check_tensor(where: str, name: str, t: torch.Tensor | None, shape: tuple, d
 
 
 def _check_cuda(where: str, X: torch.Tensor) -> None:
-    _require(X.is_cuda, where, f"inputs are on {X.device}; the library runs on CUDA devices only")
+    if not X.is_cuda:
+        _fail(where, f"inputs are on {X.device}; the library runs on CUDA devices only")
 
 
 def _check_forward_inputs(where, X, offsets, P, Wk, Wv):
@@ -735,17 +753,22 @@ def stca_keys_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Te
 def _rows_stride(where: str, name: str, x: torch.Tensor, heads: int, d: int) -> int:
     """Elements between consecutive rows of x [n, heads, d], whose heads are contiguous (a
     slice of a wider projection is fine)."""
-    _require((d == 1 or x.stride(2) == 1) and (heads == 1 or x.stride(1) == d), where,
-             f"{name}: a row's heads must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else heads * d
+    s0, s1, s2 = x.stride()
+    if s2 != 1 or (s1 != d and heads != 1):
+        _fail(where, f"{name}: a row's heads must be contiguous")
+    return s0 if x.shape[0] > 1 else heads * d
 
 
 def _check_heads(where: str, name: str, x, n, d, dev, heads=None) -> None:
-    _require(isinstance(x, torch.Tensor) and x.dim() == 3, where, f"{name} must be [n, heads, d]")
-    _require(x.dtype == torch.bfloat16, where, f"{name} has dtype {x.dtype}, expected torch.bfloat16")
+    if not (isinstance(x, torch.Tensor) and x.dim() == 3):
+        _fail(where, f"{name} must be [n, heads, d]")
+    if x.dtype != torch.bfloat16:
+        _fail(where, f"{name} has dtype {x.dtype}, expected torch.bfloat16")
     want = (n, x.shape[1] if heads is None else heads, d)
-    _require(tuple(x.shape) == want, where, f"{name} has shape {tuple(x.shape)}, expected {want}")
-    _require(x.device == dev, where, f"{name} is on {x.device}, expected {dev}")
+    if x.shape != want:
+        _fail(where, f"{name} has shape {tuple(x.shape)}, expected {want}")
+    if x.device != dev:
+        _fail(where, f"{name} is on {x.device}, expected {dev}")
 
 
 def _scale(scale, d: int) -> float:
@@ -759,8 +782,8 @@ def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
     _check_heads(where, "Q", Q, n_q, d, dev)
     _check_heads(where, "K", K, n_kv, d, dev)
     _check_heads(where, "V", V, n_kv, d, dev, Hkv)
-    _require(Hkv >= 1 and H >= 1 and H % Hkv == 0, where,
-             f"{H} query heads cannot share {Hkv} key heads")
+    if Hkv < 1 or H < 1 or H % Hkv:
+        _fail(where, f"{H} query heads cannot share {Hkv} key heads")
     _require(isinstance(q_offsets, torch.Tensor) and q_offsets.dim() == 1
              and q_offsets.numel() >= 1, where, "q_offsets must be a 1-D tensor with R + 1 entries")
     R = q_offsets.numel() - 1
@@ -795,7 +818,7 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
         out = dict(out)
         _check_tensor(where, "out", out.get("out"), (n_q, H, d), torch.bfloat16, dev)
         _check_tensor(where, "lse", out.get("lse"), (n_q, H), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _device(dev):
         if ws is None:
             nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 0)
             if nb == 0:
@@ -836,7 +859,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
         _check_tensor(where, "dQ", out.get("dQ"), (n_q, H, d), bf, dev)
         _check_tensor(where, "dK", out.get("dK"), (n_kv, Hkv, d), bf, dev)
         _check_tensor(where, "dV", out.get("dV"), (n_kv, Hkv, d), bf, dev)
-    with torch.cuda.device(dev):
+    with _device(dev):
         if ws is None:
             nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 1)
             if nb == 0:
@@ -875,17 +898,18 @@ def _check_cache(where: str, cache: dict, dev) -> tuple[int, int, int, int, int]
     K = cache.get("K") if isinstance(cache, dict) else None
     _require(isinstance(K, torch.Tensor) and K.dim() == 4, where,
              "cache must hold K [n_pages, Hkv, page_size, d]")
-    _require(K.dtype in (torch.bfloat16, torch.float8_e4m3fn), where,
-             f"cache K has dtype {K.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
     fp8 = K.dtype == torch.float8_e4m3fn
-    _check_tensor(where, "cache K", K, tuple(K.shape), K.dtype, dev)
-    _check_tensor(where, "cache V", cache.get("V"), tuple(K.shape), K.dtype, dev)
-    for n in ("k_scales", "v_scales"):
+    if not fp8 and K.dtype != torch.bfloat16:
+        _fail(where, f"cache K has dtype {K.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+    shape = tuple(K.shape)
+    _check_tensor(where, "cache K", K, shape, K.dtype, dev)
+    _check_tensor(where, "cache V", cache.get("V"), shape, K.dtype, dev)
+    for n, name in (("k_scales", "cache k_scales"), ("v_scales", "cache v_scales")):
         if fp8:
-            _check_tensor(where, f"cache {n}", cache.get(n), tuple(K.shape[:3]), torch.float32, dev)
-        else:
-            _require(cache.get(n) is None, where, f"cache {n} belongs to an FP8 cache")
-    return (SA_CODEC_FP8 if fp8 else SA_CODEC_BF16, *K.shape)
+            _check_tensor(where, name, cache.get(n), shape[:3], torch.float32, dev)
+        elif cache.get(n) is not None:
+            _fail(where, f"{name} belongs to an FP8 cache")
+    return (SA_CODEC_FP8 if fp8 else SA_CODEC_BF16, *shape)
 
 
 def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -921,7 +945,7 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
            "free_used": torch.empty(1, dtype=i64, device=dev)}
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
+    with _device(dev):
         st = sa_page_tables(_ptr(cached_lens), _ptr(new_lens), R, int(page_size), _ptr(free_pages),
                             free_pages.numel(), _ptr(free_used), _ptr(block_table),
                             block_table.shape[1], int(n_slots), _ptr(out["slots"]),
@@ -947,7 +971,7 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
     _check_tensor(where, "slots", slots, (K.shape[0],), torch.int64, dev)
     _check_cuda(where, K)
     ks, vs = _rows_stride(where, "K", K, Hkv, d), _rows_stride(where, "V", V, Hkv, d)
-    with torch.cuda.device(dev):
+    with _device(dev):
         st = sa_paged_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), K.shape[0], Hkv, d, fmt,
                              _ptr(cache["K"]), _ptr(cache["V"]), _ptr(cache["k_scales"]),
                              _ptr(cache["v_scales"]), n_pages, page_size, _stream(stream, dev))
@@ -967,8 +991,8 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     dev, (R, H, d) = Q.device, Q.shape
     fmt, n_pages, Hkv, page_size, cd = _check_cache(where, cache, dev)
     _check_heads(where, "Q", Q, R, cd, dev)
-    _require(Hkv >= 1 and H >= 1 and H % Hkv == 0, where,
-             f"{H} query heads cannot share {Hkv} key heads")
+    if Hkv < 1 or H < 1 or H % Hkv:
+        _fail(where, f"{H} query heads cannot share {Hkv} key heads")
     _require(isinstance(block_table, torch.Tensor) and block_table.dim() == 2, where,
              "block_table must be [R, max_pages]")
     _check_tensor(where, "block_table", block_table, (R, block_table.shape[1]), torch.int32, dev)
@@ -977,7 +1001,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     qs = _rows_stride(where, "Q", Q, H, d)
     out = {"out": torch.empty(R, H, d, device=dev, dtype=torch.bfloat16),
            "lse": torch.empty(R, H, device=dev, dtype=torch.float32)}
-    with torch.cuda.device(dev):
+    with _device(dev):
         if ws is None:
             nb = sa_paged_attn_workspace_size(R, H, Hkv, d)
             if nb == 0:

@@ -8,6 +8,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "sa_common.cuh"
 #include "sa_internal.h"
 
@@ -130,6 +132,27 @@ struct CrossGeo {
 // 64 columns x box_heads x box_rows, 128B swizzle. n = 0 (nothing will be read): one row.
 bool tmap_heads(CUtensorMap* m, const void* base, long long n, int heads, int d, long long stride,
                 int box_heads, int box_rows);
+
+// Dynamic shared memory of a kernel, set on its first launch on a device; regs > 0: the build must
+// have given the kernel at least as many registers (setmaxnreg.inc waits for what the launch
+// does not hold).
+template <auto kern>
+cudaError_t prepare_kernel(size_t smem, int regs = 0) {
+  static std::atomic<uint64_t> done{0};  // one bit a device
+  int id = 0;
+  cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return e;
+  if (id < 64 && ((done.load(std::memory_order_acquire) >> id) & 1u)) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if (fa.numRegs < regs) return cudaErrorInvalidConfiguration;
+  }
+  if (id < 64) done.fetch_or(1ull << id, std::memory_order_release);
+  return cudaSuccess;
+}
 
 // A launch that may start while the grid before it in the stream drains: the kernel calls
 // griddep_wait() before it touches memory.

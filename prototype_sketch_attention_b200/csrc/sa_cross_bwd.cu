@@ -649,12 +649,8 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.budget = kDefaultWaitBudget;
   constexpr size_t smem = 1024 + BSmem<D>::oBars + sizeof(BBars);
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(cross_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = prepare_kernel<cross_bwd_kernel<D>>(smem, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, cross_bwd_kernel<D>)) != cudaSuccess) return e;
-  if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;  // see the register split
   const long long ctas = p.kv_ctas + geo.pair_tiles * 2 * (a.H / geo.pg) * geo.splits;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;

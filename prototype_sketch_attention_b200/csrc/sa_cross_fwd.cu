@@ -504,12 +504,8 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.budget = kDefaultWaitBudget;
   constexpr size_t smem = 1024 + FSmem<D>::oBars + sizeof(FBars);
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = prepare_kernel<cross_fwd_kernel<D>>(smem, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, cross_fwd_kernel<D>)) != cudaSuccess) return e;
-  if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;  // see the split
   const dim3 grid((unsigned)(geo.pair_tiles * (a.H / geo.pg)), (unsigned)geo.splits);
   if ((e = launch_dependent(cross_fwd_kernel<D>, grid, dim3(kThreads), smem, s, tq, tk, tv, p)) != cudaSuccess)
     return e;

@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -206,10 +207,16 @@ sa_status cuda_status(cudaError_t e) {
 }  // namespace
 
 int device_sms(int* sms) {
+  static std::atomic<int> known[64];  // by device: its SM count, once it is known to be an sm_100
+  int id = 0;
+  if (cudaGetDevice(&id) != cudaSuccess) return SA_ERR_NO_DEVICE;
+  if (id < 64 && (*sms = known[id].load(std::memory_order_relaxed)) > 0) return SA_OK;
   Device dev;
   const sa_status st = current_device(&dev);
-  if (st == SA_OK) *sms = dev.sms;
-  return st;
+  if (st != SA_OK) return st;
+  *sms = dev.sms;
+  if (id < 64) known[id].store(dev.sms, std::memory_order_relaxed);
+  return SA_OK;
 }
 
 }  // namespace sa

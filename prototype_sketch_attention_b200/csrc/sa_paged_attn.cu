@@ -887,16 +887,15 @@ cudaError_t launch_t(const PagedAttnArgs& a, PagedParams& p, cudaStream_t s) {
   if (!tmap_cache(&tk, rows ? a.k_cache : a.Q, rows ? rows : 1, D, FP8, box) ||
       !tmap_cache(&tv, rows ? a.v_cache : a.Q, rows ? rows : 1, D, FP8, box))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, FP8, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  cudaError_t e = cross::prepare_kernel<paged_attn_kernel<D, FP8, NT>>(L::kSmem);
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, FP8, NT><<<p.ctas, L::kWarps * 32, L::kSmem, s>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const bool sliced = (long long)a.R * p.subs * 8 <= p.ctas;  // items of more than eight parts
   auto join = sliced ? paged_join_kernel<D, FP8, NT, true> : paged_join_kernel<D, FP8, NT, false>;
   const size_t join_smem = (size_t)p.ctas * 2 * 8 * NT * sizeof(float);
-  if ((e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)join_smem)) !=
-      cudaSuccess)
+  if ((e = sliced ? cross::prepare_kernel<paged_join_kernel<D, FP8, NT, true>>(join_smem)
+                  : cross::prepare_kernel<paged_join_kernel<D, FP8, NT, false>>(join_smem)) != cudaSuccess)
     return e;
   return cross::launch_dependent(join, dim3((unsigned)p.ctas, sliced ? D / 16 : 1), dim3(512), join_smem, s,
                                  p);
