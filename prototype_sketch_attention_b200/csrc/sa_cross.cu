@@ -76,6 +76,7 @@ __device__ __forceinline__ void schedule_block(const int64_t* __restrict__ qoff,
     } else {
       hdr->total_tiles = base;
       hdr->status = bad ? SA_ERR_BAD_OFFSETS : SA_OK;
+      hdr->pad[1] = 0;  // the backward's item counter
     }
   }
 }
@@ -113,12 +114,130 @@ __device__ __forceinline__ void stats_rows(const CrossArgs& a, int pg, long long
   }
 }
 
-__global__ void __launch_bounds__(1024) cross_schedule_kernel(const int64_t* qoff, const int64_t* koff, int R,
-                                                              long long n_q, long long n_kv, int pair_tokens,
-                                                              WsHeader* hdr, cross::Tile* qtiles,
-                                                              cross::Tile* ktiles) {
+// The forward's schedule, one block. An item is a query tile of one head group; its cost in
+// half steps is 2 per key tile (1 when the rows fit in one 128-row tile) and a constant for
+// its start and end. CTA b starts where the items' costs, in order, reach b / CTAs of their sum,
+// rounded to an even key tile, or (cuts = false) to the nearer end of the item.
+__global__ void __launch_bounds__(1024)
+cross_schedule_kernel(const int64_t* __restrict__ qoff, const int64_t* __restrict__ koff, int R, long long n_q,
+                      long long n_kv, int tokens, int groups, int ctas, bool cuts, WsHeader* hdr,
+                      cross::Tile* __restrict__ tiles, long long* __restrict__ costs,
+                      cross::Start* __restrict__ starts) {
   griddep_launch_dependents();
-  schedule_block(qoff, koff, R, n_q, n_kv, pair_tokens, hdr, qtiles, ktiles);
+  __shared__ int first[1025], part[32], keys[1024];
+  __shared__ long long before[1024], cpart[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int bad = 0;
+  for (int u = tid; u < R; u += 1024)
+    if (qoff[u + 1] < qoff[u] || koff[u + 1] < koff[u]) bad = 1;
+  if (tid == 0 && (qoff[0] != 0 || koff[0] != 0 || qoff[R] > n_q || koff[R] > n_kv)) bad = 1;
+  bad = __syncthreads_or(bad);
+  auto cost_of = [](int nkt, bool two) { return two ? 2 * nkt + 4 : nkt + 3; };
+  int base = 0;
+  long long cost = 0;
+  if (!bad) {
+    for (int u0 = 0; u0 < R; u0 += 1024) {
+      const int u = u0 + tid, nu = min(1024, R - u0);
+      int n = 0, nkt = 0;
+      long long c = 0;
+      if (u < R) {
+        const int lq = (int)(qoff[u + 1] - qoff[u]);
+        n = (lq + 2 * tokens - 1) / (2 * tokens);
+        nkt = (int)((koff[u + 1] - koff[u] + 127) / 128);
+        if (n > 0) c = (long long)(n - 1) * cost_of(nkt, true) + cost_of(nkt, lq - (n - 1) * 2 * tokens > tokens);
+      }
+      int x = n;  // inclusive prefix sums over the block
+      long long y = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, x, o);
+        const long long w = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+          x += v;
+          y += w;
+        }
+      }
+      if (lane == 31) {
+        part[warp] = x;
+        cpart[warp] = y;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        int v = part[lane];
+        long long w = cpart[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v1 = __shfl_up_sync(0xffffffffu, v, o);
+          const long long w1 = __shfl_up_sync(0xffffffffu, w, o);
+          if (lane >= o) {
+            v += v1;
+            w += w1;
+          }
+        }
+        part[lane] = v;
+        cpart[lane] = w;
+      }
+      __syncthreads();
+      first[tid + 1] = x + (warp ? part[warp - 1] : 0);
+      before[tid] = cost + y - c + (warp ? cpart[warp - 1] : 0);
+      keys[tid] = nkt;
+      if (tid == 0) first[0] = 0;
+      __syncthreads();
+      const int total = first[nu];
+      for (int i = tid; i < total; i += 1024) {
+        int lo = 0, hi = nu;  // first[lo] <= i < first[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first[mid] <= i) lo = mid; else hi = mid;
+        }
+        const int k = i - first[lo];
+        tiles[base + i] = cross::Tile{u0 + lo, k};
+        costs[base + i] = before[lo] + (long long)k * cost_of(keys[lo], true);
+      }
+      base += total;
+      cost += cpart[31];
+      __syncthreads();
+    }
+  }
+  if (tid == 0) {
+    hdr->total_tiles = base;
+    hdr->status = bad ? SA_ERR_BAD_OFFSETS : SA_OK;
+    costs[base] = cost;
+    starts[0] = cross::Start{0, 0, 0, 0};
+    starts[ctas] = cross::Start{base, 0, 0, 0};
+  }
+  __syncthreads();
+  const long long all = cost * groups;
+  for (int b = tid; b < ctas && base > 0; b += 1024) {
+    if (b == 0) continue;
+    const long long at = all * b / ctas;
+    int lo = 0, hi = base;  // the tile whose items hold boundary b
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (costs[mid] * groups <= at) lo = mid; else hi = mid;
+    }
+    const int c = (int)(costs[lo + 1] - costs[lo]);
+    const cross::Tile tl = tiles[lo];
+    const int nkt = (int)((koff[tl.user + 1] - koff[tl.user] + 127) / 128);
+    const bool two = qoff[tl.user + 1] - qoff[tl.user] - (long long)tl.index * 2 * tokens > tokens;
+    const long long in = at - costs[lo] * groups;
+    cross::Start s{lo, (int)(in / c), (int)(in % c), 0};
+    s.key = max(0, two ? (s.key - 4) / 2 : s.key - 3);
+    if (cuts) {
+      s.key = (s.key + 1) / 2 * 2;
+      if (s.key > nkt - 2) s.key = nkt;
+    } else {
+      s.key = 2 * s.key >= nkt ? nkt : 0;
+    }
+    if (s.key >= nkt) {  // the next item
+      s.key = 0;
+      if (++s.group == groups) {
+        s.group = 0;
+        ++s.tile;
+      }
+    }
+    starts[b] = s;
+  }
 }
 
 // The backward's: blocks 0 and 1 the schedule, the others lse2 and delta.
@@ -157,6 +276,8 @@ cross::CrossGeo geometry(int R, long long n_q, long long n_kv, int H, int Hkv, i
   const long long most = R > 0 ? n_kv / R / 512 : 1;
   if (s > most) s = most;
   g.splits = s < 1 ? 1 : (int)s;
+  g.ctas = sms;
+  g.cuts = ctas < 8LL * sms;  // with more items a CTA than that, whole ones are even enough
   return g;
 }
 
@@ -188,10 +309,16 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
   q.hdr = take(sizeof(WsHeader));
   q.qtiles = take((size_t)g.pair_tiles * sizeof(cross::Tile));
   q.ktiles = take((size_t)g.key_tiles * sizeof(cross::Tile));
-  if (backward) q.stats = take((size_t)n_q * H * sizeof(float2));
-  if (g.splits > 1) {
-    q.part_o = take((size_t)g.splits * n_q * H * d * sizeof(float));
-    if (!backward) q.part_lse = take((size_t)g.splits * n_q * H * sizeof(float));
+  if (backward) {
+    q.stats = take((size_t)n_q * H * sizeof(float2));
+    if (g.splits > 1) q.part_o = take((size_t)g.splits * n_q * H * d * sizeof(float));
+  } else {
+    q.costs = take((size_t)(g.pair_tiles + 1) * sizeof(long long));
+    q.starts = take((size_t)(g.ctas + 1) * sizeof(cross::Start));
+    if (g.cuts) {
+      q.part_o = take((size_t)2 * g.ctas * 256 * d * sizeof(float));
+      q.part_lse = take((size_t)2 * g.ctas * 256 * sizeof(float));
+    }
   }
   q.total = o;
   if (p) *p = q;
@@ -201,10 +328,10 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
 cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
-  cross_schedule_kernel<<<2, 1024, 0, s>>>(
-      a.qoff, a.koff, a.R, a.n_q, a.n_kv, 256 / g.pg, reinterpret_cast<WsHeader*>(ws + a.plan.hdr),
-      reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
-      reinterpret_cast<cross::Tile*>(ws + a.plan.ktiles));
+  cross_schedule_kernel<<<1, 1024, 0, s>>>(
+      a.qoff, a.koff, a.R, a.n_q, a.n_kv, 128 / g.pg, a.H / g.pg, g.ctas, g.cuts,
+      reinterpret_cast<WsHeader*>(ws + a.plan.hdr), reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
+      reinterpret_cast<long long*>(ws + a.plan.costs), reinterpret_cast<cross::Start*>(ws + a.plan.starts));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || g.pair_tiles == 0) return e;
   CrossArgs b = a;

@@ -30,16 +30,38 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]: A is [128 lanes] x bf16 pairs along the columns.
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// The issuing thread has about 64 clocks for an MMA of 128 x 128 x 16, so descriptors are kept as
+// a low word, to which offsets are added (the address field does not carry), and a constant
+// high word, and the accumulate flag is part of the instruction.
+// kAcc: 1 accumulate, 0 overwrite.
+template <int kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.u32 p, %5, 1;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(kAcc)
       : "memory");
 }
+// A in TMEM: [128 lanes] x bf16 pairs along the columns
+template <int kAcc>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.eq.u32 p, %5, 1;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "n"(kAcc)
+      : "memory");
+}
+// Low and high words of the descriptors of 128B-swizzled operands of 128-row boxes: K-major
+// (leading offset unused), and MN-major (64-column boxes kBox apart).
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return (addr >> 4) | ((uint32_t)(kBox >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kSwizzle128B << 29);
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -59,9 +81,61 @@ __device__ __forceinline__ void tc_wait_st() {
 }
 
 // Byte offset >> 4 of K step ks (16 of 128 or 64 columns) within a K-major operand made of
-// 64-column boxes.
-__device__ __forceinline__ uint64_t kstep(int ks) {
-  return (uint64_t)((((ks >> 2) * kBox) + (ks & 3) * 32) >> 4);
+// 64-column boxes, and of 16 rows within an MN-major one.
+__host__ __device__ constexpr uint32_t kstep(int ks) {
+  return (uint32_t)((((ks >> 2) * kBox) + (ks & 3) * 32) >> 4);
+}
+__host__ __device__ constexpr uint32_t mn_step(int ks) { return (uint32_t)((ks * 2048) >> 4); }
+
+// D = A B^T over D_ columns, both K-major in shared memory.
+template <int D_>
+__device__ __forceinline__ void product_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc) {
+  mma_ss<0>(d_tmem, a, b, kDescHi, idesc);
+#pragma unroll
+  for (int ks = 1; ks < D_ / 16; ++ks) mma_ss<1>(d_tmem, a + kstep(ks), b + kstep(ks), kDescHi, idesc);
+}
+
+// A place in a ring of N stages and the parity of its use.
+template <int N>
+struct RingPos {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Regroups a warp's 32 x 32 words (lane = row, register = column) so that register group s of
+// lane l holds row 4 s + (l mod 4), columns 4 (l / 4) .. + 3: a store of a group by the warp covers
+// four rows x 128 contiguous bytes (a row a lane would cost eight times the lines).
+template <int LB, int GB>
+__device__ __forceinline__ void regroup_step(uint32_t (&v)[32], int lane) {
+  const bool hi = (lane >> LB) & 1;
+#pragma unroll
+  for (int gi = 0; gi < 8; ++gi) {
+    if ((gi >> GB) & 1) continue;
+    const int gj = gi | (1 << GB);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t send = hi ? v[4 * gi + c] : v[4 * gj + c];
+      const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, 1 << LB);
+      if (hi) v[4 * gi + c] = recv; else v[4 * gj + c] = recv;
+    }
+  }
+}
+__device__ __forceinline__ void regroup(uint32_t (&v)[32], int lane) {
+  regroup_step<4, 2>(v, lane);
+  regroup_step<3, 1>(v, lane);
+  regroup_step<2, 0>(v, lane);
 }
 
 // The keep bits of 128 rows from row0 on: rows at or past `end` and rows whose mask byte is 0
@@ -120,12 +194,19 @@ struct Tile {
   int user, index;
 };
 
+// Where a CTA of the forward starts: query tile, head group, key tile.
+struct Start {
+  int tile, group, key, pad;
+};
+
 // Launch geometry, from the sizes that the host knows (lengths live on the device).
 struct CrossGeo {
   int pg;                // heads packed into a tile
   long long pair_tiles;  // bound on the 256-row query tiles of all users
   long long key_tiles;   // bound on the 128-row key tiles of all users
-  int splits;            // forward: CTAs that share a query tile's keys
+  int splits;            // backward: CTAs that share a query tile's keys
+  int ctas;              // forward: CTAs, and whether their boundaries may cut an item
+  bool cuts;
 };
 
 // 3-D tensor map over bf16 rows of heads [n, heads, d], rows `stride` elements apart: boxes of

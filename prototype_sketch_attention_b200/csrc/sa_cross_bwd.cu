@@ -5,24 +5,28 @@
 // dQ sums over keys, dK and dV over queries and over the heads that share the key head. One
 // pass that makes all three would have to add a 64 KB fp32 block of dQ per pair of tiles in global
 // memory (about 6,000 clocks of L2 reductions on this GPU against 2,560 of tensor work, and an
-// order that changes from run to run). So the grid has two kinds of CTA, each of which owns its
-// output and keeps it in TMEM, at 7 products a pair of tiles in place of 5 and no atomics:
-//   dK/dV CTA: a tile of 128 keys of one key head walks the user's packed query tiles (of every
+// order that changes from run to run). So there are two kinds of item, each of which owns its
+// output and keeps it in TMEM, at 7 products a pair of tiles in place of 5 and no atomics on data:
+//   dK/dV: a tile of 128 keys of one key head against the user's packed query tiles (of every
 //     head group that shares it). S^T = K Q^T and dP^T = V dO^T put keys on the TMEM lanes,
 //     so P^T and dS^T, written as bf16 over S^T and dP^T, are the A operands in place:
 //     dV += P^T dO, dK += dS^T Q. The rows' lse2 and delta run along the columns and come from
 //     shared memory as broadcasts.
-//   dQ CTA: a tile of 128 packed query rows walks the user's key tiles: S = Q K^T (two
-//     buffers), dP = dO V^T, dS over S, dQ += dS K. When there are fewer such CTAs than SMs and
+//   dQ: a tile of 128 packed query rows against the user's key tiles: S = Q K^T (two
+//     buffers), dP = dO V^T, dS over S, dQ += dS K. When there are fewer such items than SMs and
 //     many keys, `splits` of them share a tile and leave fp32 partials, summed in order.
+// One CTA per SM takes items from a counter (which CTA computes an item does not change it) and
+// runs through them without a stop: an item's own tiles, first loads and first products overlap
+// the rows' writing of the one before. (A CTA per item: 12,000 clocks an item exposed, as much as
+// four steps; 40 x 300 x 10K, 8 heads: 2.23 ms against 2.25 before: see the table of cases.)
 // Roles (384 threads): warp 0 TMA, warp 1 TMEM allocation and every MMA, warp 2 hands tiles on:
 // it zeroes the rows that an MMA would multiply by 0 but must not read (dropped keys, rows past
-// the user's end), and loads lse2 and delta; warps 4-11 two warpgroups for the elementwise
-// step, 64 columns each, one thread per row. Within a CTA the tensor pipe runs ahead of the
+// the user's end), and loads lse2 and delta; warp 3 takes the items; warps 4-11 two warpgroups for
+// the elementwise step, 64 columns each, one thread per row. The tensor pipe runs ahead of the
 // elementwise step: dK/dV: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1) | ..., so the exponentials of
 // tile i + 1 run while dK(i) and dP(i + 1) do; dQ: S(j + 1) while tile j is in the elementwise
 // step, then dP(j + 1), dQ(j), S(j + 2).
-// Bound at d = 128: 2,048 tensor clocks a pair of tiles in a dK/dV CTA, 1,536 in a dQ CTA, 1,024
+// Bound at d = 128: 2,048 tensor clocks a pair of tiles for dK/dV, 1,536 for dQ, 1,024
 // clocks of exponentials in both.
 #include <cmath>
 
@@ -37,25 +41,36 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsElem = 216;  // setmaxnreg draws on the launch's
 static_assert(128 * kRegsControl + 256 * kRegsElem <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
+// TMEM columns: dK/dV items: S^T 0, dP^T 128, dV 256, dK 384; dQ items: S 0 and 128, dP 256, dQ 384
+constexpr uint32_t kColAcc = 256;  // from here on: what an epilogue reads, or a dQ item's dP
 
 template <int D>
 struct BSmem {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTile = kBoxes * kBox;
-  static constexpr int kNS = D == 128 ? 5 : 8;  // ring stages of a dQ CTA
-  static constexpr int kNSKv = kNS - 1;         // and of a dK/dV CTA, which has (lse2, delta) in the last
-  static constexpr int oA = 0;                  // the CTA's own tile: K, V (dK/dV) or Q, dO (dQ)
+  static constexpr int kNS = D == 128 ? 4 : 8;  // ring stages
+  static constexpr int oA = 0;                  // the item's own tiles: K, V (dK/dV) or Q, dO (dQ)
   static constexpr int oRing = 2 * kTile;       // Q_i, dO_i, ... or K_j, V_j, ...
-  static constexpr int oStat = oRing + kNSKv * kTile;  // 4 x 128 (lse2, delta)
-  static constexpr int oBars = oRing + kNS * kTile;
-  static_assert(4 * 128 * 8 <= kTile, "the statistics fit in one stage");
+  static constexpr int oStat = oRing + kNS * kTile;  // 4 x (128 of -lse2, 128 of -delta)
+  static constexpr int oItems = oStat + 4 * 256 * 4;
+  static constexpr int oBars = oItems + 2 * 32;
 };
 
 struct BBars {
-  uint64_t own, full[8], empty[8];
-  uint64_t ready[8];    // by tile number mod 8: fewer tile pairs than that fit in the ring
-  uint64_t s_full[2], dp_full, p_full, ds_full, done;
+  uint64_t own, own_empty, full[8], empty[8];
+  uint64_t ready[8];    // by step mod 8: fewer tile pairs than that fit in the ring
+  uint64_t s_full[2], dp_full, p_full, ds_full, done, acc_free;
+  uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
+};
+
+enum : int { kEnd = -1, kDkv = 0, kDq = 1 };
+struct Item {
+  int kind, n;   // n: steps (query tiles of every sharing head group, or key tiles)
+  int t0, t1;    // dK/dV: the user's query rows; dQ: the tile's first token, the user's end
+  int k0, k1;    // the first key row, the user's end
+  int h;         // key head (dK/dV) or head group (dQ)
+  int aux;       // dK/dV: query tiles per head group; dQ: the split
 };
 
 struct BwdParams {
@@ -68,7 +83,7 @@ struct BwdParams {
   const float2* stats;     // [H / PG][n_q PG] (lse2, delta)
   int H, Hkv, G, PG;
   int splits;
-  long long kv_ctas;       // CTAs [0, kv_ctas) are dK/dV CTAs
+  bool dq_first;           // the longer kind of item first
   float c, scale;
   __nv_bfloat16 *dQ, *dK, *dV;
   float* part;             // [splits][n_q, H, D] (splits > 1)
@@ -76,474 +91,58 @@ struct BwdParams {
   long long budget;
 };
 
-__device__ __forceinline__ uint64_t mn_step(int ks) { return (uint64_t)((ks * 2048) >> 4); }
+constexpr int kConsumers = 11;  // warps that read an item: all but warp 3
 
-// A row of D fp32 TMEM columns, times f, to bf16 (zero: what the accumulator holds is not used).
-template <int COLS>
-__device__ __forceinline__ void write_row(uint32_t taddr, bool have, bool write, bool zero, float f,
-                                          __nv_bfloat16* row) {
+// A warp's 32 rows x COLS fp32 TMEM columns, times f, to bf16: row i (of the warp's) goes to
+// row_at(i), or nowhere when that is null. `zero` (of this lane's row): 0 whatever the accumulator
+// holds. `read` is called once the accumulator has been read.
+template <int COLS, typename RowAt, typename Read>
+__device__ __forceinline__ void write_rows(uint32_t taddr, bool have, bool zero, float f, RowAt row_at,
+                                           Read read, int lane) {
+  constexpr int kStep = COLS < 64 ? COLS : 64;
 #pragma unroll 1
-  for (int x = 0; x < COLS; x += 16) {
-    uint32_t o[16];
-    if (have) {
-      tmem_ld16(taddr + x, o);
-      tmem_wait16(o);
-    }
-    if (write) {
-      uint32_t pk[8];
+  for (int x = 0; x < COLS; x += kStep) {
+    uint32_t v[32];
 #pragma unroll
-      for (int y = 0; y < 8; ++y)
-        pk[y] = zero || !have ? 0u
-                              : cvt_bf16x2(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
-      *reinterpret_cast<uint4*>(row + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      *reinterpret_cast<uint4*>(row + x + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- dK and dV of a key tile
-template <int D>
-__device__ __forceinline__ void dkv_cta(const CUtensorMap* tmap_q, const CUtensorMap* tmap_do,
-                                        const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
-                                        const BwdParams& a, uint8_t* smem, uint32_t tmem) {
-  using L = BSmem<D>;
-  constexpr int NS = L::kNSKv;
-  constexpr uint32_t cS = 0, cP = 128, cDV = 256, cDK = 384;
-  const uint32_t sbase = smem_u32(smem);
-  BBars* bars = reinterpret_cast<BBars*>(smem + L::oBars);
-  int* status = &a.hdr->status;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  const long long g = blockIdx.x / a.Hkv;
-  const int hk = (int)(blockIdx.x - g * a.Hkv), tokens = 128 / a.PG;
-  const bool work = g < a.hdr->pad[0];
-  int k0 = 0, k1 = 0, q0 = 0, q1 = 0, nqt = 0, n = 0;
-  if (work) {
-    const Tile tl = a.ktiles[g];
-    k0 = (int)a.koff[tl.user] + tl.index * 128;
-    k1 = (int)a.koff[tl.user + 1];
-    q0 = (int)a.qoff[tl.user];
-    q1 = (int)a.qoff[tl.user + 1];
-    nqt = (q1 - q0 + tokens - 1) / tokens;
-    n = nqt * (a.G / a.PG);  // (head group, query tile) steps
-  }
-  const int hu0 = hk * (a.G / a.PG);
-
-  if (warp == 0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (lane == 0 && n > 0) {
-      const uint32_t ob = smem_u32(&bars->own);
-      mbar_arrive_expect_tx(ob, 2 * L::kTile);
-      for (int b = 0; b < L::kBoxes; ++b) {
-        tma_load_3d(sbase + L::oA + b * kBox, tmap_k, b * 64, hk, k0, ob);
-        tma_load_3d(sbase + L::oA + L::kTile + b * kBox, tmap_v, b * 64, hk, k0, ob);
+    for (int h = 0; h < kStep / 32; ++h) {
+      uint32_t o[32];
+      if (have) {
+        tmem_ld32_raw(taddr + x + 32 * h, o);
+        tmem_wait_tie(o);
       }
-      int x = 0, grp = 0, qt = 0;
-      for (; x < 2 * n; ++x) {
-        const int st = x % NS;
-        if (!mbar_wait(smem_u32(&bars->empty[st]), (uint32_t)(((x / NS) & 1) ^ 1), status, a.budget)) break;
-        const uint32_t fb = smem_u32(&bars->full[st]);
-        mbar_arrive_expect_tx(fb, L::kTile);
-        for (int b = 0; b < L::kBoxes; ++b)
-          tma_load_3d(sbase + L::oRing + st * L::kTile + b * kBox, (x & 1) ? tmap_do : tmap_q, b * 64,
-                      (hu0 + grp) * a.PG, q0 + qt * tokens, fb);
-        if ((x & 1) && ++qt == nqt) {
-          qt = 0;
-          ++grp;
-        }
-      }
-      for (int y = (x > NS ? x - NS : 0); y < x; ++y)
-        mbar_wait_drain(smem_u32(&bars->full[y % NS]), (uint32_t)((y / NS) & 1), a.budget);
-      mbar_wait_drain(ob, 0, a.budget);
+#pragma unroll
+      for (int y = 0; y < 16; ++y)
+        v[16 * h + y] = zero || !have ? 0u
+                                      : cvt_bf16x2(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
     }
-  } else if (warp == 1) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (lane == 0 && n > 0) {
-      const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
-      const uint64_t dk = smem_desc(sbase + L::oA, 16, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(sbase + L::oA + L::kTile, 16, 1024, kSwizzle128B);
-      bool ok = mbar_wait(smem_u32(&bars->own), 0, status, a.budget);
-      auto ring = [&](int x) { return sbase + L::oRing + (x % NS) * L::kTile; };
-      auto scores = [&](int i) {  // S^T = K Q_i^T
-        ok = ok && mbar_wait(smem_u32(&bars->ready[i & 7]), (uint32_t)((i >> 3) & 1), status, a.budget);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t dq = smem_desc(ring(2 * i), 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + cS, dk + kstep(ks), dq + kstep(ks), id_s, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&bars->s_full[0]));
-      };
-      auto dprob = [&](int i) {  // dP^T = V dO_i^T
-        const uint64_t ddo = smem_desc(ring(2 * i + 1), 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + cP, dv + kstep(ks), ddo + kstep(ks), id_s, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&bars->dp_full));
-      };
-      scores(0);
-      if (ok) dprob(0);
-      for (int i = 0; ok && i < n; ++i) {
-        ok = mbar_wait(smem_u32(&bars->p_full), (uint32_t)(i & 1), status, a.budget);
-        if (!ok) break;
-        tc_fence_after();
-        // dV += P^T dO_i; the packed P^T of warpgroup w's queries starts at column 64 w
-        const uint64_t ddo = smem_desc(ring(2 * i + 1), kBox, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_f16_ts(tmem + cDV, tmem + cS + 64 * (ks >> 2) + 8 * (ks & 3), ddo + mn_step(ks), id_o,
-                        (i > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&bars->empty[(2 * i + 1) % NS]));
-        if (i + 1 < n) scores(i + 1);  // overwrites P^T after the MMAs above, in order
-        ok = ok && mbar_wait(smem_u32(&bars->ds_full), (uint32_t)(i & 1), status, a.budget);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t dq = smem_desc(ring(2 * i), kBox, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_f16_ts(tmem + cDK, tmem + cP + 64 * (ks >> 2) + 8 * (ks & 3), dq + mn_step(ks), id_o,
-                        (i > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&bars->empty[(2 * i) % NS]));
-        if (i + 1 < n) dprob(i + 1);
-      }
-      tc_commit(smem_u32(&bars->done));
-      mbar_wait_drain(smem_u32(&bars->done), 0, a.budget);
-    }
-  } else if (warp == 2) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    // ================= lse2 and delta of the tile's rows; rows past the user's end: weight 0,
-    // and zeros in the Q and dO tiles
-    float2* stat = reinterpret_cast<float2*>(smem + L::oStat);
-    int grp = 0, qt = 0;
-    for (int i = 0; i < n; ++i) {
-      const int t = q0 + qt * tokens, rows = min(128, (q1 - t) * a.PG);
-      const float2* src = a.stats + ((long long)(hu0 + grp) * a.n_q + t) * a.PG;
-      float2 v[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        v[y] = lane + 32 * y < rows ? src[lane + 32 * y] : make_float2(INFINITY, 0.f);
-      bool ok = true;
-      for (int x = 2 * i; x < 2 * i + 2; ++x)
-        ok = ok && mbar_wait_warp(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), status, a.budget);
-      if (!ok) break;
-      if (rows < 128) {
-        uint32_t keep[4];
+    if (x + kStep == COLS) read();
+    if (kStep < 64) {  // 64 bytes a row
+      __nv_bfloat16* p = row_at(lane);
+      if (p) {
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          keep[y] = rows >= 32 * y + 32 ? ~0u : rows > 32 * y ? (1u << (rows - 32 * y)) - 1u : 0u;
-        zero_rows(smem + L::oRing + ((2 * i) % NS) * L::kTile, L::kBoxes, keep, lane);
-        zero_rows(smem + L::oRing + ((2 * i + 1) % NS) * L::kTile, L::kBoxes, keep, lane);
-        fence_proxy_async_smem();
+          reinterpret_cast<uint4*>(p + x)[y] = make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
       }
-      // slot i mod 4 was last read for step i - 4, whose tiles left the ring long ago
+    } else {
+      regroup(v, lane);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) stat[(i & 3) * 128 + lane + 32 * y] = v[y];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ready[i & 7]));
-      if (++qt == nqt) {
-        qt = 0;
-        ++grp;
+      for (int y = 0; y < 8; ++y) {
+        __nv_bfloat16* p = row_at(4 * y + (lane & 3));
+        if (p)
+          *reinterpret_cast<uint4*>(p + x + 8 * (lane >> 2)) =
+              make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
       }
     }
-  } else if (warp == 3) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElem));
-    // ================= elementwise: thread = key row, warpgroup w = queries [64 w, 64 w + 64)
-    const int w = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t ts = tmem + lane_off + cS + 64 * w, tp = tmem + lane_off + cP + 64 * w;
-    const float4* stat = reinterpret_cast<const float4*>(smem + L::oStat);  // two rows each
-    const float c = a.c;
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      if (!mbar_wait_warp(smem_u32(&bars->ready[i & 7]), (uint32_t)((i >> 3) & 1), status, a.budget) ||
-          !mbar_wait_warp(smem_u32(&bars->s_full[0]), (uint32_t)(i & 1), status, a.budget)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const float4* st = stat + (i & 3) * 64 + 32 * w;
-      uint32_t s[2][32];
-      tmem_ld32_raw(ts, s[0]);
-      tmem_ld32_raw(ts + 32, s[1]);
-      tmem_wait_tie(s[0]);
-      tie32(s[1]);
-      uint32_t pk[32];
-#pragma unroll
-      for (int x = 0; x < 32; ++x) {
-        const float4 f = st[x];
-        uint32_t& a0 = s[x >> 4][(2 * x) & 31];
-        uint32_t& a1 = s[x >> 4][(2 * x + 1) & 31];
-        const float p0 = ex2_approx(fmaf(__uint_as_float(a0), c, -f.x));
-        const float p1 = ex2_approx(fmaf(__uint_as_float(a1), c, -f.z));
-        a0 = __float_as_uint(p0);
-        a1 = __float_as_uint(p1);
-        pk[x] = cvt_bf16x2(p0, p1);
-      }
-      tmem_st32(ts, pk);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
-      if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(i & 1), status, a.budget)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t dp[32];
-        tmem_ld32_raw(tp + 32 * h, dp);
-        tmem_wait_tie(dp);
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float4 f = st[16 * h + x];
-          pk[16 * h + x] = cvt_bf16x2(__uint_as_float(s[h][2 * x]) * (__uint_as_float(dp[2 * x]) - f.y),
-                                      __uint_as_float(s[h][2 * x + 1]) * (__uint_as_float(dp[2 * x + 1]) - f.w));
-        }
-      }
-      tmem_st32(tp, pk);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
-    }
-    // ---- warpgroup 0 writes dV, warpgroup 1 dK; a dropped key row gets 0
-    const bool have = ok && n > 0 && mbar_wait_warp(smem_u32(&bars->done), 0, status, a.budget);
-    tc_fence_after();
-    const int j = k0 + r;
-    const bool write = work && j < k1;
-    const bool zero = write && a.mask && a.mask[j] == 0;
-    write_row<D>(tmem + lane_off + (w ? cDK : cDV), have, write, zero, w ? a.scale : 1.f,
-                 (w ? a.dK : a.dV) + ((long long)j * a.Hkv + hk) * D);
   }
 }
 
-// ---------------------------------------------------------------- dQ of a query tile
-template <int D>
-__device__ __forceinline__ void dq_cta(const CUtensorMap* tmap_q, const CUtensorMap* tmap_do,
-                                       const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
-                                       const BwdParams& a, uint8_t* smem, uint32_t tmem) {
-  using L = BSmem<D>;
-  constexpr int NS = L::kNS;
-  constexpr uint32_t cP = 256, cDQ = 384;  // S buffers at 0 and 128
-  const uint32_t sbase = smem_u32(smem);
-  BBars* bars = reinterpret_cast<BBars*>(smem + L::oBars);
-  int* status = &a.hdr->status;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // CTA -> (tile of a pair, head group, split), the group fastest: neighbours share keys in L2
-  const int groups = a.H / a.PG, tokens = 128 / a.PG;
-  long long b = blockIdx.x - a.kv_ctas;
-  const int hu = (int)(b % groups);
-  b /= groups;
-  const int half = (int)(b & 1);
-  b >>= 1;
-  const int split = (int)(b % a.splits);
-  const long long g = b / a.splits;
-  bool work = g < a.hdr->total_tiles;
-  int t0 = 0, t1 = 0, k0 = 0, k1 = 0, n = 0;
-  if (work) {
-    const Tile tl = a.qtiles[g];
-    t0 = (int)a.qoff[tl.user] + (tl.index * 2 + half) * tokens;
-    t1 = (int)a.qoff[tl.user + 1];
-    work = t0 < t1;
-    k0 = (int)a.koff[tl.user];
-    k1 = (int)a.koff[tl.user + 1];
-    const int all = (k1 - k0 + 127) / 128;
-    const int j0 = (int)((long long)all * split / a.splits);
-    n = work ? (int)((long long)all * (split + 1) / a.splits) - j0 : 0;
-    k0 += j0 * 128;
-  }
-  const int hk = hu * a.PG / a.G;
-
-  if (warp == 0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (lane == 0 && n > 0) {
-      const uint32_t ob = smem_u32(&bars->own);
-      mbar_arrive_expect_tx(ob, 2 * L::kTile);
-      for (int bx = 0; bx < L::kBoxes; ++bx) {
-        tma_load_3d(sbase + L::oA + bx * kBox, tmap_q, bx * 64, hu * a.PG, t0, ob);
-        tma_load_3d(sbase + L::oA + L::kTile + bx * kBox, tmap_do, bx * 64, hu * a.PG, t0, ob);
-      }
-      int x = 0;
-      for (; x < 2 * n; ++x) {
-        const int st = x % NS;
-        if (!mbar_wait(smem_u32(&bars->empty[st]), (uint32_t)(((x / NS) & 1) ^ 1), status, a.budget)) break;
-        const uint32_t fb = smem_u32(&bars->full[st]);
-        mbar_arrive_expect_tx(fb, L::kTile);
-        for (int bx = 0; bx < L::kBoxes; ++bx)
-          tma_load_3d(sbase + L::oRing + st * L::kTile + bx * kBox, (x & 1) ? tmap_v : tmap_k, bx * 64, hk,
-                      k0 + 128 * (x >> 1), fb);
-      }
-      for (int y = (x > NS ? x - NS : 0); y < x; ++y)
-        mbar_wait_drain(smem_u32(&bars->full[y % NS]), (uint32_t)((y / NS) & 1), a.budget);
-      mbar_wait_drain(ob, 0, a.budget);
-    }
-  } else if (warp == 1) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (lane == 0 && n > 0) {
-      const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
-      const uint64_t dq = smem_desc(sbase + L::oA, 16, 1024, kSwizzle128B);
-      const uint64_t ddo = smem_desc(sbase + L::oA + L::kTile, 16, 1024, kSwizzle128B);
-      bool ok = mbar_wait(smem_u32(&bars->own), 0, status, a.budget);
-      auto ring = [&](int x) { return sbase + L::oRing + (x % NS) * L::kTile; };
-      auto scores = [&](int j) {  // S = Q K_j^T into buffer j mod 2
-        ok = ok && mbar_wait(smem_u32(&bars->ready[j & 7]), (uint32_t)((j >> 3) & 1), status, a.budget);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t dk = smem_desc(ring(2 * j), 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + 128 * (j & 1), dq + kstep(ks), dk + kstep(ks), id_s, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&bars->s_full[j & 1]));
-      };
-      auto dprob = [&](int j) {  // dP = dO V_j^T
-        const int x = 2 * j + 1;
-        ok = ok && mbar_wait(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), status, a.budget);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t dv = smem_desc(ring(x), 16, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + cP, ddo + kstep(ks), dv + kstep(ks), id_s, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&bars->dp_full));
-        tc_commit(smem_u32(&bars->empty[x % NS]));
-      };
-      scores(0);
-      dprob(0);
-      if (n > 1) scores(1);
-      for (int j = 0; ok && j < n; ++j) {
-        ok = mbar_wait(smem_u32(&bars->ds_full), (uint32_t)(j & 1), status, a.budget);
-        if (!ok) break;
-        tc_fence_after();
-        if (j + 1 < n) dprob(j + 1);  // dP(j) has been read
-        if (!ok) break;
-        const uint64_t dk = smem_desc(ring(2 * j), kBox, 1024, kSwizzle128B);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_f16_ts(tmem + cDQ, tmem + 128 * (j & 1) + 64 * (ks >> 2) + 8 * (ks & 3), dk + mn_step(ks),
-                        id_o, (j > 0 || ks > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&bars->empty[(2 * j) % NS]));
-        if (j + 2 < n) scores(j + 2);  // overwrites dS(j) after the MMAs above, in order
-      }
-      tc_commit(smem_u32(&bars->done));
-      mbar_wait_drain(smem_u32(&bars->done), 0, a.budget);
-    }
-  } else if (warp == 2) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    // ================= K tiles: zero the dropped rows (dS = 0 meets them in dQ)
-    MaskBytes mb;
-    if (n > 0) mb.load(a.mask, k0, k1, lane);
-    for (int j = 0; j < n; ++j) {
-      uint32_t keep[4];
-      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
-      if (j + 1 < n) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
-      const int x = 2 * j;
-      if (!mbar_wait_warp(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), status, a.budget)) break;
-      if (drop) {
-        zero_rows(smem + L::oRing + (x % NS) * L::kTile, L::kBoxes, keep, lane);
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ready[j & 7]));
-    }
-  } else if (warp == 3) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElem));
-    // ================= elementwise: thread = query row, warpgroup w = keys [64 w, 64 w + 64)
-    const int w = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tp = tmem + lane_off + cP + 64 * w;
-    const int t = t0 + r / a.PG;
-    const bool row_ok = work && t < t1;
-    float lse2 = INFINITY, delta = 0.f;
-    if (row_ok) {
-      const float2 f = a.stats[((long long)hu * a.n_q + t) * a.PG + r % a.PG];
-      lse2 = f.x;
-      delta = f.y;
-    }
-    const float c = a.c;
-    bool ok = true;
-    MaskBytes mb;
-    if (n > 0) mb.load(a.mask, k0, k1, lane);
-    for (int j = 0; j < n; ++j) {
-      uint32_t keep[4];
-      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
-      if (j + 1 < n) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
-      const uint32_t kw[2] = {w ? keep[2] : keep[0], w ? keep[3] : keep[1]};
-      const uint32_t ts = tmem + lane_off + 128 * (j & 1) + 64 * w;
-      if (!mbar_wait_warp(smem_u32(&bars->s_full[j & 1]), (uint32_t)((j >> 1) & 1), status, a.budget)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t s[2][32];
-      tmem_ld32_raw(ts, s[0]);
-      tmem_ld32_raw(ts + 32, s[1]);
-      tmem_wait_tie(s[0]);
-      tie32(s[1]);
-#pragma unroll
-      for (int x = 0; x < 64; ++x)
-        s[x >> 5][x & 31] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[x >> 5][x & 31]), c, -lse2)));
-      if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(j & 1), status, a.budget)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t pk[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t dp[32];
-        tmem_ld32_raw(tp + 32 * h, dp);
-        tmem_wait_tie(dp);
-#pragma unroll
-        for (int x = 0; x < 32; ++x)
-          dp[x] = __float_as_uint(__uint_as_float(s[h][x]) * (__uint_as_float(dp[x]) - delta));
-        if (drop) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!((kw[h] >> x) & 1u)) dp[x] = 0u;
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          pk[16 * h + x] = cvt_bf16x2(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]));
-      }
-      tmem_st32(ts, pk);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
-    }
-    // ---- each warpgroup writes half of the columns
-    const bool have = ok && n > 0 && mbar_wait_warp(smem_u32(&bars->done), 0, status, a.budget);
-    tc_fence_after();
-    const long long row = ((long long)t * a.H + hu * a.PG + r % a.PG) * D + w * (D / 2);
-    const uint32_t tq = tmem + lane_off + cDQ + w * (D / 2);
-    if (a.splits == 1) {
-      write_row<D / 2>(tq, have, row_ok, false, a.scale, a.dQ + row);
-    } else {
-      float* po = a.part + (long long)split * a.n_q * a.H * D + row;
-#pragma unroll 1
-      for (int x = 0; x < D / 2; x += 16) {
-        uint32_t o[16];
-        if (have) {
-          tmem_ld16(tq + x, o);
-          tmem_wait16(o);
-        }
-        if (row_ok) {
-#pragma unroll
-          for (int y = 0; y < 16; y += 4)
-            *reinterpret_cast<float4*>(po + x + y) =
-                have ? make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]),
-                                   __uint_as_float(o[y + 2]), __uint_as_float(o[y + 3]))
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-    }
-  }
+__device__ __forceinline__ bool get_item(BBars* bars, const Item* ring, int s, int lane, int* status,
+                                         long long budget, Item* it) {
+  const bool ok = mbar_wait_warp(smem_u32(&bars->item_full[s & 1]), (uint32_t)((s >> 1) & 1), status, budget);
+  *it = ring[s & 1];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s & 1]));
+  return ok && it->kind != kEnd;
 }
 
 template <int D>
@@ -552,24 +151,32 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                  const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ BwdParams a) {
   using L = BSmem<D>;
+  constexpr int NS = L::kNS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
   BBars* bars = reinterpret_cast<BBars*>(smem + L::oBars);
-  const int warp = threadIdx.x >> 5;
+  int* status = &a.hdr->status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->own), 1);
+    mbar_init(smem_u32(&bars->own_empty), 1);
     for (int s = 0; s < 8; ++s) {
       mbar_init(smem_u32(&bars->full[s]), 1);
       mbar_init(smem_u32(&bars->empty[s]), 1);
       mbar_init(smem_u32(&bars->ready[s]), 1);
     }
-    mbar_init(smem_u32(&bars->s_full[0]), 1);
-    mbar_init(smem_u32(&bars->s_full[1]), 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(smem_u32(&bars->s_full[w]), 1);
+      mbar_init(smem_u32(&bars->item_full[w]), 1);
+      mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
+    }
     mbar_init(smem_u32(&bars->dp_full), 1);
     mbar_init(smem_u32(&bars->p_full), 8);
     mbar_init(smem_u32(&bars->ds_full), 8);
     mbar_init(smem_u32(&bars->done), 1);
+    mbar_init(smem_u32(&bars->acc_free), 8);
     fence_mbar_init();
     tma_prefetch_desc(&tmap_q);
     tma_prefetch_desc(&tmap_do);
@@ -585,8 +192,494 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   griddep_wait();  // the schedule, lse2 and delta
-  if (blockIdx.x < a.kv_ctas) dkv_cta<D>(&tmap_q, &tmap_do, &tmap_k, &tmap_v, a, smem, tmem);
-  else dq_cta<D>(&tmap_q, &tmap_do, &tmap_k, &tmap_v, a, smem, tmem);
+
+  Item* items = reinterpret_cast<Item*>(smem + L::oItems);
+  Item it;
+  const int tokens = 128 / a.PG, sharing = a.G / a.PG;  // tokens per tile; head groups of a key head
+
+  if (warp == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    // ================= TMA
+    RingPos<NS> at;
+    int loads = 0, own = 0;
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      if (lane == 0 && it.n > 0) {
+        const bool dkv = it.kind == kDkv;
+        const CUtensorMap *ma = dkv ? &tmap_k : &tmap_q, *mb = dkv ? &tmap_v : &tmap_do;
+        const CUtensorMap *rx = dkv ? &tmap_q : &tmap_k, *ry = dkv ? &tmap_do : &tmap_v;
+        ok = mbar_wait(smem_u32(&bars->own_empty), (uint32_t)((own & 1) ^ 1), status, a.budget);
+        if (ok) {
+          ++own;
+          const uint32_t ob = smem_u32(&bars->own);
+          const int y = dkv ? it.h : it.h * a.PG, z = dkv ? it.k0 : it.t0;
+          mbar_arrive_expect_tx(ob, 2 * L::kTile);
+          for (int b = 0; b < L::kBoxes; ++b) {
+            tma_load_3d(sbase + L::oA + b * kBox, ma, b * 64, y, z, ob);
+            tma_load_3d(sbase + L::oA + L::kTile + b * kBox, mb, b * 64, y, z, ob);
+          }
+        }
+        int grp = 0, qt = 0;
+        for (int x = 0; ok && x < it.n; ++x) {
+          const int y = dkv ? (it.h * sharing + grp) * a.PG : it.h * a.PG / a.G;
+          const int z = dkv ? it.t0 + qt * tokens : it.k0 + 128 * x;
+          for (int v = 0; v < 2; ++v) {
+            ok = ok && mbar_wait(smem_u32(&bars->empty[at.st]), at.ph ^ 1u, status, a.budget);
+            if (!ok) break;
+            const uint32_t fb = smem_u32(&bars->full[at.st]);
+            mbar_arrive_expect_tx(fb, L::kTile);
+            for (int b = 0; b < L::kBoxes; ++b)
+              tma_load_3d(sbase + L::oRing + at.st * L::kTile + b * kBox, v ? ry : rx, b * 64, y, z, fb);
+            at.next();
+            ++loads;
+          }
+          if (++qt == it.aux) {  // (dQ items do not use them)
+            qt = 0;
+            ++grp;
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {
+      for (int x = (loads > NS ? loads - NS : 0); x < loads; ++x)
+        mbar_wait_drain(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), a.budget);
+      if (own > 0) mbar_wait_drain(smem_u32(&bars->own), (uint32_t)((own - 1) & 1), a.budget);
+    }
+  } else if (warp == 1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    // ================= MMAs
+    const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
+    constexpr uint32_t kStage = L::kTile >> 4;
+    const uint32_t own_k = desc_k(sbase + L::oA), ring_k = desc_k(sbase + L::oRing),
+                   ring_mn = desc_mn(sbase + L::oRing);
+    RingPos<NS> at;
+    int own = 0, steps = 0, pcnt = 0;  // items with steps, steps, dK/dV steps before
+    bool ok = true;
+    // acc += A B: A packed in TMEM, warpgroup w's 64 columns from column 64 w on
+    auto accumulate = [&](uint32_t acc, uint32_t pk, uint32_t b, bool first) {
+      if (first) mma_ts<0>(tmem + acc, tmem + pk, b, kDescHi, id_o);
+      else mma_ts<1>(tmem + acc, tmem + pk, b, kDescHi, id_o);
+#pragma unroll
+      for (int ks = 1; ks < 8; ++ks)
+        mma_ts<1>(tmem + acc, tmem + pk + 64 * (ks >> 2) + 8 * (ks & 3), b + mn_step(ks), kDescHi, id_o);
+    };
+    auto after = [](RingPos<NS> x, int k) {
+      for (int i = 0; i < k; ++i) x.next();
+      return x;
+    };
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      if (lane == 0 && it.n > 0) {
+        const int n = it.n;
+        ok = mbar_wait(smem_u32(&bars->own), (uint32_t)(own & 1), status, a.budget);
+        ++own;
+        auto wait_ready = [&](int i) {
+          const int x = steps + i;
+          ok = ok && mbar_wait(smem_u32(&bars->ready[x & 7]), (uint32_t)((x >> 3) & 1), status, a.budget);
+          tc_fence_after();
+        };
+        auto wait_acc = [&]() {  // the accumulators of the item before have been read
+          ok = ok && (s == 0 || mbar_wait(smem_u32(&bars->acc_free), (uint32_t)((s - 1) & 1), status, a.budget));
+          tc_fence_after();
+        };
+        if (it.kind == kDkv) {
+          // own: K, V; ring: Q_i, dO_i
+          auto scores = [&](int i, RingPos<NS> x) {  // S^T = K Q_i^T
+            wait_ready(i);
+            if (!ok) return;
+            product_ss<D>(tmem, own_k, ring_k + x.st * kStage, id_s);
+            tc_commit(smem_u32(&bars->s_full[0]));
+          };
+          auto dprob = [&](int i, RingPos<NS> x) {  // dP^T = V dO_i^T
+            if (!ok) return;
+            product_ss<D>(tmem + 128, own_k + kStage, ring_k + x.st * kStage, id_s);
+            tc_commit(smem_u32(&bars->dp_full));
+            if (i == n - 1) tc_commit(smem_u32(&bars->own_empty));
+          };
+          scores(0, at);
+          dprob(0, after(at, 1));
+          wait_acc();
+          for (int i = 0; ok && i < n; ++i) {
+            const RingPos<NS> q = at, g = after(at, 1), q1 = after(at, 2);
+            ok = mbar_wait(smem_u32(&bars->p_full), (uint32_t)(pcnt & 1), status, a.budget);
+            if (!ok) break;
+            ++pcnt;
+            tc_fence_after();
+            accumulate(kColAcc, 0, ring_mn + g.st * kStage, i == 0);  // dV += P^T dO_i
+            tc_commit(smem_u32(&bars->empty[g.st]));
+            if (i + 1 < n) scores(i + 1, q1);  // overwrites P^T after the MMAs above, in order
+            ok = ok && mbar_wait(smem_u32(&bars->ds_full), (uint32_t)((steps + i) & 1), status, a.budget);
+            if (!ok) break;
+            tc_fence_after();
+            accumulate(384, 128, ring_mn + q.st * kStage, i == 0);    // dK += dS^T Q_i
+            tc_commit(smem_u32(&bars->empty[q.st]));
+            if (i + 1 < n) dprob(i + 1, after(q1, 1));
+            at = q1;
+          }
+        } else {
+          // own: Q, dO; ring: K_j, V_j
+          auto scores = [&](int j, RingPos<NS> x) {  // S = Q K_j^T into buffer j mod 2
+            wait_ready(j);
+            if (!ok) return;
+            product_ss<D>(tmem + 128 * (j & 1), own_k, ring_k + x.st * kStage, id_s);
+            tc_commit(smem_u32(&bars->s_full[j & 1]));
+          };
+          auto dprob = [&](int j, RingPos<NS> x) {  // dP = dO V_j^T
+            ok = ok && mbar_wait(smem_u32(&bars->full[x.st]), x.ph, status, a.budget);
+            if (!ok) return;
+            tc_fence_after();
+            product_ss<D>(tmem + kColAcc, own_k + kStage, ring_k + x.st * kStage, id_s);
+            tc_commit(smem_u32(&bars->dp_full));
+            tc_commit(smem_u32(&bars->empty[x.st]));
+            if (j == n - 1) tc_commit(smem_u32(&bars->own_empty));
+          };
+          scores(0, at);
+          wait_acc();
+          // (a single key tile's dP is its own_empty commit; S(1) precedes the last dP otherwise)
+          dprob(0, after(at, 1));
+          if (n > 1) scores(1, after(at, 2));
+          for (int j = 0; ok && j < n; ++j) {
+            const RingPos<NS> k = at, k1 = after(at, 2);
+            ok = mbar_wait(smem_u32(&bars->ds_full), (uint32_t)((steps + j) & 1), status, a.budget);
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) dprob(j + 1, after(k1, 1));  // dP(j) has been read
+            if (!ok) break;
+            accumulate(384, 128 * (j & 1), ring_mn + k.st * kStage, j == 0);  // dQ += dS K_j
+            tc_commit(smem_u32(&bars->empty[k.st]));
+            if (j + 2 < n) scores(j + 2, after(k1, 2));  // overwrites dS(j) after the MMAs above, in order
+            at = k1;
+          }
+        }
+        steps += n;
+        tc_commit(smem_u32(&bars->done));
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    // every commit of this thread has completed once its last one has
+    if (lane == 0 && own > 0) mbar_wait_drain(smem_u32(&bars->done), (uint32_t)((own - 1) & 1), a.budget);
+  } else if (warp == 2) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    // ================= hands tiles on. dK/dV: lse2 and delta of the tile's rows; rows past the user's
+    // end: weight 0, and zeros in the Q and dO tiles. dQ: zeros in the dropped rows of K.
+    float* stat = reinterpret_cast<float*>(smem + L::oStat);
+    RingPos<NS> at;
+    int steps = 0;
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      const bool dkv = it.kind == kDkv;
+      int grp = 0, qt = 0;
+      MaskBytes mb;
+      if (!dkv && it.n > 0) mb.load(a.mask, it.k0, it.k1, lane);
+      for (int i = 0; ok && i < it.n; ++i, ++steps) {
+        const RingPos<NS> x = at;
+        at.next();
+        const RingPos<NS> y = at;
+        at.next();
+        if (dkv) {
+          const int t = it.t0 + qt * tokens, rows = min(128, (it.t1 - t) * a.PG);
+          const float2* src = a.stats + ((long long)(it.h * sharing + grp) * a.n_q + t) * a.PG;
+          float2 v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            v[z] = lane + 32 * z < rows ? src[lane + 32 * z] : make_float2(INFINITY, 0.f);
+          ok = mbar_wait_warp(smem_u32(&bars->full[x.st]), x.ph, status, a.budget) &&
+               mbar_wait_warp(smem_u32(&bars->full[y.st]), y.ph, status, a.budget);
+          if (!ok) break;
+          if (rows < 128) {
+            uint32_t keep[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              keep[z] = rows >= 32 * z + 32 ? ~0u : rows > 32 * z ? (1u << (rows - 32 * z)) - 1u : 0u;
+            zero_rows(smem + L::oRing + x.st * L::kTile, L::kBoxes, keep, lane);
+            zero_rows(smem + L::oRing + y.st * L::kTile, L::kBoxes, keep, lane);
+            fence_proxy_async_smem();
+          }
+          // slot steps mod 4 was last read four steps ago, whose tiles have left the ring
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            stat[(steps & 3) * 256 + lane + 32 * z] = -v[z].x;
+            stat[(steps & 3) * 256 + 128 + lane + 32 * z] = -v[z].y;
+          }
+          if (++qt == it.aux) {
+            qt = 0;
+            ++grp;
+          }
+        } else {
+          uint32_t keep[4];
+          const bool drop = mb.vote(a.mask, it.k0 + 128 * i, it.k1, lane, keep);
+          if (i + 1 < it.n) mb.load(a.mask, it.k0 + 128 * (i + 1), it.k1, lane);
+          ok = mbar_wait_warp(smem_u32(&bars->full[x.st]), x.ph, status, a.budget);
+          if (!ok) break;
+          if (drop) {
+            zero_rows(smem + L::oRing + x.st * L::kTile, L::kBoxes, keep, lane);
+            fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->ready[steps & 7]));
+      }
+    }
+  } else if (warp == 3) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    // ================= takes items, up to two ahead
+    if (lane == 0) {
+      const int groups = a.H / a.PG;
+      const long long n_dkv = a.hdr->pad[0] * a.Hkv, n_dq = a.hdr->total_tiles * 2 * a.splits * groups;
+      bool ok = true;
+      for (int s = 0; ok;) {
+        long long id = (long long)atomicAdd(reinterpret_cast<unsigned long long*>(&a.hdr->pad[1]), 1ull);
+        Item x = {};
+        x.kind = kEnd;
+        if (id < n_dkv + n_dq) {
+          const long long n1 = a.dq_first ? n_dq : n_dkv;
+          const bool dq = (id < n1) == a.dq_first;
+          if (id >= n1) id -= n1;
+          if (!dq) {
+            const Tile tl = a.ktiles[id / a.Hkv];
+            x.kind = kDkv;
+            x.h = (int)(id % a.Hkv);
+            x.k0 = (int)a.koff[tl.user] + tl.index * 128;
+            x.k1 = (int)a.koff[tl.user + 1];
+            x.t0 = (int)a.qoff[tl.user];
+            x.t1 = (int)a.qoff[tl.user + 1];
+            x.aux = (x.t1 - x.t0 + tokens - 1) / tokens;
+            x.n = x.aux * sharing;
+          } else {
+            // the group fastest: items of the same keys run at the same time
+            x.kind = kDq;
+            x.h = (int)(id % groups);
+            id /= groups;
+            const int half = (int)(id & 1);
+            id >>= 1;
+            x.aux = (int)(id % a.splits);
+            const Tile tl = a.qtiles[id / a.splits];
+            x.t0 = (int)a.qoff[tl.user] + (tl.index * 2 + half) * tokens;
+            x.t1 = (int)a.qoff[tl.user + 1];
+            if (x.t0 >= x.t1) continue;  // the pair's second tile has no rows
+            const int k = (int)a.koff[tl.user];
+            x.k1 = (int)a.koff[tl.user + 1];
+            const int all = (x.k1 - k + 127) / 128;
+            const int j0 = (int)((long long)all * x.aux / a.splits);
+            x.n = (int)((long long)all * (x.aux + 1) / a.splits) - j0;
+            x.k0 = k + j0 * 128;
+          }
+        }
+        ok = mbar_wait(smem_u32(&bars->item_empty[s & 1]), (uint32_t)(((s >> 1) & 1) ^ 1), status, a.budget);
+        if (!ok) break;
+        items[s & 1] = x;
+        mbar_arrive(smem_u32(&bars->item_full[s & 1]));
+        ++s;
+        if (x.kind == kEnd) break;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsElem));
+    // ================= elementwise: thread = row (key of dK/dV, query of dQ), warpgroup w = columns
+    // [64 w, 64 w + 64)
+    const int w = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const float c = a.c;
+    const uint64_t c2 = f2_pack(c, c);
+    int steps = 0, own = 0;
+    uint32_t sph = 0;  // bit b: parity of the uses of S buffer b so far
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      const int n = it.n;
+      const bool dkv = it.kind == kDkv;
+      if (dkv) {
+        const uint32_t ts = tmem + lane_off + 64 * w, tp = ts + 128;
+        for (int i = 0; i < n; ++i, ++steps) {
+          if (!mbar_wait_warp(smem_u32(&bars->ready[steps & 7]), (uint32_t)((steps >> 3) & 1), status, a.budget) ||
+              !mbar_wait_warp(smem_u32(&bars->s_full[0]), sph & 1u, status, a.budget)) {
+            ok = false;
+            break;
+          }
+          sph ^= 1u;
+          tc_fence_after();
+          const ulonglong2* st =
+              reinterpret_cast<const ulonglong2*>(smem + L::oStat + (steps & 3) * 1024 + 256 * w);
+          uint32_t v[2][32];
+          tmem_ld32_raw(ts, v[0]);
+          tmem_ld32_raw(ts + 32, v[1]);
+          tmem_wait_tie(v[0]);
+          tie32(v[1]);
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {  // four columns: -lse2 of them in one load
+            const ulonglong2 f = st[x];
+            uint32_t* e = &v[x >> 3][(4 * x) & 31];
+            float p0, p1, p2, p3;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(e[0]), __uint_as_float(e[1])), c2, f.x), p0, p1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(e[2]), __uint_as_float(e[3])), c2, f.y), p2, p3);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            p2 = ex2_approx(p2);
+            p3 = ex2_approx(p3);
+            pk[2 * x] = cvt_bf16x2(p0, p1);
+            pk[2 * x + 1] = cvt_bf16x2(p2, p3);
+            e[0] = __float_as_uint(p0);
+            e[1] = __float_as_uint(p1);
+            e[2] = __float_as_uint(p2);
+            e[3] = __float_as_uint(p3);
+          }
+          tmem_st32(ts, pk);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+          if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(steps & 1), status, a.budget)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t dp[32];
+            tmem_ld32_raw(tp + 32 * h, dp);
+            tmem_wait_tie(dp);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const ulonglong2 f = st[32 + 8 * h + x];  // -delta
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int z = 4 * x + 2 * y;
+                float d0, d1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(v[h][z]), __uint_as_float(v[h][z + 1])),
+                                 f2_add(f2_pack(__uint_as_float(dp[z]), __uint_as_float(dp[z + 1])), y ? f.y : f.x)),
+                          d0, d1);
+                pk[16 * h + 2 * x + y] = cvt_bf16x2(d0, d1);
+              }
+            }
+          }
+          tmem_st32(tp, pk);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+        }
+      } else {
+        const uint32_t tp = tmem + lane_off + kColAcc + 64 * w;
+        const int t = it.t0 + r / a.PG;
+        float lse2 = INFINITY, delta = 0.f;
+        if (t < it.t1) {
+          const float2 f = a.stats[((long long)it.h * a.n_q + t) * a.PG + r % a.PG];
+          lse2 = f.x;
+          delta = f.y;
+        }
+        const uint64_t nl2 = f2_pack(-lse2, -lse2), nd2 = f2_pack(-delta, -delta);
+        MaskBytes mb;
+        if (n > 0) mb.load(a.mask, it.k0, it.k1, lane);
+        for (int j = 0; j < n; ++j, ++steps) {
+          uint32_t keep[4];
+          const bool drop = mb.vote(a.mask, it.k0 + 128 * j, it.k1, lane, keep);
+          if (j + 1 < n) mb.load(a.mask, it.k0 + 128 * (j + 1), it.k1, lane);
+          const uint32_t ts = tmem + lane_off + 128 * (j & 1) + 64 * w;
+          if (!mbar_wait_warp(smem_u32(&bars->s_full[j & 1]), (sph >> (j & 1)) & 1u, status, a.budget)) {
+            ok = false;
+            break;
+          }
+          sph ^= 1u << (j & 1);
+          tc_fence_after();
+          uint32_t v[2][32];
+          tmem_ld32_raw(ts, v[0]);
+          tmem_ld32_raw(ts + 32, v[1]);
+          tmem_wait_tie(v[0]);
+          tie32(v[1]);
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[x >> 5][x & 31]), __uint_as_float(v[x >> 5][(x & 31) + 1])), c2,
+                             nl2), p0, p1);
+            v[x >> 5][x & 31] = __float_as_uint(ex2_approx(p0));
+            v[x >> 5][(x & 31) + 1] = __float_as_uint(ex2_approx(p1));
+          }
+          if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(steps & 1), status, a.budget)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t pk[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t dp[32];
+            tmem_ld32_raw(tp + 32 * h, dp);
+            tmem_wait_tie(dp);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float d0, d1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(v[h][2 * x]), __uint_as_float(v[h][2 * x + 1])),
+                               f2_add(f2_pack(__uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1])), nd2)), d0, d1);
+              pk[16 * h + x] = cvt_bf16x2(d0, d1);
+            }
+          }
+          if (drop) {  // a pair's halves by the keep bits of its columns
+            const uint32_t k0w = w ? keep[2] : keep[0], k1w = w ? keep[3] : keep[1];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const uint32_t b = (x < 16 ? k0w : k1w) >> (2 * (x & 15));
+              pk[x] &= ((b & 1u) ? 0xffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u);
+            }
+          }
+          tmem_st32(ts, pk);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+        }
+      }
+      // ---- the accumulators are complete
+      bool have = false;
+      if (n > 0) {
+        have = ok && mbar_wait_warp(smem_u32(&bars->done), (uint32_t)(own & 1), status, a.budget);
+        ok = have;
+        ++own;
+      }
+      tc_fence_after();
+      auto freed = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
+      };
+      if (dkv) {  // warpgroup 0 writes dV, warpgroup 1 dK; a dropped key row gets 0
+        const int j = it.k0 + r;
+        const bool zero = a.mask && j < it.k1 && a.mask[j] == 0;
+        __nv_bfloat16* out = w ? a.dK : a.dV;
+        write_rows<D>(tmem + lane_off + kColAcc + 128 * w, have, zero, w ? a.scale : 1.f,
+                      [&](int i) -> __nv_bfloat16* {
+                        const int row = it.k0 + q4 * 32 + i;
+                        return row < it.k1 ? out + ((long long)row * a.Hkv + it.h) * D : nullptr;
+                      }, freed, lane);
+      } else if (a.splits == 1) {  // each warpgroup writes half of the columns
+        write_rows<D / 2>(tmem + lane_off + 384 + w * (D / 2), have, false, a.scale,
+                          [&](int i) -> __nv_bfloat16* {
+                            const int x = q4 * 32 + i, t = it.t0 + x / a.PG;
+                            return t < it.t1 ? a.dQ + ((long long)t * a.H + it.h * a.PG + x % a.PG) * D + w * (D / 2)
+                                             : nullptr;
+                          }, freed, lane);
+      } else {
+        const int t = it.t0 + r / a.PG;
+        float* po = a.part + (((long long)it.aux * a.n_q + t) * a.H + it.h * a.PG + r % a.PG) * D + w * (D / 2);
+#pragma unroll 1
+        for (int x = 0; x < D / 2; x += 16) {
+          uint32_t o[16];
+          if (have) {
+            tmem_ld16(tmem + lane_off + 384 + w * (D / 2) + x, o);
+            tmem_wait16(o);
+          }
+          if (x + 16 == D / 2) freed();
+          if (t < it.t1) {
+#pragma unroll
+            for (int y = 0; y < 16; y += 4)
+              *reinterpret_cast<float4*>(po + x + y) =
+                  have ? make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]),
+                                     __uint_as_float(o[y + 2]), __uint_as_float(o[y + 3]))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -638,7 +731,8 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.G = a.H / a.Hkv;
   p.PG = geo.pg;
   p.splits = geo.splits;
-  p.kv_ctas = geo.key_tiles * a.Hkv;
+  // a dK/dV item walks a user's packed rows, a dQ item its keys
+  p.dq_first = a.n_kv >= a.n_q * (a.H / a.Hkv);
   p.c = a.scale * kLog2e;
   p.scale = a.scale;
   p.dQ = static_cast<__nv_bfloat16*>(a.dQ);
@@ -647,14 +741,12 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.part = reinterpret_cast<float*>(ws + a.plan.part_o);
   p.n_q = a.n_q;
   p.budget = kDefaultWaitBudget;
+  static_assert(sizeof(Item) == 32, "the item ring");
   constexpr size_t smem = 1024 + BSmem<D>::oBars + sizeof(BBars);
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = prepare_kernel<cross_bwd_kernel<D>>(smem, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  const long long ctas = p.kv_ctas + geo.pair_tiles * 2 * (a.H / geo.pg) * geo.splits;
-  if (ctas == 0) return cudaSuccess;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if ((e = launch_dependent(cross_bwd_kernel<D>, dim3((unsigned)ctas), dim3(kThreads), smem, s, tq, tdo, tk,
+  if ((e = launch_dependent(cross_bwd_kernel<D>, dim3((unsigned)geo.ctas), dim3(kThreads), smem, s, tq, tdo, tk,
                             tv, p)) != cudaSuccess)
     return e;
   if (geo.splits == 1 || a.n_q == 0) return cudaSuccess;

@@ -7,18 +7,22 @@
 // a tile's maximum exceeds it by more than 8 in log2 units (O and l are then rescaled; the
 // weights stay below 2^8 otherwise, and bf16 keeps their relative precision at any size).
 //
-// One CTA works on two tiles (256 rows) of one user and head group, so that each key tile read
-// from L2 serves 256 rows (one tile would need 64 bytes a clock of L2 reads against the
-// tensor pipe, more than an SM gets), and so that one warpgroup's softmax runs while the
-// tensor cores work for the other. When the rows fit in one tile, both warpgroups take that
-// tile, on alternate key tiles, with an O, m and l each, merged at the end. When there are fewer
-// CTAs than SMs and many keys, `splits` CTAs share a user's key tiles and leave fp32 partials that
-// cross_join_kernel puts together in a fixed order.
+// An item is two tiles (256 rows) of one user and head group, so that each key tile read from L2
+// serves 256 rows (one tile would need 64 bytes a clock of L2 reads against the tensor pipe,
+// more than an SM gets), and so that one warpgroup's softmax runs while the tensor cores work
+// for the other. When the rows fit in one tile, both warpgroups take that tile, on alternate
+// key tiles, with an O, m and l each, merged at the end. The items' key tiles, in order, are split
+// evenly over one CTA per SM (the schedule's Start records): an item that a boundary cuts is
+// left by its CTAs as fp32 parts, which cross_join_kernel puts together in order. A CTA runs its
+// items through without a stop: while the warpgroups write an item's rows the next item's
+// queries and keys are loaded and its first scores computed (one CTA per item, with its
+// set-up, first loads and epilogue exposed, lost 12,000 clocks an item: 4 x 4096 x 8 heads).
 //
-// Roles (384 threads): warp 0 TMA (Q once, then K_0, V_0, K_1, V_1, ... through one ring of
+// Roles (384 threads): warp 0 TMA (Q once an item, then K_0, V_0, K_1, V_1, ... through one ring of
 // stages), warp 1 TMEM allocation and every MMA, warp 2 hands V tiles on, zeroing rows that
-// the mask or the end of the range drops (weight 0 times NaN must not count), warps 4-11 two
-// softmax warpgroups, one thread per row. P stays in TMEM as the A operand of the second MMA.
+// the mask or the end of the range drops (weight 0 times NaN must not count), warp 3 reads the
+// schedule ahead, warps 4-11 two softmax warpgroups, one thread per row. P stays in TMEM as the A
+// operand of the second MMA.
 // Bound: at d = 128 a tile costs 1,024 tensor clocks and 1,024 clocks of exponentials (16 a
 // clock and SM); at d = 64 the exponentials bound it.
 #include <cmath>
@@ -49,34 +53,56 @@ struct FSmem {
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kTile;
   static constexpr int oML = oKV + kNS * kTile;  // warpgroup 1's m and l (merge)
-  static constexpr int oBars = oML + 2 * 128 * 4;
+  static constexpr int oItems = oML + 2 * 128 * 4;
+  static constexpr int oBars = oItems + 2 * 32;
 };
 
 struct FBars {
-  uint64_t q_full, full[8], empty[8];
-  uint64_t v_ready[8];  // by key tile mod 8: fewer V tiles than that fit in the ring
+  uint64_t q_full, q_empty, full[8], empty[8];
+  uint64_t v_ready[8];  // by V tile mod 8: fewer V tiles than that fit in the ring
   uint64_t s_full[2], o_done[2];
   uint64_t p_full[2][2];  // [tile][half of the keys]: the second product starts on the first half
-  uint64_t merge, drain;
+  uint64_t o_free, merge, drain;
+  uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
+};
+
+// One CTA's piece of an item, as warp 3 hands it to the others.
+struct Item {
+  int n;            // key tiles of this piece (-1: no more items)
+  int t0, t1;       // first token of the tiles, one past the user's last
+  int k0, k1;       // first key row of the piece, one past the user's last
+  int hu, two;      // head group; rows in both tiles
+  int part;         // -1: the whole item; else the part to leave
 };
 
 struct FwdParams {
   const int64_t* qoff;
   const int64_t* koff;
   const Tile* tiles;
+  const Start* starts;   // [CTAs + 1]
   WsHeader* hdr;
   const uint8_t* mask;
   int H, G, PG;          // heads, heads per key head, heads per tile
-  int splits;
   float c;               // scale log2 e
   __nv_bfloat16* out;    // [n_q, H, D]
   float* lse;            // [n_q, H]
-  float* part_o;         // [splits][n_q, H, D] (splits > 1)
-  float* part_lse;       // [splits][n_q, H]
-  long long n_q;
+  float* part_o;         // [2 CTAs][256, D] (null: no boundary cuts an item)
+  float* part_lse;       // [2 CTAs][256], log2 units
   long long budget;
 };
+
+constexpr int kConsumers = 11;  // warps that read an item: all but warp 3
+
+// The s-th item; false: none, or the wait gave up. Whole warp.
+__device__ __forceinline__ bool get_item(FBars* bars, const Item* ring, int s, int lane, int* status,
+                                         long long budget, Item* it) {
+  const bool ok = mbar_wait_warp(smem_u32(&bars->item_full[s & 1]), (uint32_t)((s >> 1) & 1), status, budget);
+  *it = ring[s & 1];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s & 1]));
+  return ok && it->n >= 0;
+}
 
 // The 128 scores of this thread's row.
 __device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[4][32]) {
@@ -104,6 +130,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&bars->full[s]), 1);
       mbar_init(smem_u32(&bars->empty[s]), 1);
@@ -114,7 +141,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(smem_u32(&bars->p_full[w][0]), 4);
       mbar_init(smem_u32(&bars->p_full[w][1]), 4);
       mbar_init(smem_u32(&bars->o_done[w]), 1);
+      mbar_init(smem_u32(&bars->item_full[w]), 1);
+      mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
     }
+    mbar_init(smem_u32(&bars->o_free), 8);
     mbar_init(smem_u32(&bars->merge), 4);
     mbar_init(smem_u32(&bars->drain), 1);
     fence_mbar_init();
@@ -133,129 +163,193 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   griddep_wait();  // the schedule
 
   const int groups = a.H / a.PG, tokens = 128 / a.PG;  // tokens per tile
-  const long long g = blockIdx.x / groups;
-  const int hu = (int)(blockIdx.x - g * groups);
-  const bool work = g < a.hdr->total_tiles;
-  int nkt = 0, j0 = 0, hk = 0, t0 = 0, t1 = 0, k0 = 0, k1 = 0;
-  bool two = false;
-  if (work) {
-    const Tile tl = a.tiles[g];
-    t0 = (int)a.qoff[tl.user] + tl.index * 2 * tokens;
-    t1 = (int)a.qoff[tl.user + 1];
-    k0 = (int)a.koff[tl.user];
-    k1 = (int)a.koff[tl.user + 1];
-    const int all = (k1 - k0 + 127) / 128;
-    j0 = (int)((long long)all * blockIdx.y / a.splits);
-    nkt = (int)((long long)all * (blockIdx.y + 1) / a.splits) - j0;
-    k0 += j0 * 128;
-    two = t1 - t0 > tokens;
-    hk = hu * a.PG / a.G;
-  }
+  Item* items = reinterpret_cast<Item*>(smem + L::oItems);
+  Item it;
 
   // every warp changes its register count inside its role's branch, so that the compiler
   // budgets each role for its count
   if (warp == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     // ================= TMA
-    if (lane == 0 && nkt > 0) {
-      const uint32_t qf = smem_u32(&bars->q_full);
-      mbar_arrive_expect_tx(qf, (two ? 2 : 1) * L::kTile);
-      for (int w = 0; w < (two ? 2 : 1); ++w)
-        for (int b = 0; b < L::kBoxes; ++b)
-          tma_load_3d(sbase + L::oQ + w * L::kTile + b * kBox, &tmap_q, b * 64, hu * a.PG,
-                      t0 + w * tokens, qf);
-      int i = 0;
-      for (; i < 2 * nkt; ++i) {
-        const int st = i % NS;
-        if (!mbar_wait(smem_u32(&bars->empty[st]), (uint32_t)(((i / NS) & 1) ^ 1), status, a.budget)) break;
-        const uint32_t fb = smem_u32(&bars->full[st]);
-        mbar_arrive_expect_tx(fb, L::kTile);
-        for (int b = 0; b < L::kBoxes; ++b)
-          tma_load_3d(sbase + L::oKV + st * L::kTile + b * kBox, (i & 1) ? &tmap_v : &tmap_k, b * 64, hk,
-                      k0 + 128 * (i >> 1), fb);
+    int i = 0, nq = 0;  // ring entries and items loaded so far
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      if (lane == 0 && it.n > 0) {
+        const uint32_t qf = smem_u32(&bars->q_full);
+        ok = mbar_wait(smem_u32(&bars->q_empty), (uint32_t)((nq & 1) ^ 1), status, a.budget);
+        if (ok) {
+          ++nq;
+          mbar_arrive_expect_tx(qf, (it.two ? 2 : 1) * L::kTile);
+          for (int w = 0; w < (it.two ? 2 : 1); ++w)
+            for (int b = 0; b < L::kBoxes; ++b)
+              tma_load_3d(sbase + L::oQ + w * L::kTile + b * kBox, &tmap_q, b * 64, it.hu * a.PG,
+                          it.t0 + w * tokens, qf);
+        }
+        const int hk = it.hu * a.PG / a.G;
+        for (int x = 0; ok && x < 2 * it.n; ++x) {
+          const int st = i % NS;
+          ok = mbar_wait(smem_u32(&bars->empty[st]), (uint32_t)(((i / NS) & 1) ^ 1), status, a.budget);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(&bars->full[st]);
+          mbar_arrive_expect_tx(fb, L::kTile);
+          for (int b = 0; b < L::kBoxes; ++b)
+            tma_load_3d(sbase + L::oKV + st * L::kTile + b * kBox, (x & 1) ? &tmap_v : &tmap_k, b * 64, hk,
+                        it.k0 + 128 * (x >> 1), fb);
+          ++i;
+        }
       }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {
       for (int x = (i > NS ? i - NS : 0); x < i; ++x)
         mbar_wait_drain(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), a.budget);
-      mbar_wait_drain(qf, 0, a.budget);
+      if (nq > 0) mbar_wait_drain(smem_u32(&bars->q_full), (uint32_t)((nq - 1) & 1), a.budget);
     }
   } else if (warp == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     // ================= MMAs. Tile w's order is S_w(0), [O_w(j), S_w(j + 1)]...: P_w(j) lies over
     // S_w(j), and the pipe runs a thread's MMAs in order, so S_w(j + 1) overwrites it only
-    // after O_w(j) has read it.
-    if (lane == 0 && nkt > 0) {
-      const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
-      const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
-      bool ok = mbar_wait(smem_u32(&bars->q_full), 0, status, a.budget);
-      auto scores = [&](int w, int j) {  // S_w = Q_w K_j^T
-        const int i = 2 * j, st = i % NS;
-        ok = ok && mbar_wait(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t dq = smem_desc(sbase + L::oQ + (two ? w : 0) * L::kTile, 16, 1024, kSwizzle128B);
-        const uint64_t dk = smem_desc(sbase + L::oKV + st * L::kTile, 16, 1024, kSwizzle128B);
+    // after O_w(j) has read it. The next item's first scores follow the last O.
+    const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
+    const uint32_t q_lo = desc_k(sbase + L::oQ), k_lo = desc_k(sbase + L::oKV), v_lo = desc_mn(sbase + L::oKV);
+    constexpr uint32_t kStage = L::kTile >> 4;
+    RingPos<NS> at;       // the ring's next entry
+    int vbase = 0, nq = 0;  // V tiles and items with keys before this item
+    uint32_t ph = 0;      // bit w: parity of the key tiles of S buffer w so far
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      if (lane == 0 && it.n > 0) {
+        const int n = it.n;
+        const bool two = it.two;
+        ok = mbar_wait(smem_u32(&bars->q_full), (uint32_t)(nq & 1), status, a.budget);
+        ++nq;
+        auto scores = [&](int w, RingPos<NS> k, bool last_use, bool last) {  // S_w = Q_w K^T
+          ok = ok && mbar_wait(smem_u32(&bars->full[k.st]), k.ph, status, a.budget);
+          if (!ok) return;
+          tc_fence_after();
+          product_ss<D>(tmem + col_s(w), q_lo + (two ? w : 0) * kStage, k_lo + k.st * kStage, id_s);
+          tc_commit(smem_u32(&bars->s_full[w]));
+          if (last_use) tc_commit(smem_u32(&bars->empty[k.st]));
+          if (last) tc_commit(smem_u32(&bars->q_empty));
+        };
+        auto output = [&](int w, RingPos<NS> v, int vi, bool first, bool last_use) {  // O_w += P_w V
+          ok = ok && mbar_wait(smem_u32(&bars->v_ready[vi & 7]), (uint32_t)((vi >> 3) & 1), status, a.budget) &&
+               mbar_wait(smem_u32(&bars->p_full[w][0]), (ph >> w) & 1u, status, a.budget);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t o = tmem + col_o(w), p = tmem + col_s(w), b = v_lo + v.st * kStage;
+          if (first) mma_ts<0>(o, p, b, kDescHi, id_o);
+          else mma_ts<1>(o, p, b, kDescHi, id_o);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_f16(tmem + col_s(w), dq + kstep(ks), dk + kstep(ks), id_s, ks > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&bars->s_full[w]));
-        if (!two || w == 1) tc_commit(smem_u32(&bars->empty[st]));
-      };
-      auto output = [&](int w, int j, int n) {  // O_w += P_w V_j; n: this tile's n-th key tile
-        const int i = 2 * j + 1, st = i % NS;
-        ok = ok && mbar_wait(smem_u32(&bars->v_ready[j & 7]), (uint32_t)((j >> 3) & 1), status, a.budget);
-        const uint64_t dv = smem_desc(sbase + L::oKV + st * L::kTile, kBox, 1024, kSwizzle128B);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ok = ok && mbar_wait(smem_u32(&bars->p_full[w][h]), (uint32_t)(n & 1), status, a.budget);
+          for (int ks = 1; ks < 4; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          ok = mbar_wait(smem_u32(&bars->p_full[w][1]), (ph >> w) & 1u, status, a.budget);
           if (!ok) return;
           tc_fence_after();
 #pragma unroll
-          for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-            tc_mma_f16_ts(tmem + col_o(w), tmem + col_s(w) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4),
-                          id_o, (n > 0 || ks > 0) ? 1u : 0u);
-        }
-        tc_commit(smem_u32(&bars->o_done[w]));
-        if (!two || w == 1) tc_commit(smem_u32(&bars->empty[st]));
-      };
-      if (two) {
-        scores(0, 0);
-        scores(1, 0);
-        for (int j = 0; ok && j < nkt; ++j)
-          for (int w = 0; w < 2; ++w) {
-            output(w, j, j);
-            if (j + 1 < nkt) scores(w, j + 1);
+          for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          ph ^= 1u << w;
+          tc_commit(smem_u32(&bars->o_done[w]));
+          if (last_use) tc_commit(smem_u32(&bars->empty[v.st]));
+        };
+        // a tile pair's K and V stages follow each other in the ring
+        auto after = [](RingPos<NS> x, int k) {
+          for (int i = 0; i < k; ++i) x.next();
+          return x;
+        };
+        scores(0, at, !two, !two && n == 1);
+        if (two) scores(1, at, true, n == 1);
+        else if (n > 1) scores(1, after(at, 2), true, n == 2);
+        // the accumulators of the item before have been read
+        ok = ok && (s == 0 || mbar_wait(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
+        tc_fence_after();
+        for (int j = 0; ok && j < n; ++j) {
+          const RingPos<NS> v = after(at, 1);
+          if (two) {
+            const RingPos<NS> k = after(v, 1);
+            output(0, v, vbase + j, j == 0, false);
+            if (j + 1 < n) scores(0, k, false, false);
+            output(1, v, vbase + j, j == 0, true);
+            if (j + 1 < n) scores(1, k, true, j + 2 == n);
+          } else {
+            output(j & 1, v, vbase + j, j < 2, true);
+            if (j + 2 < n) scores(j & 1, after(v, 3), true, j + 3 == n);
           }
-      } else {
-        scores(0, 0);
-        if (nkt > 1) scores(1, 1);
-        for (int j = 0; ok && j < nkt; ++j) {
-          output(j & 1, j, j >> 1);
-          if (j + 2 < nkt) scores(j & 1, j + 2);
+          at = after(v, 1);
         }
+        vbase += n;
       }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (lane == 0) {
       tc_commit(smem_u32(&bars->drain));
       mbar_wait_drain(smem_u32(&bars->drain), 0, a.budget);
     }
   } else if (warp == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     // ================= V tiles: zero the dropped rows
-    MaskBytes mb;
-    if (nkt > 0) mb.load(a.mask, k0, k1, lane);
-    for (int j = 0; j < nkt; ++j) {
-      const int i = 2 * j + 1, st = i % NS;
-      uint32_t keep[4];
-      const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
-      if (j + 1 < nkt) mb.load(a.mask, k0 + 128 * (j + 1), k1, lane);
-      if (!mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget)) break;
-      if (drop) {
-        zero_rows(smem + L::oKV + st * L::kTile, L::kBoxes, keep, lane);
-        fence_proxy_async_smem();
+    int base = 0, vbase = 0;
+    bool ok = true;
+    for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
+      MaskBytes mb;
+      if (it.n > 0) mb.load(a.mask, it.k0, it.k1, lane);
+      for (int j = 0; ok && j < it.n; ++j) {
+        const int i = base + 2 * j + 1, st = i % NS, v = vbase + j;
+        uint32_t keep[4];
+        const bool drop = mb.vote(a.mask, it.k0 + 128 * j, it.k1, lane, keep);
+        if (j + 1 < it.n) mb.load(a.mask, it.k0 + 128 * (j + 1), it.k1, lane);
+        ok = mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
+        if (!ok) break;
+        if (drop) {
+          zero_rows(smem + L::oKV + st * L::kTile, L::kBoxes, keep, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->v_ready[v & 7]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->v_ready[j & 7]));
+      base += 2 * it.n;
+      vbase += it.n;
     }
   } else if (warp == 3) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    // ================= the schedule: this CTA's items, up to two ahead
+    if (lane == 0) {
+      Start at = a.starts[blockIdx.x];
+      const Start end = a.starts[blockIdx.x + 1];
+      const bool any = a.hdr->total_tiles > 0;
+      bool ok = true;
+      for (int s = 0; ok; ++s) {
+        const bool more = any && (at.tile < end.tile || (at.tile == end.tile && (at.group < end.group ||
+                                                         (at.group == end.group && at.key < end.key))));
+        Item x;
+        x.n = -1;
+        if (more) {
+          const Tile tl = a.tiles[at.tile];
+          const int t = (int)a.qoff[tl.user] + tl.index * 2 * tokens, k = (int)a.koff[tl.user];
+          x.t0 = t;
+          x.t1 = (int)a.qoff[tl.user + 1];
+          x.k1 = (int)a.koff[tl.user + 1];
+          const int all = (x.k1 - k + 127) / 128;
+          const bool cut = at.tile == end.tile && at.group == end.group;
+          const int to = cut ? end.key : all;
+          x.k0 = k + 128 * at.key;
+          x.n = to - at.key;
+          x.hu = at.group;
+          x.two = x.t1 - t > tokens;
+          x.part = at.key > 0 ? 2 * (int)blockIdx.x : cut ? 2 * (int)blockIdx.x + 1 : -1;
+          at.key = 0;
+          if (++at.group == groups) {
+            at.group = 0;
+            ++at.tile;
+          }
+        }
+        ok = mbar_wait(smem_u32(&bars->item_empty[s & 1]), (uint32_t)(((s >> 1) & 1) ^ 1), status, a.budget);
+        if (!ok) break;
+        items[s & 1] = x;
+        mbar_arrive(smem_u32(&bars->item_full[s & 1]));
+        if (!more) break;
+      }
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ================= softmax warpgroup w: tile w, or alternate key tiles of the only tile
@@ -264,38 +358,46 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t st = tmem + lane_off + col_s(w), ot = tmem + lane_off + col_o(w);
-    const int step = two ? 1 : 2, first = two ? 0 : w;
     const float c = a.c;
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
+    int cnt = 0, singles = 0;  // key tiles so far; items of one tile so far
+    for (int s = 0; ok; ++s) {
+    // the item stays in the ring while it is worked on: registers are short here
+    if (!mbar_wait_warp(smem_u32(&bars->item_full[s & 1]), (uint32_t)((s >> 1) & 1), status, a.budget)) break;
+    const Item& it = items[s & 1];
+    if (it.n < 0) break;
+    const bool two = it.two;
+    const int k0 = it.k0, k1 = it.k1;
+    const int step = two ? 1 : 2, first = two ? 0 : w, nkt = it.n;
+    float m = -INFINITY, l = 0.f;
     int n = 0;
     MaskBytes mb;
     if (first < nkt) mb.load(a.mask, k0 + 128 * first, k1, lane);
-    for (int j = first; j < nkt; j += step, ++n) {
+    for (int j = first; j < nkt; j += step, ++n, ++cnt) {
       uint32_t keep[4];
       const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
       if (j + step < nkt) mb.load(a.mask, k0 + 128 * (j + step), k1, lane);
-      if (!mbar_wait_warp(smem_u32(&bars->s_full[w]), (uint32_t)(n & 1), status, a.budget)) {
+      if (!mbar_wait_warp(smem_u32(&bars->s_full[w]), (uint32_t)(cnt & 1), status, a.budget)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s[4][32];
-      load_scores(st, s);
+      uint32_t sc[4][32];
+      load_scores(st, sc);
       if (drop) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (!((keep[i] >> x) & 1u)) s[i][x] = 0xff800000u;  // -inf
+            if (!((keep[i] >> x) & 1u)) sc[i][x] = 0xff800000u;  // -inf
       }
       float mx[4];  // four chains: the maximum is on the way to everything else
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+        mx[i] = fmaxf(__uint_as_float(sc[i][0]), __uint_as_float(sc[i][1]));
 #pragma unroll
         for (int x = 2; x < 32; x += 2)
-          mx[i] = fmax3(mx[i], __uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1]));
+          mx[i] = fmax3(mx[i], __uint_as_float(sc[i][x]), __uint_as_float(sc[i][x + 1]));
       }
       const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
       const bool raise = (mt - m) * c > kRaise;  // false for -inf - -inf
@@ -303,7 +405,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const float f = raise ? ex2_approx((m - mt) * c) : 1.f;  // 0 for the first maximum
         if (n > 0) {
           // O_w holds every tile before this one once its last MMA has completed
-          if (!mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((n - 1) & 1), status, a.budget)) {
+          if (!mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((cnt - 1) & 1), status, a.budget)) {
             ok = false;
             break;
           }
@@ -322,16 +424,20 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         if (raise) m = mt;
       }
       const float mc = m == -INFINITY ? 0.f : m * c;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+      uint64_t ls[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(s[2 * h + (x >> 4)][(2 * x) & 31]), c, -mc));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(s[2 * h + (x >> 4)][(2 * x + 1) & 31]), c, -mc));
-          ls[x & 3] += p0 + p1;
-          pk[x] = cvt_bf16x2(p0, p1);
+          float z0, z1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sc[2 * h + (x >> 4)][(2 * x) & 31]),
+                                   __uint_as_float(sc[2 * h + (x >> 4)][(2 * x + 1) & 31])), c2, mc2), z0, z1);
+          z0 = ex2_approx(z0);
+          z1 = ex2_approx(z1);
+          ls[x & 1] = f2_add(ls[x & 1], f2_pack(z0, z1));
+          pk[x] = cvt_bf16x2(z0, z1);
         }
         tmem_st32(st + 32 * h, pk);
         tc_wait_st();
@@ -339,97 +445,119 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w][h]));
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      float l0, l1;
+      f2_unpack(f2_add(ls[0], ls[1]), l0, l1);
+      l += l0 + l1;
     }
     // ---- this tile's (or half's) accumulator is complete
     if (ok && n > 0)
-      ok = mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((n - 1) & 1), status, a.budget);
+      ok = mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((cnt - 1) & 1), status, a.budget);
     tc_fence_after();
     float* ml = reinterpret_cast<float*>(smem + L::oML);
     float g0 = 1.f, g1 = 0.f;  // factors of O_0 and O_1 (two tiles: of this tile's own)
-    bool write = work;
     if (!two) {
       if (w == 1) {
+        // the item before has been written, so warpgroup 0 has read its m and l
+        ok = ok && (s == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
         ml[r] = m;
         ml[128 + r] = ok ? l : 0.f;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->merge));
-        write = false;
       } else {
-        const bool merged = mbar_wait_warp(smem_u32(&bars->merge), 0, status, a.budget);
+        ok = mbar_wait_warp(smem_u32(&bars->merge), (uint32_t)(singles & 1), status, a.budget) && ok;
         tc_fence_after();
-        const float m1 = ml[r], l1 = merged ? ml[128 + r] : 0.f;
+        const float m1 = ml[r], l1 = ml[128 + r];
         const float mm = fmaxf(m, m1);
         g0 = l > 0.f ? ex2_approx((m - mm) * c) : 0.f;
         g1 = l1 > 0.f ? ex2_approx((m1 - mm) * c) : 0.f;
         l = l * g0 + l1 * g1;
         m = mm;
       }
+      ++singles;
     }
-    const int t = t0 + (two ? w * tokens : 0) + r / a.PG;
-    write = write && t < t1;
+    const int t = it.t0 + (two ? w * tokens : 0) + r / a.PG;
+    const int part = it.part;
+    const bool mine = two || w == 0, write = mine && t < it.t1;
+    const int hu = it.hu;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     g0 *= inv;
     g1 *= inv;
-    const long long row = (long long)t * a.H + hu * a.PG + r % a.PG;
-    const float lse = l > 0.f ? (m * c + lg2_approx(l)) * kLn2 : -INFINITY;
-    if (a.splits > 1) {
-      float* po = a.part_o + ((long long)blockIdx.y * a.n_q * a.H + row) * D;
-      if (write) a.part_lse[(long long)blockIdx.y * a.n_q * a.H + row] = lse;
-      if (nkt > 0 && work && (two || w == 0)) {
-#pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-          uint32_t o[16], o1[16];
-          tmem_ld16(ot + x, o);
-          if (!two && nkt > 1) tmem_ld16(tmem + lane_off + col_o(1) + x, o1);
-          tmem_wait16(o);
-          if (!two && nkt > 1) tmem_wait16(o1);
-          if (write) {
-#pragma unroll
-            for (int y = 0; y < 16; y += 4) {
-              float v[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                v[z] = __uint_as_float(o[y + z]) * g0;
-                if (!two && nkt > 1) v[z] = fmaf(__uint_as_float(o1[y + z]), g1, v[z]);
-              }
-              *reinterpret_cast<float4*>(po + x + y) = make_float4(v[0], v[1], v[2], v[3]);
-            }
-          }
-        }
-      }
-    } else if (work && (two || w == 0)) {
-      if (write) a.lse[row] = lse;
-      __nv_bfloat16* po = a.out + row * D;
-#pragma unroll 1
-      for (int x = 0; x < D; x += 16) {
-        uint32_t o[16], o1[16];
+    const float lse2 = l > 0.f ? m * c + lg2_approx(l) : -INFINITY;
+    if (write) {
+      if (part < 0) a.lse[(long long)t * a.H + hu * a.PG + r % a.PG] = lse2 * kLn2;
+      else a.part_lse[(long long)part * 256 + w * 128 + r] = lse2;
+    }
+    const int tw = it.t0 + (two ? w * tokens : 0), t1 = it.t1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s & 1]));
+    if (mine && (nkt > 0 || part < 0)) {
+      // 32 words of a row at a time: 32 columns of a part, or 64 of out as bf16 pairs
+      auto columns = [&](int x, uint32_t (&o)[32]) {
         if (nkt > 0) {
-          tmem_ld16(ot + x, o);
-          if (!two && nkt > 1) tmem_ld16(tmem + lane_off + col_o(1) + x, o1);
-          tmem_wait16(o);
-          if (!two && nkt > 1) tmem_wait16(o1);
+          tmem_ld32_raw(ot + x, o);
+          tmem_wait_tie(o);
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * g0);
+          if (!two && nkt > 1) {
+            uint32_t o1[32];
+            tmem_ld32_raw(tmem + lane_off + col_o(1) + x, o1);
+            tmem_wait_tie(o1);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              o[y] = __float_as_uint(fmaf(__uint_as_float(o1[y]), g1, __uint_as_float(o[y])));
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = 0u;
         }
-        if (write) {
-          uint32_t pk[8];
+        if (x == D - 32) {  // the accumulators have been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
+        }
+      };
+      if (part < 0) {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 64) {
+          uint32_t v[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            columns(x + 32 * h, o);
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              v[16 * h + y] = cvt_bf16x2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
+          }
+          regroup(v, lane);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
-            float v0 = 0.f, v1 = 0.f;
-            if (nkt > 0) {
-              v0 = __uint_as_float(o[2 * y]) * g0;
-              v1 = __uint_as_float(o[2 * y + 1]) * g0;
-              if (!two && nkt > 1) {
-                v0 = fmaf(__uint_as_float(o1[2 * y]), g1, v0);
-                v1 = fmaf(__uint_as_float(o1[2 * y + 1]), g1, v1);
-              }
-            }
-            pk[y] = cvt_bf16x2(v0, v1);
+            const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
+            if (tt < t1)
+              *reinterpret_cast<uint4*>(a.out + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x +
+                                        8 * (lane >> 2)) = make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
           }
-          *reinterpret_cast<uint4*>(po + x) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(po + x + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          uint32_t v[32];
+          columns(x, v);
+          regroup(v, lane);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int rr = q4 * 32 + 4 * y + (lane & 3);
+            if (tw + rr / a.PG < t1)
+              *reinterpret_cast<uint4*>(a.part_o + ((long long)part * 256 + w * 128 + rr) * D + x + 4 * (lane >> 2)) =
+                  make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
         }
       }
+    } else {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
+    }
     }
   }
 
@@ -441,40 +569,58 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   }
 }
 
-// out = sum_s w_s O_s, w_s = exp(lse_s - lse), over the splits' normalised partials, in order.
-// One warp per row; a split that saw no key (lse = -inf) left no O.
+// Items that boundaries cut: block (b, y) joins rows [32 y, 32 y + 32) of the item that starts in CTA b
+// and goes on, from the parts of CTAs b, b + 1, ... in order: out = sum w O, w = 2^(lse2 - total).
+// A warp per row, four rows each; a part that saw no kept key (lse2 = -inf) left no O.
 template <int D>
-__global__ void __launch_bounds__(256) cross_join_kernel(const float* __restrict__ part_o,
-                                                         const float* __restrict__ part_lse,
-                                                         int splits, const int64_t* qoff, int R,
-                                                         long long n_q, int H,
-                                                         const WsHeader* hdr,
-                                                         __nv_bfloat16* __restrict__ out,
-                                                         float* __restrict__ lse_out) {
+__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdParams a) {
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5), rows = n_q * H;
-  if (read_status(&hdr->status) != 0 || row >= qoff[R] * H) return;
-  float m = -INFINITY;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, part_lse[s * rows + row]);
-  float l = 0.f, o[D / 32];
-#pragma unroll
-  for (int x = 0; x < D / 32; ++x) o[x] = 0.f;
-  if (m > -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
-      const float ls = part_lse[s * rows + row];
-      if (ls == -INFINITY) continue;
-      const float wgt = ex2_approx((ls - m) * kLog2e);
-      l += wgt;
-      const float* po = part_o + (s * rows + row) * D;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) o[x] = fmaf(wgt, po[lane + 32 * x], o[x]);
-    }
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  if (a.hdr->total_tiles == 0) return;
+  const Start at = a.starts[b], cut = a.starts[b + 1];
+  if (cut.key == 0 || (at.tile == cut.tile && at.group == cut.group && at.key > 0)) return;
+  int last = b + 1;  // the last CTA with a part
+  while (true) {
+    const Start x = a.starts[last + 1];
+    if (x.tile != cut.tile || x.group != cut.group) break;
+    ++last;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const Tile tl = a.tiles[cut.tile];
+  const int t0 = (int)a.qoff[tl.user] + tl.index * (256 / a.PG), t1 = (int)a.qoff[tl.user + 1];
+  const int parts = last - b + 1;
+  for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < (int)blockIdx.y * 32 + 32; r += 8) {
+    const int t = t0 + r / a.PG;
+    if (t >= t1) continue;
+    auto row_of = [&](int x) { return (long long)(x == 0 ? 2 * b + 1 : 2 * (b + x)) * 256 + r; };
+    auto lse_of = [&](int x) {  // -inf for a CTA between two equal boundaries: it left nothing
+      const Start p = a.starts[b + x], q = a.starts[b + x + 1];
+      const bool none = x > 0 && q.tile == p.tile && q.group == p.group && q.key == p.key;
+      return none ? -INFINITY : a.part_lse[row_of(x)];
+    };
+    float m = -INFINITY;
+    for (int x = lane; x < parts; x += 32) m = fmaxf(m, lse_of(x));
 #pragma unroll
-  for (int x = 0; x < D / 32; ++x) out[row * D + lane + 32 * x] = __float2bfloat16(o[x] * inv);
-  if (lane == 0) lse_out[row] = l > 0.f ? m + lg2_approx(l) * kLn2 : -INFINITY;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, o[D / 32];
+#pragma unroll
+    for (int y = 0; y < D / 32; ++y) o[y] = 0.f;
+    if (m > -INFINITY) {
+#pragma unroll 4
+      for (int x = 0; x < parts; ++x) {
+        const float ls = lse_of(x);
+        const float wgt = ls > -INFINITY ? ex2_approx(ls - m) : 0.f;
+        l += wgt;
+        const float* po = a.part_o + row_of(x) * D;
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y) o[y] = wgt > 0.f ? fmaf(wgt, po[lane + 32 * y], o[y]) : o[y];
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long row = (long long)t * a.H + cut.group * a.PG + r % a.PG;
+#pragma unroll
+    for (int y = 0; y < D / 32; ++y) a.out[row * D + lane + 32 * y] = __float2bfloat16(o[y] * inv);
+    if (lane == 0) a.lse[row] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
+  }
 }
 
 template <int D>
@@ -489,30 +635,28 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.qoff = a.qoff;
   p.koff = a.koff;
   p.tiles = reinterpret_cast<const Tile*>(ws + a.plan.qtiles);
+  p.starts = reinterpret_cast<const Start*>(ws + a.plan.starts);
   p.hdr = reinterpret_cast<WsHeader*>(ws + a.plan.hdr);
   p.mask = a.mask;
   p.H = a.H;
   p.G = a.H / a.Hkv;
   p.PG = geo.pg;
-  p.splits = geo.splits;
   p.c = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.part_o = reinterpret_cast<float*>(ws + a.plan.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + a.plan.part_lse);
-  p.n_q = a.n_q;
   p.budget = kDefaultWaitBudget;
+  static_assert(sizeof(Item) == 32, "the item ring");
   constexpr size_t smem = 1024 + FSmem<D>::oBars + sizeof(FBars);
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = prepare_kernel<cross_fwd_kernel<D>>(smem, kRegsLaunch);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(geo.pair_tiles * (a.H / geo.pg)), (unsigned)geo.splits);
-  if ((e = launch_dependent(cross_fwd_kernel<D>, grid, dim3(kThreads), smem, s, tq, tk, tv, p)) != cudaSuccess)
+  if ((e = launch_dependent(cross_fwd_kernel<D>, dim3((unsigned)geo.ctas), dim3(kThreads), smem, s, tq, tk, tv,
+                            p)) != cudaSuccess)
     return e;
-  if (geo.splits == 1) return cudaSuccess;
-  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)((a.n_q * a.H + 7) / 8)), dim3(256), 0, s,
-                          (const float*)p.part_o, (const float*)p.part_lse, geo.splits, a.qoff, a.R,
-                          a.n_q, a.H, (const WsHeader*)p.hdr, p.out, p.lse);
+  if (!geo.cuts) return cudaSuccess;
+  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
