@@ -168,25 +168,19 @@ struct MaskBytes {
 };
 
 // A whole warp zeroes the rows whose bit is 0 in a tile of `boxes` 128-row boxes: a dropped
-// row meets weight 0 in a product, and 0 times what it holds must not be NaN.
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, const uint32_t (&w)[4],
-                                          int lane) {
-  const int pieces = boxes * 8;  // 16-byte pieces of a row; the swizzle stays within the row
-  const int per = 32 / pieces, sub = lane / pieces, c = lane % pieces;  // rows at once
-#pragma unroll 1
-  for (int i = 0; i < 4; ++i) {
-    uint32_t gone = ~w[i];
-    while (gone) {
-      int r = -1;
-      for (int x = 0; x < per; ++x) {
-        if (x == sub && gone) r = 32 * i + __ffs(gone) - 1;
-        gone &= gone - 1;
-      }
-      if (r >= 0)
-        *reinterpret_cast<uint4*>(tile + (c >> 3) * kBox + r * 128 + (c & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+// row meets weight 0 in a product, and 0 times what it holds must not be NaN. A lane per row,
+// its 16-byte pieces in an order that keeps the lanes on different banks (a loop over the dropped
+// rows, two at a time, held the V tiles back: 0.60 against 0.34 ms at one row in ten dropped).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, const uint32_t (&w)[4], int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!((w[i] >> lane) & 1u)) {
+      uint8_t* row = tile + (32 * i + lane) * 128;
+      for (int b = 0; b < boxes; ++b)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(row + b * kBox + ((c ^ (lane & 7)) << 4)) = make_uint4(0, 0, 0, 0);
     }
-  }
 }
 
 // A tile of the schedule: its user, and its place among the user's tiles.

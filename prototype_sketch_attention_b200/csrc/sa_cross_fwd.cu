@@ -42,13 +42,15 @@ constexpr float kRaise = 8.f;
 constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
-__host__ __device__ constexpr uint32_t col_s(int w) { return w ? 128u : 0u; }
-__host__ __device__ constexpr uint32_t col_o(int w) { return w ? 384u : 256u; }
 
 template <int D>
 struct FSmem {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTile = kBoxes * kBox;
+  // TMEM columns: the score buffers, then the accumulators of the two tiles. At d = 64 a third
+  // score buffer fits, and a warpgroup's next scores are there before it asks for them.
+  static constexpr int kNB = D == 128 ? 2 : 3;
+  static constexpr uint32_t kColO = kNB * 128;
   static constexpr int kNS = D == 128 ? 5 : 8;  // stages: 2 + 5 tiles of 32 KB, or 2 + 8 of 16 KB
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kTile;
@@ -60,8 +62,8 @@ struct FSmem {
 struct FBars {
   uint64_t q_full, q_empty, full[8], empty[8];
   uint64_t v_ready[8];  // by V tile mod 8: fewer V tiles than that fit in the ring
-  uint64_t s_full[2], o_done[2];
-  uint64_t p_full[2][2];  // [tile][half of the keys]: the second product starts on the first half
+  uint64_t s_full[3], o_done[2];
+  uint64_t p_full[3][2];  // [buffer][half of the keys]: the second product starts on the first half
   uint64_t o_free, merge, drain;
   uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ FwdParams a) {
   using L = FSmem<D>;
-  constexpr int NS = L::kNS;
+  constexpr int NS = L::kNS, kNB = L::kNB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -136,10 +138,12 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->v_ready[s]), 1);
+    for (int b = 0; b < L::kNB; ++b) {
+      mbar_init(smem_u32(&bars->s_full[b]), 1);
+      mbar_init(smem_u32(&bars->p_full[b][0]), 4);
+      mbar_init(smem_u32(&bars->p_full[b][1]), 4);
+    }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(smem_u32(&bars->s_full[w]), 1);
-      mbar_init(smem_u32(&bars->p_full[w][0]), 4);
-      mbar_init(smem_u32(&bars->p_full[w][1]), 4);
       mbar_init(smem_u32(&bars->o_done[w]), 1);
       mbar_init(smem_u32(&bars->item_full[w]), 1);
       mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
@@ -207,77 +211,70 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
   } else if (warp == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    // ================= MMAs. Tile w's order is S_w(0), [O_w(j), S_w(j + 1)]...: P_w(j) lies over
-    // S_w(j), and the pipe runs a thread's MMAs in order, so S_w(j + 1) overwrites it only
-    // after O_w(j) has read it. The next item's first scores follow the last O.
+    // ================= MMAs. Step q is tile (and accumulator) q mod 2 with key tile q / 2, or key
+    // tile q of the only tile; its scores go to buffer (steps so far) mod kNB. P(q) lies over
+    // S(q), and the pipe runs a thread's MMAs in order, so S(q + kNB) overwrites it only after
+    // O(q) has read it. The next item's first scores follow the last O.
     const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
     const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
     const uint32_t q_lo = desc_k(sbase + L::oQ), k_lo = desc_k(sbase + L::oKV), v_lo = desc_mn(sbase + L::oKV);
     constexpr uint32_t kStage = L::kTile >> 4;
-    RingPos<NS> at;       // the ring's next entry
-    int vbase = 0, nq = 0;  // V tiles and items with keys before this item
-    uint32_t ph = 0;      // bit w: parity of the key tiles of S buffer w so far
+    RingPos<NS> kpos, vpos;  // the next scores' K and the next output's V
+    vpos.next();
+    RingPos<kNB> sb, pb;     // their buffers
+    int vi = 0, nq = 0;      // V tiles and items with keys so far
     bool ok = true;
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       if (lane == 0 && it.n > 0) {
-        const int n = it.n;
         const bool two = it.two;
+        const int steps = two ? 2 * it.n : it.n;
         ok = mbar_wait(smem_u32(&bars->q_full), (uint32_t)(nq & 1), status, a.budget);
         ++nq;
-        auto scores = [&](int w, RingPos<NS> k, bool last_use, bool last) {  // S_w = Q_w K^T
-          ok = ok && mbar_wait(smem_u32(&bars->full[k.st]), k.ph, status, a.budget);
+        auto scores = [&](int q) {
+          const bool last_use = !two || (q & 1);
+          ok = ok && mbar_wait(smem_u32(&bars->full[kpos.st]), kpos.ph, status, a.budget);
           if (!ok) return;
           tc_fence_after();
-          product_ss<D>(tmem + col_s(w), q_lo + (two ? w : 0) * kStage, k_lo + k.st * kStage, id_s);
-          tc_commit(smem_u32(&bars->s_full[w]));
-          if (last_use) tc_commit(smem_u32(&bars->empty[k.st]));
-          if (last) tc_commit(smem_u32(&bars->q_empty));
+          product_ss<D>(tmem + 128 * sb.st, q_lo + (two ? q & 1 : 0) * kStage, k_lo + kpos.st * kStage, id_s);
+          tc_commit(smem_u32(&bars->s_full[sb.st]));
+          sb.next();
+          if (last_use) {
+            tc_commit(smem_u32(&bars->empty[kpos.st]));
+            kpos.next();
+            kpos.next();
+          }
+          if (q == steps - 1) tc_commit(smem_u32(&bars->q_empty));
         };
-        auto output = [&](int w, RingPos<NS> v, int vi, bool first, bool last_use) {  // O_w += P_w V
-          ok = ok && mbar_wait(smem_u32(&bars->v_ready[vi & 7]), (uint32_t)((vi >> 3) & 1), status, a.budget) &&
-               mbar_wait(smem_u32(&bars->p_full[w][0]), (ph >> w) & 1u, status, a.budget);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t o = tmem + col_o(w), p = tmem + col_s(w), b = v_lo + v.st * kStage;
-          if (first) mma_ts<0>(o, p, b, kDescHi, id_o);
-          else mma_ts<1>(o, p, b, kDescHi, id_o);
-#pragma unroll
-          for (int ks = 1; ks < 4; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
-          ok = mbar_wait(smem_u32(&bars->p_full[w][1]), (ph >> w) & 1u, status, a.budget);
-          if (!ok) return;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
-          ph ^= 1u << w;
-          tc_commit(smem_u32(&bars->o_done[w]));
-          if (last_use) tc_commit(smem_u32(&bars->empty[v.st]));
-        };
-        // a tile pair's K and V stages follow each other in the ring
-        auto after = [](RingPos<NS> x, int k) {
-          for (int i = 0; i < k; ++i) x.next();
-          return x;
-        };
-        scores(0, at, !two, !two && n == 1);
-        if (two) scores(1, at, true, n == 1);
-        else if (n > 1) scores(1, after(at, 2), true, n == 2);
+        for (int q = 0; q < kNB && q < steps; ++q) scores(q);
         // the accumulators of the item before have been read
         ok = ok && (s == 0 || mbar_wait(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
         tc_fence_after();
-        for (int j = 0; ok && j < n; ++j) {
-          const RingPos<NS> v = after(at, 1);
-          if (two) {
-            const RingPos<NS> k = after(v, 1);
-            output(0, v, vbase + j, j == 0, false);
-            if (j + 1 < n) scores(0, k, false, false);
-            output(1, v, vbase + j, j == 0, true);
-            if (j + 1 < n) scores(1, k, true, j + 2 == n);
-          } else {
-            output(j & 1, v, vbase + j, j < 2, true);
-            if (j + 2 < n) scores(j & 1, after(v, 3), true, j + 3 == n);
+        for (int q = 0; ok && q < steps; ++q) {
+          const int w = q & 1;
+          ok = mbar_wait(smem_u32(&bars->v_ready[vi & 7]), (uint32_t)((vi >> 3) & 1), status, a.budget) &&
+               mbar_wait(smem_u32(&bars->p_full[pb.st][0]), pb.ph, status, a.budget);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t o = tmem + L::kColO + D * w, p = tmem + 128 * pb.st, b = v_lo + vpos.st * kStage;
+          if (q < 2) mma_ts<0>(o, p, b, kDescHi, id_o);
+          else mma_ts<1>(o, p, b, kDescHi, id_o);
+#pragma unroll
+          for (int ks = 1; ks < 4; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          ok = mbar_wait(smem_u32(&bars->p_full[pb.st][1]), pb.ph, status, a.budget);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          pb.next();
+          tc_commit(smem_u32(&bars->o_done[w]));
+          if (!two || w == 1) {
+            tc_commit(smem_u32(&bars->empty[vpos.st]));
+            vpos.next();
+            vpos.next();
+            ++vi;
           }
-          at = after(v, 1);
+          if (q + kNB < steps) scores(q + kNB);
         }
-        vbase += n;
       }
       ok = __all_sync(0xffffffffu, ok);
     }
@@ -357,10 +354,11 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t st = tmem + lane_off + col_s(w), ot = tmem + lane_off + col_o(w);
+    const uint32_t ot = tmem + lane_off + L::kColO + D * w;
     const float c = a.c;
     bool ok = true;
-    int cnt = 0, singles = 0;  // key tiles so far; items of one tile so far
+    int cnt = 0, singles = 0;  // this warpgroup's steps so far; items of one tile so far
+    RingPos<kNB> base;         // the score buffer of the item's step 0
     for (int s = 0; ok; ++s) {
     // the item stays in the ring while it is worked on: registers are short here
     if (!mbar_wait_warp(smem_u32(&bars->item_full[s & 1]), (uint32_t)((s >> 1) & 1), status, a.budget)) break;
@@ -371,16 +369,20 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int step = two ? 1 : 2, first = two ? 0 : w, nkt = it.n;
     float m = -INFINITY, l = 0.f;
     int n = 0;
+    RingPos<kNB> sb = base;
+    if (w) sb.next();
+    for (int q = (two ? 2 * nkt : nkt) % (2 * kNB); q > 0; --q) base.next();
     MaskBytes mb;
     if (first < nkt) mb.load(a.mask, k0 + 128 * first, k1, lane);
     for (int j = first; j < nkt; j += step, ++n, ++cnt) {
       uint32_t keep[4];
       const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
       if (j + step < nkt) mb.load(a.mask, k0 + 128 * (j + step), k1, lane);
-      if (!mbar_wait_warp(smem_u32(&bars->s_full[w]), (uint32_t)(cnt & 1), status, a.budget)) {
+      if (!mbar_wait_warp(smem_u32(&bars->s_full[sb.st]), sb.ph, status, a.budget)) {
         ok = false;
         break;
       }
+      const uint32_t st = tmem + lane_off + 128 * sb.st;
       tc_fence_after();
       uint32_t sc[4][32];
       load_scores(st, sc);
@@ -443,8 +445,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w][h]));
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[sb.st][h]));
       }
+      sb.next();
+      sb.next();
       float l0, l1;
       f2_unpack(f2_add(ls[0], ls[1]), l0, l1);
       l += l0 + l1;
@@ -501,7 +505,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * g0);
           if (!two && nkt > 1) {
             uint32_t o1[32];
-            tmem_ld32_raw(tmem + lane_off + col_o(1) + x, o1);
+            tmem_ld32_raw(tmem + lane_off + L::kColO + D + x, o1);
             tmem_wait_tie(o1);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
@@ -571,55 +575,96 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
 // Items that boundaries cut: block (b, y) joins rows [32 y, 32 y + 32) of the item that starts in CTA b
 // and goes on, from the parts of CTAs b, b + 1, ... in order: out = sum w O, w = 2^(lse2 - total).
-// A warp per row, four rows each; a part that saw no kept key (lse2 = -inf) left no O.
+// Bound by the chain of loads, so every load that can be is in flight at once: the boundaries by
+// a warp, all parts' lse2 by the block, four rows' O by a warp. A part that saw no kept key
+// (lse2 = -inf), or whose CTA had nothing to do, left no O.
 template <int D>
-__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdParams a) {
+__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdParams a, int ctas) {
+  extern __shared__ float wts[];  // [parts][32]: lse2, then weights
+  __shared__ float total[32];
+  __shared__ int parts_s;
   griddep_wait();
-  const int b = blockIdx.x, lane = threadIdx.x & 31;
-  if (a.hdr->total_tiles == 0) return;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r0 = blockIdx.y * 32;
   const Start at = a.starts[b], cut = a.starts[b + 1];
-  if (cut.key == 0 || (at.tile == cut.tile && at.group == cut.group && at.key > 0)) return;
-  int last = b + 1;  // the last CTA with a part
-  while (true) {
-    const Start x = a.starts[last + 1];
-    if (x.tile != cut.tile || x.group != cut.group) break;
-    ++last;
-  }
+  if (a.hdr->total_tiles == 0 || cut.key == 0 || (at.tile == cut.tile && at.group == cut.group && at.key > 0)) return;
   const Tile tl = a.tiles[cut.tile];
   const int t0 = (int)a.qoff[tl.user] + tl.index * (256 / a.PG), t1 = (int)a.qoff[tl.user + 1];
-  const int parts = last - b + 1;
-  for (int r = blockIdx.y * 32 + (threadIdx.x >> 5); r < (int)blockIdx.y * 32 + 32; r += 8) {
-    const int t = t0 + r / a.PG;
-    if (t >= t1) continue;
-    auto row_of = [&](int x) { return (long long)(x == 0 ? 2 * b + 1 : 2 * (b + x)) * 256 + r; };
-    auto lse_of = [&](int x) {  // -inf for a CTA between two equal boundaries: it left nothing
-      const Start p = a.starts[b + x], q = a.starts[b + x + 1];
-      const bool none = x > 0 && q.tile == p.tile && q.group == p.group && q.key == p.key;
-      return none ? -INFINITY : a.part_lse[row_of(x)];
-    };
-    float m = -INFINITY;
-    for (int x = lane; x < parts; x += 32) m = fmaxf(m, lse_of(x));
+  if (t0 + r0 / a.PG >= t1) return;
+  if (warp == 0) {  // CTAs b .. b + parts - 1: until a boundary lies in another item
+    int n = 1;
+    while (true) {
+      const int x = b + n + lane;
+      bool same = false;
+      if (x < ctas) {
+        const Start z = a.starts[x];
+        same = z.tile == cut.tile && z.group == cut.group;
+      }
+      const unsigned other = __ballot_sync(0xffffffffu, !same);
+      n += other ? __ffs(other) - 1 : 32;
+      if (other) break;
+    }
+    if (lane == 0) parts_s = n;
+  }
+  __syncthreads();
+  const int parts = parts_s;
+  auto row_of = [&](int x) { return (long long)(x == 0 ? 2 * b + 1 : 2 * (b + x)) * 256 + r0; };
+  for (int i = tid; i < parts * 32; i += 256) {
+    const int x = i >> 5;
+    const Start z = a.starts[b + x], y = a.starts[b + x + 1];
+    const bool none = x > 0 && z.tile == y.tile && z.group == y.group && z.key == y.key;
+    wts[i] = none ? -INFINITY : a.part_lse[row_of(x) + (i & 31)];
+  }
+  __syncthreads();
+  if (tid < 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int x = 0; x < parts; ++x) m = fmaxf(m, wts[x * 32 + tid]);
+    for (int x = 0; x < parts; ++x) {
+      const float ls = wts[x * 32 + tid], w = ls > -INFINITY ? ex2_approx(ls - m) : 0.f;
+      l += w;
+      wts[x * 32 + tid] = w;
+    }
+    total[tid] = l > 0.f ? 1.f / l : 0.f;
+    const int t = t0 + (r0 + tid) / a.PG;
+    if (t < t1)
+      a.lse[(long long)t * a.H + cut.group * a.PG + (r0 + tid) % a.PG] =
+          l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
+  }
+  __syncthreads();
+  float o[4][D / 32];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, o[D / 32];
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int y = 0; y < D / 32; ++y) o[y] = 0.f;
-    if (m > -INFINITY) {
-#pragma unroll 4
-      for (int x = 0; x < parts; ++x) {
-        const float ls = lse_of(x);
-        const float wgt = ls > -INFINITY ? ex2_approx(ls - m) : 0.f;
-        l += wgt;
-        const float* po = a.part_o + row_of(x) * D;
+    for (int y = 0; y < D / 32; ++y) o[i][y] = 0.f;
+#pragma unroll 2
+  for (int x = 0; x < parts; ++x) {
+    const float* po = a.part_o + (row_of(x) + 4 * warp) * D + lane * (D / 32);
 #pragma unroll
-        for (int y = 0; y < D / 32; ++y) o[y] = wgt > 0.f ? fmaf(wgt, po[lane + 32 * y], o[y]) : o[y];
+    for (int i = 0; i < 4; ++i) {
+      const float w = wts[x * 32 + 4 * warp + i];
+      if (w > 0.f) {  // (rows past the user's end have no weight)
+        if (D == 128) {
+          const float4 v = *reinterpret_cast<const float4*>(po + i * D);
+          o[i][0] = fmaf(w, v.x, o[i][0]);
+          o[i][1] = fmaf(w, v.y, o[i][1]);
+          o[i][2 % (D / 32)] = fmaf(w, v.z, o[i][2 % (D / 32)]);
+          o[i][3 % (D / 32)] = fmaf(w, v.w, o[i][3 % (D / 32)]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(po + i * D);
+          o[i][0] = fmaf(w, v.x, o[i][0]);
+          o[i][1] = fmaf(w, v.y, o[i][1]);
+        }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long row = (long long)t * a.H + cut.group * a.PG + r % a.PG;
+  }
 #pragma unroll
-    for (int y = 0; y < D / 32; ++y) a.out[row * D + lane + 32 * y] = __float2bfloat16(o[y] * inv);
-    if (lane == 0) a.lse[row] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * warp + i, t = t0 + r / a.PG;
+    if (t >= t1) continue;
+    const float inv = total[4 * warp + i];
+    uint32_t* out = reinterpret_cast<uint32_t*>(
+        a.out + ((long long)t * a.H + cut.group * a.PG + r % a.PG) * D) + lane * (D / 64);
+#pragma unroll
+    for (int y = 0; y < D / 64; ++y) out[y] = cvt_bf16x2(o[i][2 * y] * inv, o[i][2 * y + 1] * inv);
   }
 }
 
@@ -656,7 +701,8 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
                             p)) != cudaSuccess)
     return e;
   if (!geo.cuts) return cudaSuccess;
-  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256), 0, s, p);
+  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256),
+                          (size_t)geo.ctas * 32 * sizeof(float), s, p, geo.ctas);
 }
 
 }  // namespace
