@@ -30,9 +30,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
-// The issuing thread has about 64 clocks for an MMA of 128 x 128 x 16, so descriptors are kept as
-// a low word, to which offsets are added (the address field does not carry), and a constant
-// high word, and the accumulate flag is part of the instruction.
+// The MMA warps run their loops as a whole, on values that the compiler can see to be the same
+// in every lane (broadcast()), and elect one lane only to issue: the MMA takes its operands
+// from uniform registers, and in a branch of one lane each of them is moved there first (80
+// clocks an MMA and 200 a wait, where the tensor cores take 32 to 64). Descriptors are a low word,
+// to which offsets are added (the address field does not carry), and a constant high word.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
+}
+template <typename T>
+__device__ __forceinline__ T broadcast(T x) {
+  return (T)__shfl_sync(0xffffffffu, (int)x, 0);
+}
+
 // kAcc: 1 accumulate, 0 overwrite.
 template <int kAcc>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,

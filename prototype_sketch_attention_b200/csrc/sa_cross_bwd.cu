@@ -251,113 +251,135 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     // ================= MMAs
     const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0), id_o = idesc_bf16_f32(128, D, 0, 1);
     constexpr uint32_t kStage = L::kTile >> 4;
-    const uint32_t own_k = desc_k(sbase + L::oA), ring_k = desc_k(sbase + L::oRing),
-                   ring_mn = desc_mn(sbase + L::oRing);
+    const uint32_t tm = broadcast(tmem), sb0 = broadcast(sbase), br = broadcast(smem_u32(bars));
+    auto bar = [&](const uint64_t& b) {  // the address of a barrier, from the broadcast base
+      return br + (uint32_t)(reinterpret_cast<const uint8_t*>(&b) - reinterpret_cast<const uint8_t*>(bars));
+    };
+    const uint32_t own_k = desc_k(sb0 + L::oA), ring_k = desc_k(sb0 + L::oRing), ring_mn = desc_mn(sb0 + L::oRing);
     RingPos<NS> at;
     int own = 0, steps = 0, pcnt = 0;  // items with steps, steps, dK/dV steps before
     bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      ok = ok && mbar_wait_warp(b, parity, status, a.budget);
+      return ok;
+    };
     // acc += A B: A packed in TMEM, warpgroup w's 64 columns from column 64 w on
     auto accumulate = [&](uint32_t acc, uint32_t pk, uint32_t b, bool first) {
-      if (first) mma_ts<0>(tmem + acc, tmem + pk, b, kDescHi, id_o);
-      else mma_ts<1>(tmem + acc, tmem + pk, b, kDescHi, id_o);
+      if (first) mma_ts<0>(tm + acc, tm + pk, b, kDescHi, id_o);
+      else mma_ts<1>(tm + acc, tm + pk, b, kDescHi, id_o);
 #pragma unroll
       for (int ks = 1; ks < 8; ++ks)
-        mma_ts<1>(tmem + acc, tmem + pk + 64 * (ks >> 2) + 8 * (ks & 3), b + mn_step(ks), kDescHi, id_o);
+        mma_ts<1>(tm + acc, tm + pk + 64 * (ks >> 2) + 8 * (ks & 3), b + mn_step(ks), kDescHi, id_o);
     };
     auto after = [](RingPos<NS> x, int k) {
       for (int i = 0; i < k; ++i) x.next();
       return x;
     };
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
-      if (lane == 0 && it.n > 0) {
-        const int n = it.n;
-        ok = mbar_wait(smem_u32(&bars->own), (uint32_t)(own & 1), status, a.budget);
-        ++own;
-        auto wait_ready = [&](int i) {
-          const int x = steps + i;
-          ok = ok && mbar_wait(smem_u32(&bars->ready[x & 7]), (uint32_t)((x >> 3) & 1), status, a.budget);
-          tc_fence_after();
+      const int n = broadcast(it.n);
+      const bool dkv = broadcast(it.kind) == kDkv;
+      if (n == 0) continue;
+      wait(bar(bars->own), (uint32_t)(own & 1));
+      ++own;
+      auto wait_ready = [&](int i) {
+        const int x = steps + i;
+        wait(bar(bars->ready[0]) + 8 * (x & 7), (uint32_t)((x >> 3) & 1));
+        tc_fence_after();
+      };
+      auto wait_acc = [&]() {  // the accumulators of the item before have been read
+        if (s > 0) wait(bar(bars->acc_free), (uint32_t)((s - 1) & 1));
+        tc_fence_after();
+      };
+      if (dkv) {
+        // own: K, V; ring: Q_i, dO_i
+        auto scores = [&](int i, RingPos<NS> x) {  // S^T = K Q_i^T
+          wait_ready(i);
+          if (ok && elect_one()) {
+            product_ss<D>(tm, own_k, ring_k + x.st * kStage, id_s);
+            tc_commit(bar(bars->s_full[0]));
+          }
+          __syncwarp();
         };
-        auto wait_acc = [&]() {  // the accumulators of the item before have been read
-          ok = ok && (s == 0 || mbar_wait(smem_u32(&bars->acc_free), (uint32_t)((s - 1) & 1), status, a.budget));
-          tc_fence_after();
+        auto dprob = [&](int i, RingPos<NS> x) {  // dP^T = V dO_i^T
+          if (ok && elect_one()) {
+            product_ss<D>(tm + 128, own_k + kStage, ring_k + x.st * kStage, id_s);
+            tc_commit(bar(bars->dp_full));
+            if (i == n - 1) tc_commit(bar(bars->own_empty));
+          }
+          __syncwarp();
         };
-        if (it.kind == kDkv) {
-          // own: K, V; ring: Q_i, dO_i
-          auto scores = [&](int i, RingPos<NS> x) {  // S^T = K Q_i^T
-            wait_ready(i);
-            if (!ok) return;
-            product_ss<D>(tmem, own_k, ring_k + x.st * kStage, id_s);
-            tc_commit(smem_u32(&bars->s_full[0]));
-          };
-          auto dprob = [&](int i, RingPos<NS> x) {  // dP^T = V dO_i^T
-            if (!ok) return;
-            product_ss<D>(tmem + 128, own_k + kStage, ring_k + x.st * kStage, id_s);
-            tc_commit(smem_u32(&bars->dp_full));
-            if (i == n - 1) tc_commit(smem_u32(&bars->own_empty));
-          };
-          scores(0, at);
-          dprob(0, after(at, 1));
-          wait_acc();
-          for (int i = 0; ok && i < n; ++i) {
-            const RingPos<NS> q = at, g = after(at, 1), q1 = after(at, 2);
-            ok = mbar_wait(smem_u32(&bars->p_full), (uint32_t)(pcnt & 1), status, a.budget);
-            if (!ok) break;
-            ++pcnt;
-            tc_fence_after();
+        scores(0, at);
+        dprob(0, after(at, 1));
+        wait_acc();
+        for (int i = 0; ok && i < n; ++i) {
+          const RingPos<NS> q = at, g = after(at, 1), q1 = after(at, 2);
+          if (!wait(bar(bars->p_full), (uint32_t)(pcnt & 1))) break;
+          ++pcnt;
+          tc_fence_after();
+          if (elect_one()) {
             accumulate(kColAcc, 0, ring_mn + g.st * kStage, i == 0);  // dV += P^T dO_i
-            tc_commit(smem_u32(&bars->empty[g.st]));
-            if (i + 1 < n) scores(i + 1, q1);  // overwrites P^T after the MMAs above, in order
-            ok = ok && mbar_wait(smem_u32(&bars->ds_full), (uint32_t)((steps + i) & 1), status, a.budget);
-            if (!ok) break;
-            tc_fence_after();
+            tc_commit(bar(bars->empty[0]) + 8 * g.st);
+          }
+          __syncwarp();
+          if (i + 1 < n) scores(i + 1, q1);  // overwrites P^T after the MMAs above, in order
+          if (!wait(bar(bars->ds_full), (uint32_t)((steps + i) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
             accumulate(384, 128, ring_mn + q.st * kStage, i == 0);    // dK += dS^T Q_i
-            tc_commit(smem_u32(&bars->empty[q.st]));
-            if (i + 1 < n) dprob(i + 1, after(q1, 1));
-            at = q1;
+            tc_commit(bar(bars->empty[0]) + 8 * q.st);
           }
-        } else {
-          // own: Q, dO; ring: K_j, V_j
-          auto scores = [&](int j, RingPos<NS> x) {  // S = Q K_j^T into buffer j mod 2
-            wait_ready(j);
-            if (!ok) return;
-            product_ss<D>(tmem + 128 * (j & 1), own_k, ring_k + x.st * kStage, id_s);
-            tc_commit(smem_u32(&bars->s_full[j & 1]));
-          };
-          auto dprob = [&](int j, RingPos<NS> x) {  // dP = dO V_j^T
-            ok = ok && mbar_wait(smem_u32(&bars->full[x.st]), x.ph, status, a.budget);
-            if (!ok) return;
-            tc_fence_after();
-            product_ss<D>(tmem + kColAcc, own_k + kStage, ring_k + x.st * kStage, id_s);
-            tc_commit(smem_u32(&bars->dp_full));
-            tc_commit(smem_u32(&bars->empty[x.st]));
-            if (j == n - 1) tc_commit(smem_u32(&bars->own_empty));
-          };
-          scores(0, at);
-          wait_acc();
-          // (a single key tile's dP is its own_empty commit; S(1) precedes the last dP otherwise)
-          dprob(0, after(at, 1));
-          if (n > 1) scores(1, after(at, 2));
-          for (int j = 0; ok && j < n; ++j) {
-            const RingPos<NS> k = at, k1 = after(at, 2);
-            ok = mbar_wait(smem_u32(&bars->ds_full), (uint32_t)((steps + j) & 1), status, a.budget);
-            if (!ok) break;
-            tc_fence_after();
-            if (j + 1 < n) dprob(j + 1, after(k1, 1));  // dP(j) has been read
-            if (!ok) break;
-            accumulate(384, 128 * (j & 1), ring_mn + k.st * kStage, j == 0);  // dQ += dS K_j
-            tc_commit(smem_u32(&bars->empty[k.st]));
-            if (j + 2 < n) scores(j + 2, after(k1, 2));  // overwrites dS(j) after the MMAs above, in order
-            at = k1;
-          }
+          __syncwarp();
+          if (i + 1 < n) dprob(i + 1, after(q1, 1));
+          at = q1;
         }
-        steps += n;
-        tc_commit(smem_u32(&bars->done));
+      } else {
+        // own: Q, dO; ring: K_j, V_j
+        auto scores = [&](int j, RingPos<NS> x) {  // S = Q K_j^T into buffer j mod 2
+          wait_ready(j);
+          if (ok && elect_one()) {
+            product_ss<D>(tm + 128 * (j & 1), own_k, ring_k + x.st * kStage, id_s);
+            tc_commit(bar(bars->s_full[0]) + 8 * (j & 1));
+          }
+          __syncwarp();
+        };
+        auto dprob = [&](int j, RingPos<NS> x) {  // dP = dO V_j^T
+          if (!wait(bar(bars->full[0]) + 8 * x.st, x.ph)) return;
+          tc_fence_after();
+          if (elect_one()) {
+            product_ss<D>(tm + kColAcc, own_k + kStage, ring_k + x.st * kStage, id_s);
+            tc_commit(bar(bars->dp_full));
+            tc_commit(bar(bars->empty[0]) + 8 * x.st);
+            if (j == n - 1) tc_commit(bar(bars->own_empty));  // (every S of the item precedes its last dP)
+          }
+          __syncwarp();
+        };
+        scores(0, at);
+        wait_acc();
+        dprob(0, after(at, 1));
+        if (n > 1) scores(1, after(at, 2));
+        for (int j = 0; ok && j < n; ++j) {
+          const RingPos<NS> k = at, k1 = after(at, 2);
+          if (!wait(bar(bars->ds_full), (uint32_t)((steps + j) & 1))) break;
+          tc_fence_after();
+          if (j + 1 < n) dprob(j + 1, after(k1, 1));  // dP(j) has been read
+          if (!ok) break;
+          if (elect_one()) {
+            accumulate(384, 128 * (j & 1), ring_mn + k.st * kStage, j == 0);  // dQ += dS K_j
+            tc_commit(bar(bars->empty[0]) + 8 * k.st);
+          }
+          __syncwarp();
+          if (j + 2 < n) scores(j + 2, after(k1, 2));  // overwrites dS(j) after the MMAs above, in order
+          at = k1;
+        }
       }
-      ok = __all_sync(0xffffffffu, ok);
+      steps += n;
+      if (elect_one()) tc_commit(bar(bars->done));
+      __syncwarp();
     }
-    // every commit of this thread has completed once its last one has
-    if (lane == 0 && own > 0) mbar_wait_drain(smem_u32(&bars->done), (uint32_t)((own - 1) & 1), a.budget);
+    // every commit of the issuing lane (the same lane is elected each time) has completed once its
+    // last one has
+    if (own > 0) mbar_wait_drain(smem_u32(&bars->done), (uint32_t)((own - 1) & 1), a.budget);
+    __syncwarp();
   } else if (warp == 2) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     // ================= hands tiles on. dK/dV: lse2 and delta of the tile's rows; rows past the user's

@@ -217,68 +217,83 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     // O(q) has read it. The next item's first scores follow the last O.
     const uint32_t id_s = idesc_bf16_f32(128, 128, 0, 0);
     const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);
-    const uint32_t q_lo = desc_k(sbase + L::oQ), k_lo = desc_k(sbase + L::oKV), v_lo = desc_mn(sbase + L::oKV);
+    const uint32_t tm = broadcast(tmem), sb0 = broadcast(sbase), br = broadcast(smem_u32(bars));
+    auto bar = [&](const uint64_t& b) {  // the address of a barrier, from the broadcast base
+      return br + (uint32_t)(reinterpret_cast<const uint8_t*>(&b) - reinterpret_cast<const uint8_t*>(bars));
+    };
+    const uint32_t q_lo = desc_k(sb0 + L::oQ), k_lo = desc_k(sb0 + L::oKV), v_lo = desc_mn(sb0 + L::oKV);
     constexpr uint32_t kStage = L::kTile >> 4;
     RingPos<NS> kpos, vpos;  // the next scores' K and the next output's V
     vpos.next();
     RingPos<kNB> sb, pb;     // their buffers
     int vi = 0, nq = 0;      // V tiles and items with keys so far
     bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      ok = ok && mbar_wait_warp(b, parity, status, a.budget);
+      return ok;
+    };
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
-      if (lane == 0 && it.n > 0) {
-        const bool two = it.two;
-        const int steps = two ? 2 * it.n : it.n;
-        ok = mbar_wait(smem_u32(&bars->q_full), (uint32_t)(nq & 1), status, a.budget);
-        ++nq;
-        auto scores = [&](int q) {
-          const bool last_use = !two || (q & 1);
-          ok = ok && mbar_wait(smem_u32(&bars->full[kpos.st]), kpos.ph, status, a.budget);
-          if (!ok) return;
-          tc_fence_after();
-          product_ss<D>(tmem + 128 * sb.st, q_lo + (two ? q & 1 : 0) * kStage, k_lo + kpos.st * kStage, id_s);
-          tc_commit(smem_u32(&bars->s_full[sb.st]));
-          sb.next();
-          if (last_use) {
-            tc_commit(smem_u32(&bars->empty[kpos.st]));
-            kpos.next();
-            kpos.next();
-          }
-          if (q == steps - 1) tc_commit(smem_u32(&bars->q_empty));
-        };
-        for (int q = 0; q < kNB && q < steps; ++q) scores(q);
-        // the accumulators of the item before have been read
-        ok = ok && (s == 0 || mbar_wait(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
+      const bool two = broadcast(it.two);
+      const int n = broadcast(it.n), steps = two ? 2 * n : n;
+      if (n == 0) continue;
+      wait(bar(bars->q_full), (uint32_t)(nq & 1));
+      ++nq;
+      auto scores = [&](int q) {
+        const bool last_use = !two || (q & 1);
+        if (!wait(bar(bars->full[0]) + 8 * kpos.st, kpos.ph)) return;
         tc_fence_after();
-        for (int q = 0; ok && q < steps; ++q) {
-          const int w = q & 1;
-          ok = mbar_wait(smem_u32(&bars->v_ready[vi & 7]), (uint32_t)((vi >> 3) & 1), status, a.budget) &&
-               mbar_wait(smem_u32(&bars->p_full[pb.st][0]), pb.ph, status, a.budget);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t o = tmem + L::kColO + D * w, p = tmem + 128 * pb.st, b = v_lo + vpos.st * kStage;
+        if (elect_one()) {
+          product_ss<D>(tm + 128 * sb.st, q_lo + (two ? q & 1 : 0) * kStage, k_lo + kpos.st * kStage, id_s);
+          tc_commit(bar(bars->s_full[0]) + 8 * sb.st);
+          if (last_use) tc_commit(bar(bars->empty[0]) + 8 * kpos.st);
+          if (q == steps - 1) tc_commit(bar(bars->q_empty));
+        }
+        __syncwarp();
+        sb.next();
+        if (last_use) {
+          kpos.next();
+          kpos.next();
+        }
+      };
+      for (int q = 0; q < kNB && q < steps; ++q) scores(q);
+      // the accumulators of the item before have been read
+      if (s > 0) wait(bar(bars->o_free), (uint32_t)((s - 1) & 1));
+      tc_fence_after();
+      for (int q = 0; ok && q < steps; ++q) {
+        const int w = q & 1;
+        const bool last_use = !two || w == 1;
+        const uint32_t o = tm + L::kColO + D * w, p = tm + 128 * pb.st, b = v_lo + vpos.st * kStage;
+        const uint32_t pf = bar(bars->p_full[0][0]) + 16 * pb.st;
+        if (!wait(bar(bars->v_ready[0]) + 8 * (vi & 7), (uint32_t)((vi >> 3) & 1)) || !wait(pf, pb.ph)) break;
+        tc_fence_after();
+        if (elect_one()) {
           if (q < 2) mma_ts<0>(o, p, b, kDescHi, id_o);
           else mma_ts<1>(o, p, b, kDescHi, id_o);
 #pragma unroll
           for (int ks = 1; ks < 4; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
-          ok = mbar_wait(smem_u32(&bars->p_full[pb.st][1]), pb.ph, status, a.budget);
-          if (!ok) break;
-          tc_fence_after();
+        }
+        __syncwarp();
+        if (!wait(pf + 8, pb.ph)) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
-          pb.next();
-          tc_commit(smem_u32(&bars->o_done[w]));
-          if (!two || w == 1) {
-            tc_commit(smem_u32(&bars->empty[vpos.st]));
-            vpos.next();
-            vpos.next();
-            ++vi;
-          }
-          if (q + kNB < steps) scores(q + kNB);
+          tc_commit(bar(bars->o_done[0]) + 8 * w);
+          if (last_use) tc_commit(bar(bars->empty[0]) + 8 * vpos.st);
         }
+        __syncwarp();
+        pb.next();
+        if (last_use) {
+          vpos.next();
+          vpos.next();
+          ++vi;
+        }
+        if (q + kNB < steps) scores(q + kNB);
       }
-      ok = __all_sync(0xffffffffu, ok);
     }
-    if (lane == 0) {
+    __syncwarp();
+    // commits follow the MMAs of the thread that issued them: the same lane is elected each time
+    if (elect_one()) {
       tc_commit(smem_u32(&bars->drain));
       mbar_wait_drain(smem_u32(&bars->drain), 0, a.budget);
     }
