@@ -8,24 +8,25 @@
 // order that changes from run to run). So there are two kinds of item, each of which owns its
 // output and keeps it in TMEM, at 7 products a pair of tiles in place of 5 and no atomics on data:
 //   dK/dV: a tile of 128 keys of one key head against the user's packed query tiles (of every
-//     head group that shares it). S^T = K Q^T and dP^T = V dO^T put keys on the TMEM lanes,
-//     so P^T and dS^T, written as bf16 over S^T and dP^T, are the A operands in place:
-//     dV += P^T dO, dK += dS^T Q. The rows' lse2 and delta run along the columns and come from
-//     shared memory as broadcasts.
+//     head group that shares it). S^T = K Q^T and dP^T = V dO^T put keys on the TMEM lanes. P^T goes
+//     to shared memory as the bf16 A operand of dV += P^T dO, which frees S^T as soon as it is in
+//     registers, so that the next tile's is computed meanwhile; dS^T, as bf16 over dP^T, is the A
+//     operand of dK += dS^T Q in place. The rows' lse2 and delta run along the columns and come
+//     from shared memory as broadcasts.
 //   dQ: a tile of 128 packed query rows against the user's key tiles: S = Q K^T (two
 //     buffers), dP = dO V^T, dS over S, dQ += dS K. When there are fewer such items than SMs and
 //     many keys, `splits` of them share a tile and leave fp32 partials, summed in order.
 // One CTA per SM takes items from a counter (which CTA computes an item does not change it) and
 // runs through them without a stop: an item's own tiles, first loads and first products overlap
-// the rows' writing of the one before. (A CTA per item: 12,000 clocks an item exposed, as much as
-// four steps; 40 x 300 x 10K, 8 heads: 2.23 ms against 2.25 before: see the table of cases.)
+// the writing of the one before.
 // Roles (384 threads): warp 0 TMA, warp 1 TMEM allocation and every MMA, warp 2 hands tiles on:
 // it zeroes the rows that an MMA would multiply by 0 but must not read (dropped keys, rows past
 // the user's end), and loads lse2 and delta; warp 3 takes the items; warps 4-11 two warpgroups for
 // the elementwise step, 64 columns each, one thread per row. The tensor pipe runs ahead of the
-// elementwise step: dK/dV: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1) | ..., so the exponentials of
-// tile i + 1 run while dK(i) and dP(i + 1) do; dQ: S(j + 1) while tile j is in the elementwise
-// step, then dP(j + 1), dQ(j), S(j + 2).
+// elementwise step: dK/dV: S(i+1) as soon as S(i) is read, dV(i) when P(i) is stored, dK(i) and
+// dP(i+1) when dS(i) is; dQ: S(j+1) while tile j is in the elementwise step, then dP(j+1), dQ(j),
+// S(j+2). A key tile is held from S(j) to dQ(j), so three K and two V stages (one ring of
+// two pairs made every S wait for a load: 3,700 clocks a step).
 // Bound at d = 128: 2,048 tensor clocks a pair of tiles for dK/dV, 1,536 for dQ, 1,024
 // clocks of exponentials in both.
 #include <cmath>
@@ -44,22 +45,29 @@ static_assert(128 * kRegsControl + 256 * kRegsElem <= kThreads * kRegsLaunch,
 // TMEM columns: dK/dV items: S^T 0, dP^T 128, dV 256, dK 384; dQ items: S 0 and 128, dP 256, dQ 384
 constexpr uint32_t kColAcc = 256;  // from here on: what an epilogue reads, or a dQ item's dP
 
+// Shared memory: the item's own tiles (K, V of dK/dV; Q, dO of dQ), then slots of a tile each,
+// which the two kinds of item use in their own way:
+//   dK/dV: NQ slots of Q_i, NQ of dO_i, and (d = 128) the last one for P^T, which has its own
+//          place at d = 64; dQ: NK slots of K_j, NV of V_j.
 template <int D>
 struct BSmem {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTile = kBoxes * kBox;
-  static constexpr int kNS = D == 128 ? 4 : 8;  // ring stages
-  static constexpr int oA = 0;                  // the item's own tiles: K, V (dK/dV) or Q, dO (dQ)
-  static constexpr int oRing = 2 * kTile;       // Q_i, dO_i, ... or K_j, V_j, ...
-  static constexpr int oStat = oRing + kNS * kTile;  // 4 x (128 of -lse2, 128 of -delta)
-  static constexpr int oItems = oStat + 4 * 256 * 4;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int NK = D == 128 ? 3 : 5, NV = kSlots - NK, NQ = D == 128 ? 2 : 3;
+  static constexpr int kStats = D == 128 ? 2 : 4;  // NQ steps at least can hold theirs
+  static constexpr int oA = 0;
+  static constexpr int oRing = 2 * kTile;
+  static constexpr int oP = D == 128 ? oRing + 4 * kTile : oRing + kSlots * kTile;
+  static constexpr int oStat = D == 128 ? oRing + kSlots * kTile : oP + 2 * kBox;
+  static constexpr int oItems = oStat + kStats * 256 * 4;  // a step: 128 of -lse2, 128 of -delta
   static constexpr int oBars = oItems + 2 * 32;
 };
 
 struct BBars {
   uint64_t own, own_empty, full[8], empty[8];
-  uint64_t ready[8];    // by step mod 8: fewer tile pairs than that fit in the ring
-  uint64_t s_full[2], dp_full, p_full, ds_full, done, acc_free;
+  uint64_t ready[8];    // by step mod 8: fewer steps' tiles than that are in the slots
+  uint64_t s_full[2], s_free, dp_full, p_full, p_free, ds_full, done, acc_free;
   uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
 };
@@ -151,13 +159,18 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                  const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ BwdParams a) {
   using L = BSmem<D>;
-  constexpr int NS = L::kNS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  constexpr int NK = L::NK, NV = L::NV, NQ = L::NQ;
+  // d = 128 leaves no room to align by hand; the swizzle needs 1024 bytes, which dynamic shared
+  // memory has when a kernel has no other (checked below)
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   BBars* bars = reinterpret_cast<BBars*>(smem + L::oBars);
   int* status = &a.hdr->status;
+  if (sbase & 1023u) {
+    griddep_wait();
+    latch_status(status, SA_ERR_CUDA);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->own), 1);
@@ -173,7 +186,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
     }
     mbar_init(smem_u32(&bars->dp_full), 1);
+    mbar_init(smem_u32(&bars->s_free), 8);
     mbar_init(smem_u32(&bars->p_full), 8);
+    mbar_init(smem_u32(&bars->p_free), 1);
     mbar_init(smem_u32(&bars->ds_full), 8);
     mbar_init(smem_u32(&bars->done), 1);
     mbar_init(smem_u32(&bars->acc_free), 8);
@@ -200,8 +215,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   if (warp == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     // ================= TMA
-    RingPos<NS> at;
-    int loads = 0, own = 0;
+    uint32_t used = 0, loaded = 0;  // bit: parity of a slot's uses, and of its loads, so far
+    uint32_t any = 0;               // slots ever loaded
+    int own = 0;
     bool ok = true;
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       if (lane == 0 && it.n > 0) {
@@ -219,19 +235,25 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             tma_load_3d(sbase + L::oA + L::kTile + b * kBox, mb, b * 64, y, z, ob);
           }
         }
+        if (D == 128 && dkv && ok) {  // the slot of P: free of the item before
+          ok = mbar_wait(smem_u32(&bars->empty[4]), ((used >> 4) & 1u) ^ 1u, status, a.budget);
+          used ^= 1u << 4;
+        }
         int grp = 0, qt = 0;
         for (int x = 0; ok && x < it.n; ++x) {
           const int y = dkv ? (it.h * sharing + grp) * a.PG : it.h * a.PG / a.G;
           const int z = dkv ? it.t0 + qt * tokens : it.k0 + 128 * x;
           for (int v = 0; v < 2; ++v) {
-            ok = ok && mbar_wait(smem_u32(&bars->empty[at.st]), at.ph ^ 1u, status, a.budget);
+            const int st = dkv ? v * NQ + x % NQ : v ? NK + x % NV : x % NK;
+            ok = ok && mbar_wait(smem_u32(&bars->empty[st]), ((used >> st) & 1u) ^ 1u, status, a.budget);
             if (!ok) break;
-            const uint32_t fb = smem_u32(&bars->full[at.st]);
+            const uint32_t fb = smem_u32(&bars->full[st]);
             mbar_arrive_expect_tx(fb, L::kTile);
             for (int b = 0; b < L::kBoxes; ++b)
-              tma_load_3d(sbase + L::oRing + at.st * L::kTile + b * kBox, v ? ry : rx, b * 64, y, z, fb);
-            at.next();
-            ++loads;
+              tma_load_3d(sbase + L::oRing + st * L::kTile + b * kBox, v ? ry : rx, b * 64, y, z, fb);
+            used ^= 1u << st;
+            loaded ^= 1u << st;
+            any |= 1u << st;
           }
           if (++qt == it.aux) {  // (dQ items do not use them)
             qt = 0;
@@ -242,8 +264,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       ok = __all_sync(0xffffffffu, ok);
     }
     if (lane == 0) {
-      for (int x = (loads > NS ? loads - NS : 0); x < loads; ++x)
-        mbar_wait_drain(smem_u32(&bars->full[x % NS]), (uint32_t)((x / NS) & 1), a.budget);
+      for (int x = 0; x < L::kSlots; ++x)
+        if ((any >> x) & 1u) mbar_wait_drain(smem_u32(&bars->full[x]), ((loaded >> x) & 1u) ^ 1u, a.budget);
       if (own > 0) mbar_wait_drain(smem_u32(&bars->own), (uint32_t)((own - 1) & 1), a.budget);
     }
   } else if (warp == 1) {
@@ -256,8 +278,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       return br + (uint32_t)(reinterpret_cast<const uint8_t*>(&b) - reinterpret_cast<const uint8_t*>(bars));
     };
     const uint32_t own_k = desc_k(sb0 + L::oA), ring_k = desc_k(sb0 + L::oRing), ring_mn = desc_mn(sb0 + L::oRing);
-    RingPos<NS> at;
-    int own = 0, steps = 0, pcnt = 0;  // items with steps, steps, dK/dV steps before
+    const uint32_t p_k = desc_k(sb0 + L::oP);
+    uint32_t loaded = 0;                // bit: parity of a slot's loads before
+    int own = 0, steps = 0, pcnt = 0;   // items with steps, steps, dK/dV steps before
     bool ok = true;
     auto wait = [&](uint32_t b, uint32_t parity) {
       ok = ok && mbar_wait_warp(b, parity, status, a.budget);
@@ -270,10 +293,6 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
       for (int ks = 1; ks < 8; ++ks)
         mma_ts<1>(tm + acc, tm + pk + 64 * (ks >> 2) + 8 * (ks & 3), b + mn_step(ks), kDescHi, id_o);
-    };
-    auto after = [](RingPos<NS> x, int k) {
-      for (int i = 0; i < k; ++i) x.next();
-      return x;
     };
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const int n = broadcast(it.n);
@@ -291,85 +310,95 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         tc_fence_after();
       };
       if (dkv) {
-        // own: K, V; ring: Q_i, dO_i
-        auto scores = [&](int i, RingPos<NS> x) {  // S^T = K Q_i^T
+        // own: K, V; slots: Q_i in i mod NQ, dO_i in NQ + i mod NQ
+        auto scores = [&](int i) {  // S^T = K Q_i^T
           wait_ready(i);
           if (ok && elect_one()) {
-            product_ss<D>(tm, own_k, ring_k + x.st * kStage, id_s);
+            product_ss<D>(tm, own_k, ring_k + (i % NQ) * kStage, id_s);
             tc_commit(bar(bars->s_full[0]));
           }
           __syncwarp();
         };
-        auto dprob = [&](int i, RingPos<NS> x) {  // dP^T = V dO_i^T
+        auto dprob = [&](int i) {  // dP^T = V dO_i^T
           if (ok && elect_one()) {
-            product_ss<D>(tm + 128, own_k + kStage, ring_k + x.st * kStage, id_s);
+            product_ss<D>(tm + 128, own_k + kStage, ring_k + (NQ + i % NQ) * kStage, id_s);
             tc_commit(bar(bars->dp_full));
             if (i == n - 1) tc_commit(bar(bars->own_empty));
           }
           __syncwarp();
         };
-        scores(0, at);
-        dprob(0, after(at, 1));
+        scores(0);
+        dprob(0);
         wait_acc();
         for (int i = 0; ok && i < n; ++i) {
-          const RingPos<NS> q = at, g = after(at, 1), q1 = after(at, 2);
+          const int q = i % NQ, g = NQ + i % NQ;
+          if (i + 1 < n) {  // S(i) is in registers
+            if (!wait(bar(bars->s_free), (uint32_t)(pcnt & 1))) break;
+            scores(i + 1);
+          }
           if (!wait(bar(bars->p_full), (uint32_t)(pcnt & 1))) break;
           ++pcnt;
           tc_fence_after();
-          if (elect_one()) {
-            accumulate(kColAcc, 0, ring_mn + g.st * kStage, i == 0);  // dV += P^T dO_i
-            tc_commit(bar(bars->empty[0]) + 8 * g.st);
+          if (elect_one()) {  // dV += P^T dO_i
+            const uint32_t b = ring_mn + g * kStage;
+            if (i == 0) mma_ss<0>(tm + kColAcc, p_k, b, kDescHi, id_o);
+            else mma_ss<1>(tm + kColAcc, p_k, b, kDescHi, id_o);
+#pragma unroll
+            for (int ks = 1; ks < 8; ++ks) mma_ss<1>(tm + kColAcc, p_k + kstep(ks), b + mn_step(ks), kDescHi, id_o);
+            tc_commit(bar(bars->p_free));
+            tc_commit(bar(bars->empty[0]) + 8 * g);
+            if (D == 128 && i == n - 1) tc_commit(bar(bars->empty[4]));
           }
           __syncwarp();
-          if (i + 1 < n) scores(i + 1, q1);  // overwrites P^T after the MMAs above, in order
           if (!wait(bar(bars->ds_full), (uint32_t)((steps + i) & 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            accumulate(384, 128, ring_mn + q.st * kStage, i == 0);    // dK += dS^T Q_i
-            tc_commit(bar(bars->empty[0]) + 8 * q.st);
+            accumulate(384, 128, ring_mn + q * kStage, i == 0);  // dK += dS^T Q_i
+            tc_commit(bar(bars->empty[0]) + 8 * q);
           }
           __syncwarp();
-          if (i + 1 < n) dprob(i + 1, after(q1, 1));
-          at = q1;
+          if (i + 1 < n) dprob(i + 1);  // overwrites dS^T after the MMAs above, in order
+          loaded ^= (1u << q) | (1u << g);
         }
       } else {
-        // own: Q, dO; ring: K_j, V_j
-        auto scores = [&](int j, RingPos<NS> x) {  // S = Q K_j^T into buffer j mod 2
+        // own: Q, dO; slots: K_j in j mod NK, V_j in NK + j mod NV
+        auto scores = [&](int j) {  // S = Q K_j^T into buffer j mod 2
           wait_ready(j);
           if (ok && elect_one()) {
-            product_ss<D>(tm + 128 * (j & 1), own_k, ring_k + x.st * kStage, id_s);
+            product_ss<D>(tm + 128 * (j & 1), own_k, ring_k + (j % NK) * kStage, id_s);
             tc_commit(bar(bars->s_full[0]) + 8 * (j & 1));
           }
           __syncwarp();
+          loaded ^= 1u << (j % NK);
         };
-        auto dprob = [&](int j, RingPos<NS> x) {  // dP = dO V_j^T
-          if (!wait(bar(bars->full[0]) + 8 * x.st, x.ph)) return;
+        auto dprob = [&](int j) {  // dP = dO V_j^T
+          const int v = NK + j % NV;
+          if (!wait(bar(bars->full[0]) + 8 * v, (loaded >> v) & 1u)) return;
+          loaded ^= 1u << v;
           tc_fence_after();
           if (elect_one()) {
-            product_ss<D>(tm + kColAcc, own_k + kStage, ring_k + x.st * kStage, id_s);
+            product_ss<D>(tm + kColAcc, own_k + kStage, ring_k + v * kStage, id_s);
             tc_commit(bar(bars->dp_full));
-            tc_commit(bar(bars->empty[0]) + 8 * x.st);
+            tc_commit(bar(bars->empty[0]) + 8 * v);
             if (j == n - 1) tc_commit(bar(bars->own_empty));  // (every S of the item precedes its last dP)
           }
           __syncwarp();
         };
-        scores(0, at);
+        scores(0);
         wait_acc();
-        dprob(0, after(at, 1));
-        if (n > 1) scores(1, after(at, 2));
+        dprob(0);
+        if (n > 1) scores(1);
         for (int j = 0; ok && j < n; ++j) {
-          const RingPos<NS> k = at, k1 = after(at, 2);
           if (!wait(bar(bars->ds_full), (uint32_t)((steps + j) & 1))) break;
           tc_fence_after();
-          if (j + 1 < n) dprob(j + 1, after(k1, 1));  // dP(j) has been read
+          if (j + 1 < n) dprob(j + 1);  // dP(j) has been read
           if (!ok) break;
           if (elect_one()) {
-            accumulate(384, 128 * (j & 1), ring_mn + k.st * kStage, j == 0);  // dQ += dS K_j
-            tc_commit(bar(bars->empty[0]) + 8 * k.st);
+            accumulate(384, 128 * (j & 1), ring_mn + (j % NK) * kStage, j == 0);  // dQ += dS K_j
+            tc_commit(bar(bars->empty[0]) + 8 * (j % NK));
           }
           __syncwarp();
-          if (j + 2 < n) scores(j + 2, after(k1, 2));  // overwrites dS(j) after the MMAs above, in order
-          at = k1;
+          if (j + 2 < n) scores(j + 2);  // overwrites dS(j) after the MMAs above, in order
         }
       }
       steps += n;
@@ -385,7 +414,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     // ================= hands tiles on. dK/dV: lse2 and delta of the tile's rows; rows past the user's
     // end: weight 0, and zeros in the Q and dO tiles. dQ: zeros in the dropped rows of K.
     float* stat = reinterpret_cast<float*>(smem + L::oStat);
-    RingPos<NS> at;
+    uint32_t loaded = 0;
     int steps = 0;
     bool ok = true;
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
@@ -394,10 +423,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       MaskBytes mb;
       if (!dkv && it.n > 0) mb.load(a.mask, it.k0, it.k1, lane);
       for (int i = 0; ok && i < it.n; ++i, ++steps) {
-        const RingPos<NS> x = at;
-        at.next();
-        const RingPos<NS> y = at;
-        at.next();
+        const int x = dkv ? i % NQ : i % NK, y = dkv ? NQ + i % NQ : NK + i % NV;
+        const uint32_t xp = (loaded >> x) & 1u, yp = (loaded >> y) & 1u;
+        loaded ^= (1u << x) | (1u << y);
         if (dkv) {
           const int t = it.t0 + qt * tokens, rows = min(128, (it.t1 - t) * a.PG);
           const float2* src = a.stats + ((long long)(it.h * sharing + grp) * a.n_q + t) * a.PG;
@@ -405,23 +433,23 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
           for (int z = 0; z < 4; ++z)
             v[z] = lane + 32 * z < rows ? src[lane + 32 * z] : make_float2(INFINITY, 0.f);
-          ok = mbar_wait_warp(smem_u32(&bars->full[x.st]), x.ph, status, a.budget) &&
-               mbar_wait_warp(smem_u32(&bars->full[y.st]), y.ph, status, a.budget);
+          ok = mbar_wait_warp(smem_u32(&bars->full[x]), xp, status, a.budget) &&
+               mbar_wait_warp(smem_u32(&bars->full[y]), yp, status, a.budget);
           if (!ok) break;
           if (rows < 128) {
             uint32_t keep[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z)
               keep[z] = rows >= 32 * z + 32 ? ~0u : rows > 32 * z ? (1u << (rows - 32 * z)) - 1u : 0u;
-            zero_rows(smem + L::oRing + x.st * L::kTile, L::kBoxes, keep, lane);
-            zero_rows(smem + L::oRing + y.st * L::kTile, L::kBoxes, keep, lane);
+            zero_rows(smem + L::oRing + x * L::kTile, L::kBoxes, keep, lane);
+            zero_rows(smem + L::oRing + y * L::kTile, L::kBoxes, keep, lane);
             fence_proxy_async_smem();
           }
-          // slot steps mod 4 was last read four steps ago, whose tiles have left the ring
+          // the place of step - kStats was last read for its dS, before its tiles left the slots
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            stat[(steps & 3) * 256 + lane + 32 * z] = -v[z].x;
-            stat[(steps & 3) * 256 + 128 + lane + 32 * z] = -v[z].y;
+            stat[steps % L::kStats * 256 + lane + 32 * z] = -v[z].x;
+            stat[steps % L::kStats * 256 + 128 + lane + 32 * z] = -v[z].y;
           }
           if (++qt == it.aux) {
             qt = 0;
@@ -431,15 +459,17 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           uint32_t keep[4];
           const bool drop = mb.vote(a.mask, it.k0 + 128 * i, it.k1, lane, keep);
           if (i + 1 < it.n) mb.load(a.mask, it.k0 + 128 * (i + 1), it.k1, lane);
-          ok = mbar_wait_warp(smem_u32(&bars->full[x.st]), x.ph, status, a.budget);
+          ok = mbar_wait_warp(smem_u32(&bars->full[x]), xp, status, a.budget);
           if (!ok) break;
           if (drop) {
-            zero_rows(smem + L::oRing + x.st * L::kTile, L::kBoxes, keep, lane);
+            zero_rows(smem + L::oRing + x * L::kTile, L::kBoxes, keep, lane);
             fence_proxy_async_smem();
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->ready[steps & 7]));
+        // V too, after the fact: every load of a slot is waited for before its next use's
+        if (!dkv) ok = mbar_wait_warp(smem_u32(&bars->full[y]), yp, status, a.budget);
       }
     }
   } else if (warp == 3) {
@@ -503,7 +533,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const float c = a.c;
     const uint64_t c2 = f2_pack(c, c);
-    int steps = 0, own = 0;
+    int steps = 0, own = 0, pcnt = 0;
     uint32_t sph = 0;  // bit b: parity of the uses of S buffer b so far
     bool ok = true;
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
@@ -511,7 +541,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       const bool dkv = it.kind == kDkv;
       if (dkv) {
         const uint32_t ts = tmem + lane_off + 64 * w, tp = ts + 128;
-        for (int i = 0; i < n; ++i, ++steps) {
+        uint8_t* prow = smem + L::oP + w * kBox + r * 128;  // this row's 64 queries of P^T
+        for (int i = 0; i < n; ++i, ++steps, ++pcnt) {
           if (!mbar_wait_warp(smem_u32(&bars->ready[steps & 7]), (uint32_t)((steps >> 3) & 1), status, a.budget) ||
               !mbar_wait_warp(smem_u32(&bars->s_full[0]), sph & 1u, status, a.budget)) {
             ok = false;
@@ -520,12 +551,15 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           sph ^= 1u;
           tc_fence_after();
           const ulonglong2* st =
-              reinterpret_cast<const ulonglong2*>(smem + L::oStat + (steps & 3) * 1024 + 256 * w);
+              reinterpret_cast<const ulonglong2*>(smem + L::oStat + steps % L::kStats * 1024 + 256 * w);
           uint32_t v[2][32];
           tmem_ld32_raw(ts, v[0]);
           tmem_ld32_raw(ts + 32, v[1]);
           tmem_wait_tie(v[0]);
           tie32(v[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
           uint32_t pk[32];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {  // four columns: -lse2 of them in one load
@@ -545,9 +579,16 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             e[2] = __float_as_uint(p2);
             e[3] = __float_as_uint(p3);
           }
-          tmem_st32(ts, pk);
-          tc_wait_st();
-          tc_fence_before();
+          // dV of the step before has read P^T
+          if (!mbar_wait_warp(smem_u32(&bars->p_free), (uint32_t)((pcnt & 1) ^ 1), status, a.budget)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(prow + ((x ^ (r & 7)) << 4)) =
+                make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
           if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(steps & 1), status, a.budget)) {
@@ -764,7 +805,7 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.n_q = a.n_q;
   p.budget = kDefaultWaitBudget;
   static_assert(sizeof(Item) == 32, "the item ring");
-  constexpr size_t smem = 1024 + BSmem<D>::oBars + sizeof(BBars);
+  constexpr size_t smem = BSmem<D>::oBars + sizeof(BBars);
   static_assert(smem <= 227 * 1024, "shared memory");
   cudaError_t e = prepare_kernel<cross_bwd_kernel<D>>(smem, kRegsLaunch);
   if (e != cudaSuccess) return e;
