@@ -8,11 +8,10 @@
 // order that changes from run to run). So there are two kinds of item, each of which owns its
 // output and keeps it in TMEM, at 7 products a pair of tiles in place of 5 and no atomics on data:
 //   dK/dV: a tile of 128 keys of one key head against the user's packed query tiles (of every
-//     head group that shares it). S^T = K Q^T and dP^T = V dO^T put keys on the TMEM lanes. P^T goes
-//     to shared memory as the bf16 A operand of dV += P^T dO, which frees S^T as soon as it is in
-//     registers, so that the next tile's is computed meanwhile; dS^T, as bf16 over dP^T, is the A
-//     operand of dK += dS^T Q in place. The rows' lse2 and delta run along the columns and come
-//     from shared memory as broadcasts.
+//     head group that shares it). S^T = K Q^T and dP^T = V dO^T put keys on the TMEM lanes,
+//     so P^T and dS^T, written as bf16 over S^T and dP^T, are the A operands in place:
+//     dV += P^T dO, dK += dS^T Q. The rows' lse2 and delta run along the columns and come from
+//     shared memory as broadcasts. At d = 64 there is room for a second S^T.
 //   dQ: a tile of 128 packed query rows against the user's key tiles: S = Q K^T (two
 //     buffers), dP = dO V^T, dS over S, dQ += dS K. When there are fewer such items than SMs and
 //     many keys, `splits` of them share a tile and leave fp32 partials, summed in order.
@@ -23,10 +22,13 @@
 // it zeroes the rows that an MMA would multiply by 0 but must not read (dropped keys, rows past
 // the user's end), and loads lse2 and delta; warp 3 takes the items; warps 4-11 two warpgroups for
 // the elementwise step, 64 columns each, one thread per row. The tensor pipe runs ahead of the
-// elementwise step: dK/dV: S(i+1) as soon as S(i) is read, dV(i) when P(i) is stored, dK(i) and
-// dP(i+1) when dS(i) is; dQ: S(j+1) while tile j is in the elementwise step, then dP(j+1), dQ(j),
-// S(j+2). A key tile is held from S(j) to dQ(j), so three K and two V stages (one ring of
-// two pairs made every S wait for a load: 3,700 clocks a step).
+// elementwise step: dK/dV: dV(i) and the next free S when P(i) is stored, dK(i) and dP(i+1) when
+// dS(i) is, so the exponentials of tile i + 1 run while dK(i) and dP(i + 1) do; dQ: S(j+1) while
+// tile j is in the elementwise step, then dP(j+1), dQ(j), S(j+2).
+// K_j (and Q_i) is held from its first product to its last, V_j (dO_i) for half as long, so three
+// slots of the one and two of the other; one ring of two pairs made every S wait for a load
+// (3,700 clocks a step), and P^T through shared memory, which lets S^T go at once but
+// leaves two slots of each, no less (3,700).
 // Bound at d = 128: 2,048 tensor clocks a pair of tiles for dK/dV, 1,536 for dQ, 1,024
 // clocks of exponentials in both.
 #include <cmath>
@@ -42,32 +44,29 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kRegsLaunch = 168, kRegsControl = 72, kRegsElem = 216;  // setmaxnreg draws on the launch's
 static_assert(128 * kRegsControl + 256 * kRegsElem <= kThreads * kRegsLaunch,
               "register split exceeds the launch allocation");
-// TMEM columns: dK/dV items: S^T 0, dP^T 128, dV 256, dK 384; dQ items: S 0 and 128, dP 256, dQ 384
-constexpr uint32_t kColAcc = 256;  // from here on: what an epilogue reads, or a dQ item's dP
-
-// Shared memory: the item's own tiles (K, V of dK/dV; Q, dO of dQ), then slots of a tile each,
-// which the two kinds of item use in their own way:
-//   dK/dV: NQ slots of Q_i, NQ of dO_i, and (d = 128) the last one for P^T, which has its own
-//          place at d = 64; dQ: NK slots of K_j, NV of V_j.
+// Shared memory: the item's own tiles (K, V of dK/dV; Q, dO of dQ), then slots of a tile each: NK of
+// Q_i or K_j, NV of dO_i or V_j. TMEM columns: dQ items: S 0 and 128, dP 256, dQ 384; dK/dV
+// items: S^T, dP^T, dV, dK as below (what an epilogue reads starts at 256 or later).
 template <int D>
 struct BSmem {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTile = kBoxes * kBox;
   static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr int NK = D == 128 ? 3 : 5, NV = kSlots - NK, NQ = D == 128 ? 2 : 3;
-  static constexpr int kStats = D == 128 ? 2 : 4;  // NQ steps at least can hold theirs
+  static constexpr int NK = D == 128 ? 3 : 5, NV = kSlots - NK;
   static constexpr int oA = 0;
   static constexpr int oRing = 2 * kTile;
-  static constexpr int oP = D == 128 ? oRing + 4 * kTile : oRing + kSlots * kTile;
-  static constexpr int oStat = D == 128 ? oRing + kSlots * kTile : oP + 2 * kBox;
-  static constexpr int oItems = oStat + kStats * 256 * 4;  // a step: 128 of -lse2, 128 of -delta
+  static constexpr int oStat = oRing + kSlots * kTile;
+  static constexpr int oItems = oStat + 2 * 256 * 4;  // a step: 128 of -lse2, 128 of -delta
   static constexpr int oBars = oItems + 2 * 32;
+  static constexpr int kSBufs = D == 128 ? 1 : 2;
+  static constexpr uint32_t cP = 128 * kSBufs, cDV = cP + 128, cDK = cDV + D;
 };
+constexpr uint32_t kColDp = 256, kColDq = 384;
 
 struct BBars {
   uint64_t own, own_empty, full[8], empty[8];
   uint64_t ready[8];    // by step mod 8: fewer steps' tiles than that are in the slots
-  uint64_t s_full[2], s_free, dp_full, p_full, p_free, ds_full, done, acc_free;
+  uint64_t s_full[2], dp_full, p_full, ds_full[2], done, acc_free;
   uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
 };
@@ -159,7 +158,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                  const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  const __grid_constant__ BwdParams a) {
   using L = BSmem<D>;
-  constexpr int NK = L::NK, NV = L::NV, NQ = L::NQ;
+  constexpr int NK = L::NK, NV = L::NV;
   // d = 128 leaves no room to align by hand; the swizzle needs 1024 bytes, which dynamic shared
   // memory has when a kernel has no other (checked below)
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -186,10 +185,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
     }
     mbar_init(smem_u32(&bars->dp_full), 1);
-    mbar_init(smem_u32(&bars->s_free), 8);
     mbar_init(smem_u32(&bars->p_full), 8);
-    mbar_init(smem_u32(&bars->p_free), 1);
-    mbar_init(smem_u32(&bars->ds_full), 8);
+    mbar_init(smem_u32(&bars->ds_full[0]), 8);
+    mbar_init(smem_u32(&bars->ds_full[1]), 8);
     mbar_init(smem_u32(&bars->done), 1);
     mbar_init(smem_u32(&bars->acc_free), 8);
     fence_mbar_init();
@@ -235,16 +233,12 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             tma_load_3d(sbase + L::oA + L::kTile + b * kBox, mb, b * 64, y, z, ob);
           }
         }
-        if (D == 128 && dkv && ok) {  // the slot of P: free of the item before
-          ok = mbar_wait(smem_u32(&bars->empty[4]), ((used >> 4) & 1u) ^ 1u, status, a.budget);
-          used ^= 1u << 4;
-        }
         int grp = 0, qt = 0;
         for (int x = 0; ok && x < it.n; ++x) {
           const int y = dkv ? (it.h * sharing + grp) * a.PG : it.h * a.PG / a.G;
           const int z = dkv ? it.t0 + qt * tokens : it.k0 + 128 * x;
           for (int v = 0; v < 2; ++v) {
-            const int st = dkv ? v * NQ + x % NQ : v ? NK + x % NV : x % NK;
+            const int st = v ? NK + x % NV : x % NK;
             ok = ok && mbar_wait(smem_u32(&bars->empty[st]), ((used >> st) & 1u) ^ 1u, status, a.budget);
             if (!ok) break;
             const uint32_t fb = smem_u32(&bars->full[st]);
@@ -278,7 +272,6 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       return br + (uint32_t)(reinterpret_cast<const uint8_t*>(&b) - reinterpret_cast<const uint8_t*>(bars));
     };
     const uint32_t own_k = desc_k(sb0 + L::oA), ring_k = desc_k(sb0 + L::oRing), ring_mn = desc_mn(sb0 + L::oRing);
-    const uint32_t p_k = desc_k(sb0 + L::oP);
     uint32_t loaded = 0;                // bit: parity of a slot's loads before
     int own = 0, steps = 0, pcnt = 0;   // items with steps, steps, dK/dV steps before
     bool ok = true;
@@ -310,50 +303,44 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         tc_fence_after();
       };
       if (dkv) {
-        // own: K, V; slots: Q_i in i mod NQ, dO_i in NQ + i mod NQ
+        // own: K, V; slots: Q_i in i mod NK, dO_i in NK + i mod NV
+        constexpr int NB = L::kSBufs;
         auto scores = [&](int i) {  // S^T = K Q_i^T
           wait_ready(i);
+          const uint32_t sb = NB == 1 ? 0 : i & 1;
           if (ok && elect_one()) {
-            product_ss<D>(tm, own_k, ring_k + (i % NQ) * kStage, id_s);
-            tc_commit(bar(bars->s_full[0]));
+            product_ss<D>(tm + 128 * sb, own_k, ring_k + (i % NK) * kStage, id_s);
+            tc_commit(bar(bars->s_full[0]) + 8 * sb);
           }
           __syncwarp();
         };
         auto dprob = [&](int i) {  // dP^T = V dO_i^T
           if (ok && elect_one()) {
-            product_ss<D>(tm + 128, own_k + kStage, ring_k + (NQ + i % NQ) * kStage, id_s);
+            product_ss<D>(tm + L::cP, own_k + kStage, ring_k + (NK + i % NV) * kStage, id_s);
             tc_commit(bar(bars->dp_full));
-            if (i == n - 1) tc_commit(bar(bars->own_empty));
+            if (i == n - 1) tc_commit(bar(bars->own_empty));  // (every S of the item precedes its last dP)
           }
           __syncwarp();
         };
         scores(0);
         dprob(0);
+        if (NB == 2 && n > 1) scores(1);
         wait_acc();
         for (int i = 0; ok && i < n; ++i) {
-          const int q = i % NQ, g = NQ + i % NQ;
-          if (i + 1 < n) {  // S(i) is in registers
-            if (!wait(bar(bars->s_free), (uint32_t)(pcnt & 1))) break;
-            scores(i + 1);
-          }
+          const int q = i % NK, g = NK + i % NV;
           if (!wait(bar(bars->p_full), (uint32_t)(pcnt & 1))) break;
           ++pcnt;
           tc_fence_after();
-          if (elect_one()) {  // dV += P^T dO_i
-            const uint32_t b = ring_mn + g * kStage;
-            if (i == 0) mma_ss<0>(tm + kColAcc, p_k, b, kDescHi, id_o);
-            else mma_ss<1>(tm + kColAcc, p_k, b, kDescHi, id_o);
-#pragma unroll
-            for (int ks = 1; ks < 8; ++ks) mma_ss<1>(tm + kColAcc, p_k + kstep(ks), b + mn_step(ks), kDescHi, id_o);
-            tc_commit(bar(bars->p_free));
+          if (elect_one()) {
+            accumulate(L::cDV, NB == 1 ? 0 : 128 * (i & 1), ring_mn + g * kStage, i == 0);  // dV += P^T dO_i
             tc_commit(bar(bars->empty[0]) + 8 * g);
-            if (D == 128 && i == n - 1) tc_commit(bar(bars->empty[4]));
           }
           __syncwarp();
-          if (!wait(bar(bars->ds_full), (uint32_t)((steps + i) & 1))) break;
+          if (i + NB < n) scores(i + NB);  // overwrites P^T after the MMAs above, in order
+          if (!wait(bar(bars->ds_full[0]) + 8 * ((steps + i) & 1), (uint32_t)(((steps + i) >> 1) & 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            accumulate(384, 128, ring_mn + q * kStage, i == 0);  // dK += dS^T Q_i
+            accumulate(L::cDK, L::cP, ring_mn + q * kStage, i == 0);  // dK += dS^T Q_i
             tc_commit(bar(bars->empty[0]) + 8 * q);
           }
           __syncwarp();
@@ -377,7 +364,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           loaded ^= 1u << v;
           tc_fence_after();
           if (elect_one()) {
-            product_ss<D>(tm + kColAcc, own_k + kStage, ring_k + v * kStage, id_s);
+            product_ss<D>(tm + kColDp, own_k + kStage, ring_k + v * kStage, id_s);
             tc_commit(bar(bars->dp_full));
             tc_commit(bar(bars->empty[0]) + 8 * v);
             if (j == n - 1) tc_commit(bar(bars->own_empty));  // (every S of the item precedes its last dP)
@@ -389,12 +376,12 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         dprob(0);
         if (n > 1) scores(1);
         for (int j = 0; ok && j < n; ++j) {
-          if (!wait(bar(bars->ds_full), (uint32_t)((steps + j) & 1))) break;
+          if (!wait(bar(bars->ds_full[0]) + 8 * ((steps + j) & 1), (uint32_t)(((steps + j) >> 1) & 1))) break;
           tc_fence_after();
           if (j + 1 < n) dprob(j + 1);  // dP(j) has been read
           if (!ok) break;
           if (elect_one()) {
-            accumulate(384, 128 * (j & 1), ring_mn + (j % NK) * kStage, j == 0);  // dQ += dS K_j
+            accumulate(kColDq, 128 * (j & 1), ring_mn + (j % NK) * kStage, j == 0);  // dQ += dS K_j
             tc_commit(bar(bars->empty[0]) + 8 * (j % NK));
           }
           __syncwarp();
@@ -423,7 +410,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       MaskBytes mb;
       if (!dkv && it.n > 0) mb.load(a.mask, it.k0, it.k1, lane);
       for (int i = 0; ok && i < it.n; ++i, ++steps) {
-        const int x = dkv ? i % NQ : i % NK, y = dkv ? NQ + i % NQ : NK + i % NV;
+        const int x = i % NK, y = NK + i % NV;
         const uint32_t xp = (loaded >> x) & 1u, yp = (loaded >> y) & 1u;
         loaded ^= (1u << x) | (1u << y);
         if (dkv) {
@@ -445,11 +432,14 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             zero_rows(smem + L::oRing + y * L::kTile, L::kBoxes, keep, lane);
             fence_proxy_async_smem();
           }
-          // the place of step - kStats was last read for its dS, before its tiles left the slots
+          // the place of two steps ago has been read for its dS
+          ok = steps < 2 || mbar_wait_warp(smem_u32(&bars->ds_full[steps & 1]), (uint32_t)(((steps >> 1) & 1) ^ 1),
+                                           status, a.budget);
+          if (!ok) break;
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            stat[steps % L::kStats * 256 + lane + 32 * z] = -v[z].x;
-            stat[steps % L::kStats * 256 + 128 + lane + 32 * z] = -v[z].y;
+            stat[(steps & 1) * 256 + lane + 32 * z] = -v[z].x;
+            stat[(steps & 1) * 256 + 128 + lane + 32 * z] = -v[z].y;
           }
           if (++qt == it.aux) {
             qt = 0;
@@ -533,33 +523,31 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const float c = a.c;
     const uint64_t c2 = f2_pack(c, c);
-    int steps = 0, own = 0, pcnt = 0;
+    int steps = 0, own = 0;
     uint32_t sph = 0;  // bit b: parity of the uses of S buffer b so far
     bool ok = true;
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const int n = it.n;
       const bool dkv = it.kind == kDkv;
       if (dkv) {
-        const uint32_t ts = tmem + lane_off + 64 * w, tp = ts + 128;
-        uint8_t* prow = smem + L::oP + w * kBox + r * 128;  // this row's 64 queries of P^T
-        for (int i = 0; i < n; ++i, ++steps, ++pcnt) {
+        const uint32_t tp = tmem + lane_off + 64 * w + L::cP;
+        for (int i = 0; i < n; ++i, ++steps) {
           if (!mbar_wait_warp(smem_u32(&bars->ready[steps & 7]), (uint32_t)((steps >> 3) & 1), status, a.budget) ||
-              !mbar_wait_warp(smem_u32(&bars->s_full[0]), sph & 1u, status, a.budget)) {
+              !mbar_wait_warp(smem_u32(&bars->s_full[L::kSBufs == 1 ? 0 : i & 1]),
+                              (sph >> (L::kSBufs == 1 ? 0 : i & 1)) & 1u, status, a.budget)) {
             ok = false;
             break;
           }
-          sph ^= 1u;
+          sph ^= 1u << (L::kSBufs == 1 ? 0 : i & 1);
+          const uint32_t ts = tmem + lane_off + 64 * w + (L::kSBufs == 1 ? 0 : 128 * (i & 1));
           tc_fence_after();
           const ulonglong2* st =
-              reinterpret_cast<const ulonglong2*>(smem + L::oStat + steps % L::kStats * 1024 + 256 * w);
+              reinterpret_cast<const ulonglong2*>(smem + L::oStat + (steps & 1) * 1024 + 256 * w);
           uint32_t v[2][32];
           tmem_ld32_raw(ts, v[0]);
           tmem_ld32_raw(ts + 32, v[1]);
           tmem_wait_tie(v[0]);
           tie32(v[1]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
           uint32_t pk[32];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {  // four columns: -lse2 of them in one load
@@ -579,16 +567,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             e[2] = __float_as_uint(p2);
             e[3] = __float_as_uint(p3);
           }
-          // dV of the step before has read P^T
-          if (!mbar_wait_warp(smem_u32(&bars->p_free), (uint32_t)((pcnt & 1) ^ 1), status, a.budget)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<uint4*>(prow + ((x ^ (r & 7)) << 4)) =
-                make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-          fence_proxy_async_smem();
+          tmem_st32(ts, pk);
+          tc_wait_st();
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
           if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(steps & 1), status, a.budget)) {
@@ -619,10 +600,10 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[steps & 1]));
         }
       } else {
-        const uint32_t tp = tmem + lane_off + kColAcc + 64 * w;
+        const uint32_t tp = tmem + lane_off + kColDp + 64 * w;
         const int t = it.t0 + r / a.PG;
         float lse2 = INFINITY, delta = 0.f;
         if (t < it.t1) {
@@ -688,7 +669,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+          if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full[steps & 1]));
         }
       }
       // ---- the accumulators are complete
@@ -708,13 +689,13 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const int j = it.k0 + r;
         const bool zero = a.mask && j < it.k1 && a.mask[j] == 0;
         __nv_bfloat16* out = w ? a.dK : a.dV;
-        write_rows<D>(tmem + lane_off + kColAcc + 128 * w, have, zero, w ? a.scale : 1.f,
+        write_rows<D>(tmem + lane_off + (w ? L::cDK : L::cDV), have, zero, w ? a.scale : 1.f,
                       [&](int i) -> __nv_bfloat16* {
                         const int row = it.k0 + q4 * 32 + i;
                         return row < it.k1 ? out + ((long long)row * a.Hkv + it.h) * D : nullptr;
                       }, freed, lane);
       } else if (a.splits == 1) {  // each warpgroup writes half of the columns
-        write_rows<D / 2>(tmem + lane_off + 384 + w * (D / 2), have, false, a.scale,
+        write_rows<D / 2>(tmem + lane_off + kColDq + w * (D / 2), have, false, a.scale,
                           [&](int i) -> __nv_bfloat16* {
                             const int x = q4 * 32 + i, t = it.t0 + x / a.PG;
                             return t < it.t1 ? a.dQ + ((long long)t * a.H + it.h * a.PG + x % a.PG) * D + w * (D / 2)
@@ -727,7 +708,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         for (int x = 0; x < D / 2; x += 16) {
           uint32_t o[16];
           if (have) {
-            tmem_ld16(tmem + lane_off + 384 + w * (D / 2) + x, o);
+            tmem_ld16(tmem + lane_off + kColDq + w * (D / 2) + x, o);
             tmem_wait16(o);
           }
           if (x + 16 == D / 2) freed();
