@@ -290,7 +290,10 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const int n = broadcast(it.n);
       const bool dkv = broadcast(it.kind) == kDkv;
-      if (n == 0) continue;
+      if (n == 0) {  // (a wait by parity tells adjacent phases apart: each is waited for, in order)
+        if (s > 0) wait(bar(bars->acc_free), (uint32_t)((s - 1) & 1));
+        continue;
+      }
       wait(bar(bars->own), (uint32_t)(own & 1));
       ++own;
       auto wait_ready = [&](int i) {

@@ -63,6 +63,9 @@ struct FBars {
   uint64_t q_full, q_empty, full[8], empty[8];
   uint64_t v_ready[8];  // by V tile mod 8: fewer V tiles than that fit in the ring
   uint64_t s_full[3], o_done[2];
+  // an item's last output of each accumulator: o_done may be two phases behind there (a third score
+  // buffer lets a warpgroup run ahead), and a wait by parity tells adjacent phases apart only
+  uint64_t o_last[2];
   uint64_t p_full[3][2];  // [buffer][half of the keys]: the second product starts on the first half
   uint64_t o_free, merge, drain;
   uint64_t item_full[2], item_empty[2];
@@ -145,6 +148,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(smem_u32(&bars->o_done[w]), 1);
+      mbar_init(smem_u32(&bars->o_last[w]), 1);
       mbar_init(smem_u32(&bars->item_full[w]), 1);
       mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
     }
@@ -235,7 +239,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const bool two = broadcast(it.two);
       const int n = broadcast(it.n), steps = two ? 2 * n : n;
-      if (n == 0) continue;
+      if (n == 0) {  // (every phase of o_free is waited for, in order: see o_last)
+        if (s > 0) wait(bar(bars->o_free), (uint32_t)((s - 1) & 1));
+        continue;
+      }
       wait(bar(bars->q_full), (uint32_t)(nq & 1));
       ++nq;
       auto scores = [&](int q) {
@@ -279,6 +286,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
           for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
           tc_commit(bar(bars->o_done[0]) + 8 * w);
+          if (q + 2 >= steps) tc_commit(bar(bars->o_last[0]) + 8 * w);
           if (last_use) tc_commit(bar(bars->empty[0]) + 8 * vpos.st);
         }
         __syncwarp();
@@ -310,7 +318,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         uint32_t keep[4];
         const bool drop = mb.vote(a.mask, it.k0 + 128 * j, it.k1, lane, keep);
         if (j + 1 < it.n) mb.load(a.mask, it.k0 + 128 * (j + 1), it.k1, lane);
-        ok = mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
+        // K first: a stage holds K and V in turn, and a wait by parity needs the use before this
+        // one to be over
+        ok = mbar_wait_warp(smem_u32(&bars->full[(i - 1) % NS]), (uint32_t)(((i - 1) / NS) & 1), status, a.budget) &&
+             mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
         if (!ok) break;
         if (drop) {
           zero_rows(smem + L::oKV + st * L::kTile, L::kBoxes, keep, lane);
@@ -372,7 +383,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const uint32_t ot = tmem + lane_off + L::kColO + D * w;
     const float c = a.c;
     bool ok = true;
-    int cnt = 0, singles = 0;  // this warpgroup's steps so far; items of one tile so far
+    int cnt = 0, singles = 0, lasts = 0;  // this warpgroup's steps, items of one tile, items with steps
     RingPos<kNB> base;         // the score buffer of the item's step 0
     for (int s = 0; ok; ++s) {
     // the item stays in the ring while it is worked on: registers are short here
@@ -469,15 +480,19 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       l += l0 + l1;
     }
     // ---- this tile's (or half's) accumulator is complete
-    if (ok && n > 0)
-      ok = mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((cnt - 1) & 1), status, a.budget);
+    if (ok && n > 0) {
+      ok = mbar_wait_warp(smem_u32(&bars->o_last[w]), (uint32_t)(lasts & 1), status, a.budget);
+      ++lasts;
+    }
     tc_fence_after();
     float* ml = reinterpret_cast<float*>(smem + L::oML);
     float g0 = 1.f, g1 = 0.f;  // factors of O_0 and O_1 (two tiles: of this tile's own)
+    // the item before has been written, so warpgroup 0 has read its m and l (waited for at every
+    // item: phase by phase)
+    if (w == 1)
+      ok = ok && (s == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
     if (!two) {
       if (w == 1) {
-        // the item before has been written, so warpgroup 0 has read its m and l
-        ok = ok && (s == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
         ml[r] = m;
         ml[128 + r] = ok ? l : 0.f;
         tc_fence_before();
