@@ -117,9 +117,9 @@ def _load() -> ctypes.CDLL:
     lib.sa_cross_attn_workspace_size.argtypes = [i32, i64, i64, i32, i32, i32, i32]
     cross = [vp, i64, vp, i32, i64, i32, i32, vp, i64, vp, i64, vp, i64, i32, vp, f32]
     lib.sa_cross_attn_forward.restype = i32
-    lib.sa_cross_attn_forward.argtypes = cross + [vp, vp, vp, sz, vp]
+    lib.sa_cross_attn_forward.argtypes = cross + [vp, vp, vp, vp, sz, vp]
     lib.sa_cross_attn_backward.restype = i32
-    lib.sa_cross_attn_backward.argtypes = cross + [vp] * 7 + [sz, vp]
+    lib.sa_cross_attn_backward.argtypes = cross + [vp] * 8 + [sz, vp]
     lib.sa_page_tables.restype = i32
     lib.sa_page_tables.argtypes = [vp, vp, i32, i32, vp, i64, vp, vp, i32, i64, vp, vp, vp, vp, vp,
                                    sz, vp]
@@ -286,19 +286,20 @@ def sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, backward) -> int:
 
 
 def sa_cross_attn_forward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V, v_stride,
-                          kv_offsets, n_kv, Hkv, key_mask, scale, out, lse, workspace, ws_bytes,
-                          stream) -> int:
+                          kv_offsets, n_kv, Hkv, key_mask, scale, out, out_rest, lse, workspace,
+                          ws_bytes, stream) -> int:
     return int(_lib.sa_cross_attn_forward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V,
                                           v_stride, kv_offsets, n_kv, Hkv, key_mask, scale, out,
-                                          lse, workspace, ws_bytes, stream))
+                                          out_rest, lse, workspace, ws_bytes, stream))
 
 
 def sa_cross_attn_backward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V, v_stride,
-                           kv_offsets, n_kv, Hkv, key_mask, scale, out, lse, dout, dQ, dK, dV,
-                           workspace, ws_bytes, stream) -> int:
+                           kv_offsets, n_kv, Hkv, key_mask, scale, out, out_rest, lse, dout, dQ,
+                           dK, dV, workspace, ws_bytes, stream) -> int:
     return int(_lib.sa_cross_attn_backward(Q, q_stride, q_offsets, R, n_q, H, d, K, k_stride, V,
                                            v_stride, kv_offsets, n_kv, Hkv, key_mask, scale, out,
-                                           lse, dout, dQ, dK, dV, workspace, ws_bytes, stream))
+                                           out_rest, lse, dout, dQ, dK, dV, workspace, ws_bytes,
+                                           stream))
 
 
 def sa_page_tables(cached_lens, new_lens, R, page_size, free_pages, n_free, free_used, block_table,
@@ -801,22 +802,27 @@ def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
 
 def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V: torch.Tensor,
                     kv_offsets: torch.Tensor, *, key_mask: torch.Tensor | None = None,
-                    scale: float | None = None, out: dict | None = None,
+                    scale: float | None = None, want_rest: bool = True, out: dict | None = None,
                     ws: torch.Tensor | None = None, stream=None) -> dict:
     """Multi-head cross attention from user u's query rows Q[q_offsets[u]:q_offsets[u+1]] to its
     key rows K, V[kv_offsets[u]:kv_offsets[u+1]] (sa_cross_attn_forward). Q [n_q, H, d], K and V
     [n_kv, Hkv, d] bf16 (rows may be strided, a row's heads contiguous), offsets [R + 1] int64,
     key_mask [n_kv] bool (False drops a key row), scale 1 / sqrt(d) by default. Returns out
-    [n_q, H, d] bf16 and lse [n_q, H] fp32, written into `out` ({"out", "lse"}) when given."""
+    [n_q, H, d] bf16, lse [n_q, H] fp32 and, for the backward, what rounding took from out (rest,
+    like out; want_rest=False leaves it away). They are written into `out` ({"out", "lse"} and,
+    if wanted, "rest") when given."""
     where = "cross_attention"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
                                                               key_mask)
     if out is None:
         out = {"out": torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16),
                "lse": torch.empty(n_q, H, device=dev, dtype=torch.float32)}
+        if want_rest:
+            out["rest"] = torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16)
     else:
         out = dict(out)
         _check_tensor(where, "out", out.get("out"), (n_q, H, d), torch.bfloat16, dev)
+        _check_tensor(where, "rest", out.get("rest"), (n_q, H, d), torch.bfloat16, dev, optional=True)
         _check_tensor(where, "lse", out.get("lse"), (n_q, H), torch.float32, dev)
     with _device(dev):
         if ws is None:
@@ -826,8 +832,8 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         st = sa_cross_attn_forward(_ptr(Q), qs, _ptr(q_offsets), R, n_q, H, d, _ptr(K), ks, _ptr(V),
                                    vs, _ptr(kv_offsets), n_kv, Hkv, _ptr(key_mask),
-                                   _scale(scale, d), _ptr(out["out"]), _ptr(out["lse"]), _ptr(ws),
-                                   ws.nbytes, _stream(stream, dev))
+                                   _scale(scale, d), _ptr(out["out"]), _ptr(out.get("rest")),
+                                   _ptr(out["lse"]), _ptr(ws), ws.nbytes, _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_forward")
     out["_ws"] = ws
@@ -839,7 +845,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
                              dout: torch.Tensor, *, key_mask: torch.Tensor | None = None,
                              scale: float | None = None, out: dict | None = None,
                              ws: torch.Tensor | None = None, stream=None) -> dict:
-    """Gradients of cross_attention given its outputs `fwd` (out, lse) and dout = dL/dout
+    """Gradients of cross_attention given its outputs `fwd` (out, lse, rest if it has one) and dout = dL/dout
     [n_q, H, d] bf16: dQ [n_q, H, d], dK and dV [n_kv, Hkv, d], bf16 (sa_cross_attn_backward),
     written into `out` ({"dQ", "dK", "dV"}) when given. Other arguments as passed to the
     forward."""
@@ -849,6 +855,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     bf = torch.bfloat16
     _check_tensor(where, "out", fwd.get("out"), (n_q, H, d), bf, dev)
     _check_tensor(where, "lse", fwd.get("lse"), (n_q, H), torch.float32, dev)
+    _check_tensor(where, "rest", fwd.get("rest"), (n_q, H, d), bf, dev, optional=True)
     _check_tensor(where, "dout", dout, (n_q, H, d), bf, dev)
     if out is None:
         out = {"dQ": torch.empty(n_q, H, d, device=dev, dtype=bf),
@@ -867,8 +874,8 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         st = sa_cross_attn_backward(_ptr(Q), qs, _ptr(q_offsets), R, n_q, H, d, _ptr(K), ks,
                                     _ptr(V), vs, _ptr(kv_offsets), n_kv, Hkv, _ptr(key_mask),
-                                    _scale(scale, d), _ptr(fwd["out"]), _ptr(fwd["lse"]),
-                                    _ptr(dout), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]),
+                                    _scale(scale, d), _ptr(fwd["out"]), _ptr(fwd.get("rest")),
+                                    _ptr(fwd["lse"]), _ptr(dout), _ptr(out["dQ"]), _ptr(out["dK"]), _ptr(out["dV"]),
                                     _ptr(ws), ws.nbytes, _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_backward")

@@ -55,7 +55,7 @@ int check_cross(const CrossArgs& a) {
   if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return SA_ERR_INVALID_ARG;
   if (!a.qoff || !a.koff || (a.n_q > 0 && (!a.Q || !a.out || !a.lse)) || (a.n_kv > 0 && (!a.K || !a.V)))
     return SA_ERR_INVALID_ARG;
-  if (!on16(a.Q) || !on16(a.K) || !on16(a.V) || !on16(a.out) || !on16(a.lse) || !on8(a.qoff) ||
+  if (!on16(a.Q) || !on16(a.K) || !on16(a.V) || !on16(a.out) || !on16(a.rest) || !on16(a.lse) || !on8(a.qoff) ||
       !on8(a.koff))
     return SA_ERR_INVALID_ARG;
   if (a.q_stride < (long long)a.H * a.d || a.k_stride < (long long)a.Hkv * a.d ||
@@ -83,7 +83,8 @@ int sa_cross_attn_forward(const void* Q, int64_t q_stride, const int64_t* q_offs
                           int64_t n_q, int H, int d, const void* K, int64_t k_stride,
                           const void* V, int64_t v_stride, const int64_t* kv_offsets,
                           int64_t n_kv, int Hkv, const uint8_t* key_mask, float scale, void* out,
-                          float* lse, void* workspace, size_t ws_bytes, void* stream) {
+                          void* out_rest, float* lse, void* workspace, size_t ws_bytes,
+                          void* stream) {
   CrossArgs a = {};
   a.Q = Q;
   a.K = K;
@@ -102,6 +103,7 @@ int sa_cross_attn_forward(const void* Q, int64_t q_stride, const int64_t* q_offs
   a.mask = key_mask;
   a.scale = scale;
   a.out = out;
+  a.rest = out_rest;
   a.lse = lse;
   int st = check_cross(a);
   if (st != SA_OK || (st = device_sms(&a.sms)) != SA_OK) return st;
@@ -115,8 +117,9 @@ int sa_cross_attn_backward(const void* Q, int64_t q_stride, const int64_t* q_off
                            int64_t n_q, int H, int d, const void* K, int64_t k_stride,
                            const void* V, int64_t v_stride, const int64_t* kv_offsets,
                            int64_t n_kv, int Hkv, const uint8_t* key_mask, float scale,
-                           const void* out, const float* lse, const void* dout, void* dQ, void* dK,
-                           void* dV, void* workspace, size_t ws_bytes, void* stream) {
+                           const void* out, const void* out_rest, const float* lse,
+                           const void* dout, void* dQ, void* dK, void* dV, void* workspace,
+                           size_t ws_bytes, void* stream) {
   CrossArgs a = {};
   a.Q = Q;
   a.K = K;
@@ -135,6 +138,7 @@ int sa_cross_attn_backward(const void* Q, int64_t q_stride, const int64_t* q_off
   a.mask = key_mask;
   a.scale = scale;
   a.out = const_cast<void*>(out);
+  a.rest = const_cast<void*>(out_rest);
   a.lse = const_cast<float*>(lse);
   a.dout = dout;
   a.dQ = dQ;

@@ -102,6 +102,16 @@ __device__ __forceinline__ void stats_rows(const CrossArgs& a, int pg, long long
         s = fmaf(__uint_as_float(u[z] & 0xffff0000u), __uint_as_float(v[z] & 0xffff0000u), s);
       }
     }
+    if (i < rows && a.rest) {
+      const uint4 x = reinterpret_cast<const uint4*>(a.dout)[i * LANES + lane];
+      const uint4 y = reinterpret_cast<const uint4*>(a.rest)[i * LANES + lane];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        s = fmaf(__uint_as_float(u[z] << 16), __uint_as_float(v[z] << 16), s);
+        s = fmaf(__uint_as_float(u[z] & 0xffff0000u), __uint_as_float(v[z] & 0xffff0000u), s);
+      }
+    }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (i < rows && lane == 0) {

@@ -66,7 +66,7 @@ constexpr uint32_t kColDp = 256, kColDq = 384;
 struct BBars {
   uint64_t own, own_empty, full[8], empty[8];
   uint64_t ready[8];    // by step mod 8: fewer steps' tiles than that are in the slots
-  uint64_t s_full[2], dp_full, p_full, ds_full[2], done, acc_free;
+  uint64_t s_full[2], dp_full, p_full[2], ds_full[2], done, acc_free;
   uint64_t item_full[2], item_empty[2];
   uint32_t tmem_base;
 };
@@ -176,7 +176,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     mbar_init(smem_u32(&bars->own_empty), 1);
     for (int s = 0; s < 8; ++s) {
       mbar_init(smem_u32(&bars->full[s]), 1);
-      mbar_init(smem_u32(&bars->empty[s]), 1);
+      mbar_init(smem_u32(&bars->empty[s]), s < NK ? 1 : 2);  // the last MMA that reads it; NK..: and warp 2
       mbar_init(smem_u32(&bars->ready[s]), 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -185,7 +185,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(smem_u32(&bars->item_empty[w]), kConsumers);
     }
     mbar_init(smem_u32(&bars->dp_full), 1);
-    mbar_init(smem_u32(&bars->p_full), 8);
+    mbar_init(smem_u32(&bars->p_full[0]), 8);
+    mbar_init(smem_u32(&bars->p_full[1]), 8);
     mbar_init(smem_u32(&bars->ds_full[0]), 8);
     mbar_init(smem_u32(&bars->ds_full[1]), 8);
     mbar_init(smem_u32(&bars->done), 1);
@@ -273,7 +274,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     };
     const uint32_t own_k = desc_k(sb0 + L::oA), ring_k = desc_k(sb0 + L::oRing), ring_mn = desc_mn(sb0 + L::oRing);
     uint32_t loaded = 0;                // bit: parity of a slot's loads before
-    int own = 0, steps = 0, pcnt = 0;   // items with steps, steps, dK/dV steps before
+    uint32_t pph = 0;                   // bit: parity of the uses of an S^T buffer before
+    int own = 0, steps = 0;             // items with steps, steps before
     bool ok = true;
     auto wait = [&](uint32_t b, uint32_t parity) {
       ok = ok && mbar_wait_warp(b, parity, status, a.budget);
@@ -290,10 +292,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const int n = broadcast(it.n);
       const bool dkv = broadcast(it.kind) == kDkv;
-      if (n == 0) {  // (a wait by parity tells adjacent phases apart: each is waited for, in order)
-        if (s > 0) wait(bar(bars->acc_free), (uint32_t)((s - 1) & 1));
-        continue;
-      }
+      if (n == 0) continue;
       wait(bar(bars->own), (uint32_t)(own & 1));
       ++own;
       auto wait_ready = [&](int i) {
@@ -301,8 +300,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         wait(bar(bars->ready[0]) + 8 * (x & 7), (uint32_t)((x >> 3) & 1));
         tc_fence_after();
       };
-      auto wait_acc = [&]() {  // the accumulators of the item before have been read
-        if (s > 0) wait(bar(bars->acc_free), (uint32_t)((s - 1) & 1));
+      auto wait_acc = [&]() {  // the accumulators of the item with steps before have been read
+        if (own > 1) wait(bar(bars->acc_free), (uint32_t)(own & 1));
         tc_fence_after();
       };
       if (dkv) {
@@ -331,8 +330,9 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         wait_acc();
         for (int i = 0; ok && i < n; ++i) {
           const int q = i % NK, g = NK + i % NV;
-          if (!wait(bar(bars->p_full), (uint32_t)(pcnt & 1))) break;
-          ++pcnt;
+          const int pb = NB == 1 ? 0 : i & 1;
+          if (!wait(bar(bars->p_full[0]) + 8 * pb, (pph >> pb) & 1u)) break;
+          pph ^= 1u << pb;
           tc_fence_after();
           if (elect_one()) {
             accumulate(L::cDV, NB == 1 ? 0 : 128 * (i & 1), ring_mn + g * kStage, i == 0);  // dV += P^T dO_i
@@ -435,7 +435,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             zero_rows(smem + L::oRing + y * L::kTile, L::kBoxes, keep, lane);
             fence_proxy_async_smem();
           }
-          // the place of two steps ago has been read for its dS
+          // the place of two steps ago has been read for its dS (an item's tiles are loaded after the last
+          // dP of the item before, so the phase before this one is over at an item's first steps too)
           ok = steps < 2 || mbar_wait_warp(smem_u32(&bars->ds_full[steps & 1]), (uint32_t)(((steps >> 1) & 1) ^ 1),
                                            status, a.budget);
           if (!ok) break;
@@ -461,8 +462,10 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->ready[steps & 7]));
-        // V too, after the fact: every load of a slot is waited for before its next use's
+        // V too, after the fact: a wait by parity can tell a phase from the ones next to it only, so no
+        // phase of a slot may go unseen, and the slot is free once this warp has seen it
         if (!dkv) ok = mbar_wait_warp(smem_u32(&bars->full[y]), yp, status, a.budget);
+        if (ok && lane == 0) mbar_arrive(smem_u32(&bars->empty[y]));
       }
     }
   } else if (warp == 3) {
@@ -574,7 +577,7 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+          if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[L::kSBufs == 1 ? 0 : i & 1]));
           if (!mbar_wait_warp(smem_u32(&bars->dp_full), (uint32_t)(steps & 1), status, a.budget)) {
             ok = false;
             break;
@@ -686,7 +689,8 @@ cross_bwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       auto freed = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
+        // (an item without steps has no phase: it could pass before the MMA warp has seen the last)
+        if (n > 0 && lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
       };
       if (dkv) {  // warpgroup 0 writes dV, warpgroup 1 dK; a dropped key row gets 0
         const int j = it.k0 + r;

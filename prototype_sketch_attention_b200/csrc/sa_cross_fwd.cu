@@ -91,6 +91,7 @@ struct FwdParams {
   int H, G, PG;          // heads, heads per key head, heads per tile
   float c;               // scale log2 e
   __nv_bfloat16* out;    // [n_q, H, D]
+  __nv_bfloat16* rest;   // [n_q, H, D], nullable: out's rounding
   float* lse;            // [n_q, H]
   float* part_o;         // [2 CTAs][256, D] (null: no boundary cuts an item)
   float* part_lse;       // [2 CTAs][256], log2 units
@@ -107,6 +108,13 @@ __device__ __forceinline__ bool get_item(FBars* bars, const Item* ring, int s, i
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s & 1]));
   return ok && it->n >= 0;
+}
+
+// Two values as bf16, and what rounding took from them, as bf16 too.
+__device__ __forceinline__ uint32_t round_pair(float x, float y, uint32_t& rest) {
+  const uint32_t v = cvt_bf16x2(x, y);
+  rest = cvt_bf16x2(x - __uint_as_float(v << 16), y - __uint_as_float(v & 0xffff0000u));
+  return v;
 }
 
 // The 128 scores of this thread's row.
@@ -138,7 +146,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     mbar_init(smem_u32(&bars->q_empty), 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(smem_u32(&bars->full[s]), 1);
-      mbar_init(smem_u32(&bars->empty[s]), 1);
+      mbar_init(smem_u32(&bars->empty[s]), 2);  // the last MMA that reads the stage, and warp 2
     }
     for (int s = 0; s < 8; ++s) mbar_init(smem_u32(&bars->v_ready[s]), 1);
     for (int b = 0; b < L::kNB; ++b) {
@@ -239,10 +247,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const bool two = broadcast(it.two);
       const int n = broadcast(it.n), steps = two ? 2 * n : n;
-      if (n == 0) {  // (every phase of o_free is waited for, in order: see o_last)
-        if (s > 0) wait(bar(bars->o_free), (uint32_t)((s - 1) & 1));
-        continue;
-      }
+      if (n == 0) continue;
       wait(bar(bars->q_full), (uint32_t)(nq & 1));
       ++nq;
       auto scores = [&](int q) {
@@ -263,8 +268,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
       };
       for (int q = 0; q < kNB && q < steps; ++q) scores(q);
-      // the accumulators of the item before have been read
-      if (s > 0) wait(bar(bars->o_free), (uint32_t)((s - 1) & 1));
+      // the accumulators of the item with keys before have been read
+      if (nq > 1) wait(bar(bars->o_free), (uint32_t)(nq & 1));
       tc_fence_after();
       for (int q = 0; ok && q < steps; ++q) {
         const int w = q & 1;
@@ -318,17 +323,22 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         uint32_t keep[4];
         const bool drop = mb.vote(a.mask, it.k0 + 128 * j, it.k1, lane, keep);
         if (j + 1 < it.n) mb.load(a.mask, it.k0 + 128 * (j + 1), it.k1, lane);
-        // K first: a stage holds K and V in turn, and a wait by parity needs the use before this
-        // one to be over
-        ok = mbar_wait_warp(smem_u32(&bars->full[(i - 1) % NS]), (uint32_t)(((i - 1) / NS) & 1), status, a.budget) &&
-             mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
+        // K first: a stage holds K and V in turn, and a wait by parity can tell a phase from the ones
+        // next to it only. So no phase may go unseen: a stage is free once this warp has seen it too.
+        ok = mbar_wait_warp(smem_u32(&bars->full[(i - 1) % NS]), (uint32_t)(((i - 1) / NS) & 1), status, a.budget);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(smem_u32(&bars->empty[(i - 1) % NS]));
+        ok = mbar_wait_warp(smem_u32(&bars->full[st]), (uint32_t)((i / NS) & 1), status, a.budget);
         if (!ok) break;
         if (drop) {
           zero_rows(smem + L::oKV + st * L::kTile, L::kBoxes, keep, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->v_ready[v & 7]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->v_ready[v & 7]));
+          mbar_arrive(smem_u32(&bars->empty[st]));
+        }
       }
       base += 2 * it.n;
       vbase += it.n;
@@ -383,7 +393,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const uint32_t ot = tmem + lane_off + L::kColO + D * w;
     const float c = a.c;
     bool ok = true;
-    int cnt = 0, singles = 0, lasts = 0;  // this warpgroup's steps, items of one tile, items with steps
+    int cnt = 0, lasts = 0;         // this warpgroup's steps, items where it had steps
+    int singles = 0, filled = 0;    // items with keys: of one tile, all (counted by warpgroup 1)
     RingPos<kNB> base;         // the score buffer of the item's step 0
     for (int s = 0; ok; ++s) {
     // the item stays in the ring while it is worked on: registers are short here
@@ -487,11 +498,13 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     tc_fence_after();
     float* ml = reinterpret_cast<float*>(smem + L::oML);
     float g0 = 1.f, g1 = 0.f;  // factors of O_0 and O_1 (two tiles: of this tile's own)
-    // the item before has been written, so warpgroup 0 has read its m and l (waited for at every
-    // item: phase by phase)
-    if (w == 1)
-      ok = ok && (s == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((s - 1) & 1), status, a.budget));
-    if (!two) {
+    // the item with keys before has been written, so warpgroup 0 has read its m and l (waited for at
+    // every such item: phase by phase)
+    if (w == 1 && nkt > 0) {
+      ok = ok && (filled == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((filled - 1) & 1), status, a.budget));
+      ++filled;
+    }
+    if (!two && nkt > 0) {
       if (w == 1) {
         ml[r] = m;
         ml[128 + r] = ok ? l : 0.f;
@@ -510,6 +523,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       }
       ++singles;
     }
+    // an item of one key tile has no step of warpgroup 1, whose next wait for scores would then be two
+    // phases ahead of the last it saw: tile 0's last output follows every score of the item
+    if (w == 1 && nkt > 0)
+      ok = ok && mbar_wait_warp(smem_u32(&bars->o_last[0]), (uint32_t)((filled - 1) & 1), status, a.budget);
     const int t = it.t0 + (two ? w * tokens : 0) + r / a.PG;
     const int part = it.part;
     const bool mine = two || w == 0, write = mine && t < it.t1;
@@ -525,6 +542,13 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int tw = it.t0 + (two ? w * tokens : 0), t1 = it.t1;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s & 1]));
+    // the accumulators have been read (an item without keys has no phase: it could pass before the
+    // MMA warp has seen the last)
+    auto freed = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (nkt > 0 && lane == 0) mbar_arrive(smem_u32(&bars->o_free));
+    };
     if (mine && (nkt > 0 || part < 0)) {
       // 32 words of a row at a time: 32 columns of a part, or 64 of out as bf16 pairs
       auto columns = [&](int x, uint32_t (&o)[32]) {
@@ -545,32 +569,32 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] = 0u;
         }
-        if (x == D - 32) {  // the accumulators have been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
-        }
+        if (x == D - 32) freed();
       };
       if (part < 0) {
 #pragma unroll 1
         for (int x = 0; x < D; x += 64) {
-          uint32_t v[32];
+          uint32_t v[32], rest[32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t o[32];
             columns(x + 32 * h, o);
 #pragma unroll
             for (int y = 0; y < 16; ++y)
-              v[16 * h + y] = cvt_bf16x2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
+              v[16 * h + y] = round_pair(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), rest[16 * h + y]);
           }
-          regroup(v, lane);
+          auto store = [&](__nv_bfloat16* to, uint32_t (&u)[32]) {
+            regroup(u, lane);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
-            if (tt < t1)
-              *reinterpret_cast<uint4*>(a.out + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x +
-                                        8 * (lane >> 2)) = make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
-          }
+            for (int y = 0; y < 8; ++y) {
+              const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
+              if (tt < t1)
+                *reinterpret_cast<uint4*>(to + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x + 8 * (lane >> 2)) =
+                    make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
+            }
+          };
+          store(a.out, v);
+          if (a.rest) store(a.rest, rest);
         }
       } else {
 #pragma unroll 1
@@ -588,9 +612,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
       }
     } else {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->o_free));
+      freed();
     }
     }
   }
@@ -691,10 +713,13 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     const int r = r0 + 4 * warp + i, t = t0 + r / a.PG;
     if (t >= t1) continue;
     const float inv = total[4 * warp + i];
-    uint32_t* out = reinterpret_cast<uint32_t*>(
-        a.out + ((long long)t * a.H + cut.group * a.PG + r % a.PG) * D) + lane * (D / 64);
+    const long long at = (((long long)t * a.H + cut.group * a.PG + r % a.PG) * D + lane * (D / 32)) / 2;
 #pragma unroll
-    for (int y = 0; y < D / 64; ++y) out[y] = cvt_bf16x2(o[i][2 * y] * inv, o[i][2 * y + 1] * inv);
+    for (int y = 0; y < D / 64; ++y) {
+      uint32_t rest;
+      reinterpret_cast<uint32_t*>(a.out)[at + y] = round_pair(o[i][2 * y] * inv, o[i][2 * y + 1] * inv, rest);
+      if (a.rest) reinterpret_cast<uint32_t*>(a.rest)[at + y] = rest;
+    }
   }
 }
 
@@ -718,6 +743,7 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.PG = geo.pg;
   p.c = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.rest = static_cast<__nv_bfloat16*>(a.rest);
   p.lse = a.lse;
   p.part_o = reinterpret_cast<float*>(ws + a.plan.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + a.plan.part_lse);

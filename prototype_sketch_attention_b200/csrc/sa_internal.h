@@ -321,6 +321,7 @@ struct CrossArgs {
   const uint8_t* mask;    // [n_kv], nullable
   float scale;
   void* out;              // bf16 [n_q, H, d] (read by the backward)
+  void* rest;             // bf16 [n_q, H, d], nullable: out + rest is out before its rounding
   float* lse;             // [n_q, H]
   const void* dout;       // backward only
   void *dQ, *dK, *dV;

@@ -25,9 +25,9 @@ def _sum_err(n):
     return (128 + n / 128 + 2) * 2.0 ** -24
 
 
-def cross(Q, qo, K, V, ko, mask=None, scale=None, dout=None, kernel_out_err=True):
+def cross(Q, qo, K, V, ko, mask=None, scale=None, dout=None, rest=False):
     """Q [n, H, d], K, V [m, Hkv, d]; offsets lists; returns dict of (value, bound) pairs:
-    out, lse and, with dout, dQ, dK, dV. Rows outside the offsets hold 0 and bound inf."""
+    out, lse, wide (out + rest) and, with dout, dQ, dK, dV (rest: with the rest given). Rows outside the offsets hold 0 and bound inf."""
     H, d = Q.shape[1:]
     Hkv = K.shape[1]
     G = H // Hkv
@@ -37,7 +37,7 @@ def cross(Q, qo, K, V, ko, mask=None, scale=None, dout=None, kernel_out_err=True
     Qd, Kd, Vd = Q.double(), K.double(), V.double()
     out, oerr = torch.zeros(Q.shape, **z64), torch.full(Q.shape, math.inf, **z64)
     lse, lerr = torch.zeros(Q.shape[:2], **z64), torch.full(Q.shape[:2], math.inf, **z64)
-    res = {"out": (out, oerr), "lse": (lse, lerr)}
+    res = {"out": (out, oerr), "lse": (lse, lerr), "wide": (out, torch.full(Q.shape, math.inf, **z64))}
     if dout is not None:
         gd = dout.double()
         for n, x in (("dQ", Q), ("dK", K), ("dV", V)):
@@ -51,7 +51,7 @@ def cross(Q, qo, K, V, ko, mask=None, scale=None, dout=None, kernel_out_err=True
                 res[n][1][rows] = 0.0
         if dout is not None:
             res["dQ"][1][a:b] = 0.0
-        oerr[a:b], lerr[a:b] = 0.0, 0.0
+        oerr[a:b], lerr[a:b], res["wide"][1][a:b] = 0.0, 0.0, 0.0
         if len(keep) == 0:
             lse[a:b] = -math.inf
             continue
@@ -72,13 +72,15 @@ def cross(Q, qo, K, V, ko, mask=None, scale=None, dout=None, kernel_out_err=True
             e = (HALF + 2 * rel) * A
             oe = e + HALF * (o.abs() + e)
             oerr[a:b, h] = oe
+            res["wide"][1][a:b, h] = e + HALF ** 2 * (o.abs() + e) + TINY
             lerr[a:b, h] = (zerr + rel)[:, 0] + l[:, 0].abs() * 2.0 ** -22
             if dout is None:
                 continue
             g = gd[a:b, h]
             D = (g * o).sum(1, keepdim=True)
-            # delta is formed from the rounded out
-            Derr = (g.abs() * (oe if kernel_out_err else 0)).sum(1, keepdim=True) + \
+            # delta is formed from the rounded out, or from out + rest: rest is at most HALF of out, and
+            # off by HALF of itself
+            Derr = (g.abs() * (e + HALF ** 2 * (o.abs() + e) + TINY if rest else oe)).sum(1, keepdim=True) + \
                 (g.abs() * o.abs()).sum(1, keepdim=True) * (d + 2) * 2.0 ** -24
             dp = g @ v.T
             dperr = (g.abs() @ v.abs().T) * (d + 2) * 2.0 ** -24

@@ -19,10 +19,10 @@ def b():
 
 def _cross(b, back=False, **kw):
     a = dict(Q=16, qs=256, qo=8, R=1, n_q=4, H=2, d=128, K=16, ks=128, V=16, vs=128, ko=8, n_kv=5, Hkv=1, mask=None,
-             scale=0.1, out=16, lse=16, dout=16, dQ=16, dK=16, dV=16, ws=256, nb=1 << 30)
+             scale=0.1, out=16, rest=None, lse=16, dout=16, dQ=16, dK=16, dV=16, ws=256, nb=1 << 30)
     a.update(kw)
     head = [a[n] for n in ("Q", "qs", "qo", "R", "n_q", "H", "d", "K", "ks", "V", "vs", "ko", "n_kv", "Hkv", "mask",
-                           "scale", "out", "lse")]
+                           "scale", "out", "rest", "lse")]
     if back:
         return b.sa_cross_attn_backward(*head, a["dout"], a["dQ"], a["dK"], a["dV"], a["ws"], a["nb"], None)
     return b.sa_cross_attn_forward(*head, a["ws"], a["nb"], None)
@@ -34,7 +34,7 @@ def _cross(b, back=False, **kw):
     (dict(n_q=-1), 1), (dict(n_kv=1 << 31), 1), (dict(scale=0.0), 1), (dict(scale=math.inf), 1),
     (dict(scale=math.nan), 1), (dict(scale=-1.0), 1), (dict(Q=None), 1), (dict(K=None), 1), (dict(V=24), 1),
     (dict(qo=None), 1), (dict(ko=12), 1), (dict(out=None), 1), (dict(lse=None), 1), (dict(qs=255), 1),
-    (dict(qs=128), 1), (dict(ks=132), 1), (dict(vs=64), 1), (dict(out=8), 1),
+    (dict(qs=128), 1), (dict(ks=132), 1), (dict(vs=64), 1), (dict(out=8), 1), (dict(rest=8), 1),
     (dict(n_q=(1 << 31) - 1, H=1024, qs=1024 * 128), 2),
 ])
 def test_cross_attention_refuses(b, back, kw, code):

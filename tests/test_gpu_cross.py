@@ -236,3 +236,69 @@ def test_replays_from_a_graph():
     want = _run(Q2, _offsets([129, 3, 37]), K2, V2, _offsets([31, 600, 100]), d2)
     for n in NAMES:
         assert torch.equal({**f, **r}[n], want[n]), n
+
+
+@pytest.mark.parametrize("lq,lk,H,Hkv,d", [([40], [300], 4, 2, 64), ([0, 70, 9], [12, 500, 900], 8, 2, 128),
+                                           ([3, 200], [2000, 1], 16, 1, 128)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_rest_of_the_output(lq, lk, H, Hkv, d, masked):
+    """out + rest has the digits that rounding took, and the gradients formed with it are held to the
+    narrower bound; without it out is the same and the gradients keep theirs."""
+    from prototype_sketch_attention_b200 import binding as b
+    Q, K, V, dout = _inputs(lq, lk, H, Hkv, d, seed=301)
+    qo, ko = _offsets(lq), _offsets(lk)
+    mask = torch.rand(ko[-1], generator=torch.Generator(device="cuda").manual_seed(6), device="cuda") < 0.5 if masked else None
+    qd, kd = _dev(qo), _dev(ko)
+    got = _run(Q, qo, K, V, ko, dout, mask)
+    got["wide"] = got["out"].double() + got["rest"].double()
+    assert (got["rest"].double().abs() <= ref.HALF * got["out"].double().abs() + ref.TINY).all()
+    ref.check(got, ref.cross(Q, qo, K, V, ko, mask, dout=dout, rest=True), (*NAMES, "wide"))
+    f = b.cross_attention(Q, qd, K, V, kd, key_mask=mask, want_rest=False)
+    assert f.get("rest") is None and torch.equal(f["out"], got["out"]) and torch.equal(f["lse"], got["lse"])
+    g = b.cross_attention_backward(Q, qd, K, V, kd, f, dout, key_mask=mask)
+    torch.cuda.synchronize()
+    ref.check({**f, **g}, ref.cross(Q, qo, K, V, ko, mask, dout=dout), NAMES)
+
+
+REPEATED = [
+    # lq, lk, H, Hkv, d: persistent blocks take many items each, of every kind, in changing order
+    ([700, 1, 0, 130, 400] * 6, [900, 64, 500, 0, 1] * 6, 8, 2, 64),
+    ([700, 1, 0, 130, 400] * 6, [900, 64, 500, 0, 1] * 6, 8, 2, 128),
+    ([100, 0, 60] * 30, [100, 0, 128, 0, 129, 1] * 15, 12, 12, 64),
+    ([100, 0, 60] * 30, [100, 0, 128, 0, 129, 1] * 15, 12, 12, 128),
+    ([1024] * 12, [1024] * 12, 8, 8, 64),
+    ([300] * 8, [4000] * 8, 8, 8, 128),
+]
+
+
+@pytest.mark.parametrize("lq,lk,H,Hkv,d", REPEATED)
+def test_repeated_calls_agree_bit_for_bit(lq, lk, H, Hkv, d):
+    """Calls back to back, two inputs in turn, with no wait between them: every result is the first one's."""
+    from prototype_sketch_attention_b200 import binding as b
+    qo, ko = _dev(_offsets(lq)), _dev(_offsets(lk))
+    sets = [_inputs(lq, lk, H, Hkv, d, seed=400 + i) for i in range(2)]
+    mask = torch.rand(sum(lk), generator=torch.Generator(device="cuda").manual_seed(7), device="cuda") < 0.9
+    runs, first = [], {}
+    for n in range(24):
+        Q, K, V, dout = sets[n & 1]
+        m = mask if n & 2 else None
+        f = b.cross_attention(Q, qo, K, V, ko, key_mask=m)
+        g = b.cross_attention_backward(Q, qo, K, V, ko, f, dout, key_mask=m)
+        base = first.setdefault(n & 3, {**f, **g})
+        runs.append((n, torch.stack([(x[name] != base[name]).sum() for x in ({**f, **g},) for name in (*NAMES, "rest")]),
+                     f["_ws"], g["_ws"]))
+    torch.cuda.synchronize()
+    for n, off, fw, gw in runs:
+        assert not off.any(), (n, off.tolist())
+        assert b.device_status(fw) == 0 and b.device_status(gw) == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 64), (4, 1, 128)])
+def test_items_without_steps_between_others(H, Hkv, d):
+    """Users with one key tile, no keys or no queries between longer ones."""
+    lq = [1, 0, 3, 300, 2, 0, 140, 1, 1] * 20
+    lk = [1, 5, 0, 128, 0, 0, 127, 129, 700, 2, 0] * 18
+    lq, lk = lq[:180], lk[:180]
+    Q, K, V, dout = _inputs(lq, lk, H, Hkv, d, seed=500)
+    qo, ko = _offsets(lq), _offsets(lk)
+    ref.check(_run(Q, qo, K, V, ko, dout), ref.cross(Q, qo, K, V, ko, dout=dout, rest=True), NAMES)

@@ -323,3 +323,21 @@ def test_prefill_then_decode_steps(fp8):
         r = ref.cross(Q, list(range(R + 1)), K, V, off.tolist())
         ref.check(f, r, ("out", "lse"))
         ref.check(got, r, ("out", "lse"))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 64), (16, 1, 128), (4, 4, 128)])
+@pytest.mark.parametrize("amp", [1e-6, 1.0, 1e3])
+def test_attention_fp8_scales_of_many_magnitudes(H, Hkv, d, amp):
+    """Row scales over nine decades, K against the query's magnitude: a row's product is scaled in fp32."""
+    from prototype_sketch_attention_b200 import binding as b
+    lens = [1, 70, 1500, 4000]
+    Q, cache, table, ln = _filled(lens, H, Hkv, d, 32, True, seed=600 + H)
+    g = torch.Generator(device="cuda").manual_seed(601)
+    p = cache["k_scales"].shape
+    cache["k_scales"].mul_(10.0 ** (torch.rand(p, generator=g, device="cuda") * 3 - 3) / amp)
+    cache["v_scales"].mul_(10.0 ** (torch.rand(p, generator=g, device="cuda") * 9 - 6))
+    Q.mul_(amp)
+    got = b.paged_attention(Q, cache, table, ln)
+    torch.cuda.synchronize()
+    assert b.device_status(got["_ws"]) == 0
+    _check(Q, cache, table, ln, 32, 0, got)
