@@ -393,8 +393,11 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const uint32_t ot = tmem + lane_off + L::kColO + D * w;
     const float c = a.c;
     bool ok = true;
-    int cnt = 0, lasts = 0;         // this warpgroup's steps, items where it had steps
-    int singles = 0, filled = 0;    // items with keys: of one tile, all (counted by warpgroup 1)
+    // parities, a bit each: this warpgroup's steps; items where it had steps; items with keys, of one
+    // tile and all (registers are short here)
+    constexpr uint32_t kCnt = 1, kLasts = 2, kSingles = 4, kFilled = 8;
+    uint32_t par = 0;
+    auto parity = [&](uint32_t bit) { return (par & bit) ? 1u : 0u; };
     RingPos<kNB> base;         // the score buffer of the item's step 0
     for (int s = 0; ok; ++s) {
     // the item stays in the ring while it is worked on: registers are short here
@@ -411,7 +414,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int q = (two ? 2 * nkt : nkt) % (2 * kNB); q > 0; --q) base.next();
     MaskBytes mb;
     if (first < nkt) mb.load(a.mask, k0 + 128 * first, k1, lane);
-    for (int j = first; j < nkt; j += step, ++n, ++cnt) {
+    for (int j = first; j < nkt; j += step, ++n, par ^= kCnt) {
       uint32_t keep[4];
       const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
       if (j + step < nkt) mb.load(a.mask, k0 + 128 * (j + step), k1, lane);
@@ -444,7 +447,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const float f = raise ? ex2_approx((m - mt) * c) : 1.f;  // 0 for the first maximum
         if (n > 0) {
           // O_w holds every tile before this one once its last MMA has completed
-          if (!mbar_wait_warp(smem_u32(&bars->o_done[w]), (uint32_t)((cnt - 1) & 1), status, a.budget)) {
+          if (!mbar_wait_warp(smem_u32(&bars->o_done[w]), parity(kCnt) ^ 1, status, a.budget)) {
             ok = false;
             break;
           }
@@ -492,18 +495,16 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     }
     // ---- this tile's (or half's) accumulator is complete
     if (ok && n > 0) {
-      ok = mbar_wait_warp(smem_u32(&bars->o_last[w]), (uint32_t)(lasts & 1), status, a.budget);
-      ++lasts;
+      ok = mbar_wait_warp(smem_u32(&bars->o_last[w]), parity(kLasts), status, a.budget);
+      par ^= kLasts;
     }
     tc_fence_after();
     float* ml = reinterpret_cast<float*>(smem + L::oML);
     float g0 = 1.f, g1 = 0.f;  // factors of O_0 and O_1 (two tiles: of this tile's own)
     // the item with keys before has been written, so warpgroup 0 has read its m and l (waited for at
     // every such item: phase by phase)
-    if (w == 1 && nkt > 0) {
-      ok = ok && (filled == 0 || mbar_wait_warp(smem_u32(&bars->o_free), (uint32_t)((filled - 1) & 1), status, a.budget));
-      ++filled;
-    }
+    if (w == 1 && nkt > 0)  // (passes at once for the first)
+      ok = ok && mbar_wait_warp(smem_u32(&bars->o_free), parity(kFilled) ^ 1, status, a.budget);
     if (!two && nkt > 0) {
       if (w == 1) {
         ml[r] = m;
@@ -512,7 +513,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->merge));
       } else {
-        ok = mbar_wait_warp(smem_u32(&bars->merge), (uint32_t)(singles & 1), status, a.budget) && ok;
+        ok = mbar_wait_warp(smem_u32(&bars->merge), parity(kSingles), status, a.budget) && ok;
         tc_fence_after();
         const float m1 = ml[r], l1 = ml[128 + r];
         const float mm = fmaxf(m, m1);
@@ -521,12 +522,13 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         l = l * g0 + l1 * g1;
         m = mm;
       }
-      ++singles;
+      par ^= kSingles;
     }
     // an item of one key tile has no step of warpgroup 1, whose next wait for scores would then be two
     // phases ahead of the last it saw: tile 0's last output follows every score of the item
     if (w == 1 && nkt > 0)
-      ok = ok && mbar_wait_warp(smem_u32(&bars->o_last[0]), (uint32_t)((filled - 1) & 1), status, a.budget);
+      ok = ok && mbar_wait_warp(smem_u32(&bars->o_last[0]), parity(kFilled), status, a.budget);
+    if (nkt > 0) par ^= kFilled;
     const int t = it.t0 + (two ? w * tokens : 0) + r / a.PG;
     const int part = it.part;
     const bool mine = two || w == 0, write = mine && t < it.t1;
@@ -571,30 +573,46 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
         if (x == D - 32) freed();
       };
-      if (part < 0) {
+      if (part < 0 && a.rest) {  // 32 columns: 16 words of out, 16 of rest
+        __nv_bfloat16* to = (lane >> 4) ? a.rest : a.out;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          uint32_t v[32], o[32];
+          columns(x, o);
+#pragma unroll
+          for (int y = 0; y < 16; ++y)
+            v[y] = round_pair(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), v[16 + y]);
+          regroup(v, lane);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
+            if (tt < t1)
+              *reinterpret_cast<uint4*>(to + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x +
+                                        8 * ((lane >> 2) & 3)) =
+                  make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
+        }
+      } else if (part < 0) {
 #pragma unroll 1
         for (int x = 0; x < D; x += 64) {
-          uint32_t v[32], rest[32];
+          uint32_t v[32];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t o[32];
             columns(x + 32 * h, o);
 #pragma unroll
             for (int y = 0; y < 16; ++y)
-              v[16 * h + y] = round_pair(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]), rest[16 * h + y]);
+              v[16 * h + y] = cvt_bf16x2(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
           }
-          auto store = [&](__nv_bfloat16* to, uint32_t (&u)[32]) {
-            regroup(u, lane);
+          regroup(v, lane);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
-              if (tt < t1)
-                *reinterpret_cast<uint4*>(to + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x + 8 * (lane >> 2)) =
-                    make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
-            }
-          };
-          store(a.out, v);
-          if (a.rest) store(a.rest, rest);
+          for (int y = 0; y < 8; ++y) {
+            const int rr = q4 * 32 + 4 * y + (lane & 3), tt = tw + rr / a.PG;
+            if (tt < t1)
+              *reinterpret_cast<uint4*>(a.out + ((long long)tt * a.H + hu * a.PG + rr % a.PG) * D + x +
+                                        8 * (lane >> 2)) =
+                  make_uint4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
         }
       } else {
 #pragma unroll 1
