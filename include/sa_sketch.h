@@ -561,8 +561,8 @@ int sa_page_tables(const int32_t* cached_lens, const int32_t* new_lens, int R, i
  * multiples of 8) go to slots[i]; a slot outside [0, n_pages page_size) is skipped (the
  * padding of sa_page_tables is -1). SA_CODEC_BF16 copies the bits; SA_CODEC_FP8 stores
  * s = max |row| / 448 (1 for a row of zeros) and the E4M3 codes of row / s as
- * sa_sketch_pack does (finite rows). Slots named twice hold one of the rows, which one is
- * not fixed. n_pages Hkv page_size <= INT32_MAX; d in {64, 128}; Hkv <= 1024; pointers
+ * sa_sketch_pack does (finite rows). A slot named twice by one call holds a mixture of its
+ * rows afterwards; the others are not affected. n_pages Hkv page_size <= INT32_MAX; d in {64, 128}; Hkv <= 1024; pointers
  * 16-byte aligned (slots: 8). One kernel, no workspace.
  */
 int sa_paged_append(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
@@ -585,9 +585,12 @@ int sa_paged_append(const void* K, int64_t k_stride, const void* V, int64_t v_st
  *   (SA_ERR_BAD_PAGES) is latched in the device status word and nothing outside the cache
  *   is read; the outputs are then unspecified. Entries past the length are not read as ids.
  * Rows past the length and before the window are never used, whatever they hold. d in
- * {64, 128}; H / Hkv <= 64; H <= 1024; n_pages Hkv page_size <= INT32_MAX; R <=
- * SA_MAX_USERS. Precision as for the forward above; FP8 codes are exact in bf16, their
- * scales enter in fp32. Workspace: sa_paged_attn_workspace_size(...) bytes, 256-aligned.
+ * {64, 128}; H / Hkv <= 64; H <= 1024; n_pages Hkv page_size <= INT32_MAX;
+ * max_pages page_size <= INT32_MAX - 256; R <= SA_MAX_USERS. Precision as for the forward
+ * above. FP8: the codes are exact in fp16, Q is as well but for what lies 2^-33 under a
+ * head's largest value, K's scales enter in fp32, and a weight times its row's v_scale is
+ * rounded to fp16 (2^-12 of its value; below 2^-14 of the largest v_scale of the positions
+ * read, 2^-25 of that). Workspace: sa_paged_attn_workspace_size(...) bytes, 256-aligned.
  */
 size_t sa_paged_attn_workspace_size(int R, int H, int Hkv, int d);
 int sa_paged_attn(const void* Q, int64_t q_stride, int R, int H, int d, const void* k_cache,

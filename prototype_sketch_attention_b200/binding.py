@@ -365,9 +365,24 @@ def _dt(x: torch.Tensor) -> int:
     raise TypeError(f"X must be bfloat16 or float32, got {x.dtype}")
 
 
+# the current stream's handle without a Stream object around it (0.1 us in place of 2.3)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device=None) -> int:
+    if stream is None and _raw_stream is not None and device is not None and device.index is not None:
+        return _raw_stream(device.index)
     s = torch.cuda.current_stream(device) if stream is None else stream
     return s.cuda_stream
+
+
+def _used_on(stream, out: dict) -> None:
+    """A result that is dropped early stays allocated until the given stream has passed this call:
+    its tensors may come from another stream's pool."""
+    if stream is not None:
+        for t in out.values():
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
 
 
 def _fail(where: str, what: str):
@@ -795,8 +810,8 @@ def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
                  where, "key_mask must be a bool or uint8 tensor")
         _check_tensor(where, "key_mask", key_mask, (n_kv,), key_mask.dtype, dev)
     _check_cuda(where, Q)
-    strides = tuple(_rows_stride(where, name, x, heads, d)
-                    for name, x, heads in (("Q", Q, H), ("K", K, Hkv), ("V", V, Hkv)))
+    strides = (_rows_stride(where, "Q", Q, H, d), _rows_stride(where, "K", K, Hkv, d),
+               _rows_stride(where, "V", V, Hkv, d))
     return R, n_q, H, d, n_kv, Hkv, dev, strides
 
 
@@ -837,6 +852,7 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_forward")
     out["_ws"] = ws
+    _used_on(stream, out)
     return out
 
 
@@ -880,6 +896,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_backward")
     out["_ws"] = ws
+    _used_on(stream, out)
     return out
 
 
@@ -961,6 +978,7 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_page_tables")
     out["_ws"] = ws
+    _used_on(stream, out)
     return out
 
 
@@ -968,7 +986,7 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
                  stream=None) -> None:
     """Writes rows K, V [n, Hkv, d] bf16 (rows may be strided) into the slots [n] int64 of a
     paged_cache, quantised for an FP8 cache (sa_paged_append). Slots outside the cache, such as
-    the -1 of page_tables, are skipped."""
+    the -1 of page_tables, are skipped; a slot must not be named twice."""
     where = "paged_append"
     _require(isinstance(K, torch.Tensor) and K.dim() == 3, where, "K must be [n, heads, d]")
     dev = K.device
@@ -1022,6 +1040,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_paged_attn")
     out["_ws"] = ws
+    _used_on(stream, out)
     return out
 
 

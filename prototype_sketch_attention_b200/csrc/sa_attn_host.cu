@@ -259,7 +259,7 @@ int sa_paged_attn(const void* Q, int64_t q_stride, int R, int H, int d, const vo
   PagedAttnArgs a = {};
   a.fp8 = format == SA_CODEC_FP8;
   if ((a.log2_page = page_log2(page_size)) < 0 || n_pages * Hkv * page_size > INT32_MAX ||
-      (int64_t)max_pages * page_size > INT32_MAX)
+      (int64_t)max_pages * page_size > INT32_MAX - 256)  // (positions round up to a tile in 31 bits)
     return SA_ERR_UNSUPPORTED;
   if ((R > 0 && (!Q || !out || !seq_lens || (max_pages > 0 && !block_table))) ||
       (n_pages > 0 && (!k_cache || !v_cache || (a.fp8 && (!k_scales || !v_scales)))))

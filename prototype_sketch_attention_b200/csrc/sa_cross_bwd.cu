@@ -30,7 +30,10 @@
 // (3,700 clocks a step), and P^T through shared memory, which lets S^T go at once but
 // leaves two slots of each, no less (3,700).
 // Bound at d = 128: 2,048 tensor clocks a pair of tiles for dK/dV, 1,536 for dQ, 1,024
-// clocks of exponentials in both.
+// clocks of exponentials in both. Measured (10 d a pair and head): 4 x 4096 queries and keys, 8 heads
+// of 128: 725 us, 945 TFLOP/s; 40 x 300 over 10K keys, 8 heads over 2: 1.6 ms, 770 TFLOP/s; 40 x
+// 100-300 over 1K-10K masked keys, 8 heads over 4: 540 us, 585 TFLOP/s: a dK/dV item has 2 to 5 steps there
+// and its epilogue, which the tensor cores wait for, costs about one.
 #include <cmath>
 
 #include "sa_cross.cuh"
