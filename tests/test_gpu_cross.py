@@ -302,3 +302,46 @@ def test_items_without_steps_between_others(H, Hkv, d):
     Q, K, V, dout = _inputs(lq, lk, H, Hkv, d, seed=500)
     qo, ko = _offsets(lq), _offsets(lk)
     ref.check(_run(Q, qo, K, V, ko, dout), ref.cross(Q, qo, K, V, ko, dout=dout, rest=True), NAMES)
+
+
+def test_history_to_sketch_to_heads_and_back():
+    """A training step's chain: histories to sketches, keys and values of heads from the sketch rows,
+    cross attention, its gradients, and back into the histories' gradients, against 64-bit autograd
+    of the whole. Tolerance on the relative L2 error: 1e-2 of the sketch's backward (its own tests'),
+    and one half step of bf16, 2^-8, for each of what is rounded between: the sketch, K or V, the
+    weights, dS, dK or dV, out."""
+    from prototype_sketch_attention_b200 import binding as b
+    g = torch.Generator(device="cuda").manual_seed(700)
+    n, lq, k, d, H, Hkv, dh = [700, 64, 1500], [40, 3, 129], 128, 128, 4, 2, 64
+    off, qo, ko = _offsets(n), _offsets(lq), _offsets([k] * 3)
+
+    def draw(*shape, amp=1.0):
+        return (amp * torch.randn(*shape, generator=g, device="cuda")).to(BF)
+    X, P = draw(sum(n), d), draw(k, d)
+    Wk, Wv, Ak, Av = (draw(d, m, amp=d ** -0.5) for m in (d, d, Hkv * dh, Hkv * dh))
+    Q, dout = draw(sum(lq), H, dh), draw(sum(lq), H, dh)
+
+    fw = b.forward(X, _dev(off), P, Wk, Wv)
+    rows = fw["sketch"].reshape(-1, d).to(BF)
+    K, V = (rows @ Ak).view(-1, Hkv, dh), (rows @ Av).view(-1, Hkv, dh)
+    f = b.cross_attention(Q, _dev(qo), K, V, _dev(ko))
+    c = b.cross_attention_backward(Q, _dev(qo), K, V, _dev(ko), f, dout)
+    ds = c["dK"].view(-1, Hkv * dh).float() @ Ak.float().T + c["dV"].view(-1, Hkv * dh).float() @ Av.float().T
+    gr = b.backward(X, _dev(off), P, Wk, Wv, fw, ds.view(3, k, d).contiguous())
+    torch.cuda.synchronize()
+
+    leaves = [x.double().requires_grad_() for x in (X, P, Wk, Wv, Q)]
+    Xd, Pd, Wkd, Wvd, Qd = leaves
+    total = 0
+    for u in range(3):
+        x = Xd[off[u]:off[u + 1]]
+        a = torch.softmax((x @ Wkd) @ Pd.T * d ** -0.5, 1)
+        s = a.T @ (x @ Wvd) / a.sum(0)[:, None]
+        kk, vv = ((s @ A.double()).view(k, Hkv, dh).repeat_interleave(H // Hkv, 1) for A in (Ak, Av))
+        z = torch.einsum("thd,khd->htk", Qd[qo[u]:qo[u + 1]], kk) * dh ** -0.5
+        o = torch.einsum("htk,khd->thd", torch.softmax(z, 2), vv)
+        total = total + (o * dout[qo[u]:qo[u + 1]].double()).sum()
+    want = torch.autograd.grad(total, leaves)
+    for name, w, x in zip(("dX", "dP", "dWk", "dWv", "dQ"), want, (gr["dX"], gr["dP"], gr["dWk"], gr["dWv"], c["dQ"])):
+        err = float((x.double() - w).norm() / w.norm())
+        assert err <= 1e-2 + 6 * ref.HALF, (name, err)
