@@ -538,10 +538,10 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int part = it.part;
     const bool mine = two || w == 0, write = mine && t < it.t1;
     const int hu = it.hu;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
     g0 *= inv;
     g1 *= inv;
-    const float lse2 = l > 0.f ? m * c + lg2_approx(l) : -INFINITY;
+    const float lse2 = l == 0.f ? -INFINITY : m * c + lg2_approx(l);
     if (write) {
       if (part < 0) a.lse[(long long)t * a.H + hu * a.PG + r % a.PG] = lse2 * kLn2;
       else a.part_lse[(long long)part * 256 + w * 128 + r] = lse2;
@@ -694,15 +694,15 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     float m = -INFINITY, l = 0.f;
     for (int x = 0; x < parts; ++x) m = fmaxf(m, wts[x * 32 + tid]);
     for (int x = 0; x < parts; ++x) {
-      const float ls = wts[x * 32 + tid], w = ls > -INFINITY ? ex2_approx(ls - m) : 0.f;
+      const float ls = wts[x * 32 + tid], w = ls == -INFINITY ? 0.f : ex2_approx(ls - m);
       l += w;
       wts[x * 32 + tid] = w;
     }
-    total[tid] = l > 0.f ? 1.f / l : 0.f;
+    total[tid] = l == 0.f ? 0.f : 1.f / l;
     const int t = t0 + (r0 + tid) / a.PG;
     if (t < t1)
       a.lse[(long long)t * a.H + cut.group * a.PG + (r0 + tid) % a.PG] =
-          l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
+          l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kLn2;
   }
   __syncthreads();
   float o[4][D / 32];
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float w = wts[x * 32 + 4 * warp + i];
-      if (w > 0.f) {  // (rows past the user's end have no weight)
+      if (w != 0.f) {
         if (D == 128) {
           const float4 v = *reinterpret_cast<const float4*>(po + i * D);
           o[i][0] = fmaf(w, v.x, o[i][0]);

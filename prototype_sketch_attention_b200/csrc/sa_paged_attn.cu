@@ -329,8 +329,8 @@ __device__ __forceinline__ void write_item(const PagedParams& a, const State<D, 
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float i0 = st.l[n][0] > 0.f ? 1.f / st.l[n][0] : 0.f;
-    const float i1 = st.l[n][1] > 0.f ? 1.f / st.l[n][1] : 0.f;
+    const float i0 = st.l[n][0] == 0.f ? 0.f : 1.f / st.l[n][0];  // (a NaN stays one)
+    const float i1 = st.l[n][1] == 0.f ? 0.f : 1.f / st.l[n][1];
     __nv_bfloat16* row = a.out + ((long long)r * a.H + h0 + 8 * n + g) * D;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
@@ -340,7 +340,7 @@ __device__ __forceinline__ void write_item(const PagedParams& a, const State<D, 
       for (int e = 0; e < 2; ++e)
         if (8 * n + 2 * t + e < nh)
           a.lse[(long long)r * a.H + h0 + 8 * n + 2 * t + e] =
-              st.l[n][e] > 0.f ? (st.m[n][e] + lg2_approx(st.l[n][e])) * kLn2 : -INFINITY;
+              st.l[n][e] == 0.f ? -INFINITY : (st.m[n][e] + lg2_approx(st.l[n][e])) * kLn2;
     }
   }
 }
@@ -813,13 +813,13 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
   if (warp < kHeads) {  // 16 warps: one head each
     float m = -INFINITY, l = 0.f;
     for (int x = lane; x < nb; x += 32)
-      if (ls[x * kHeads + warp] > 0.f) m = fmaxf(m, ms[x * kHeads + warp]);
+      if (!(ls[x * kHeads + warp] <= 0.f)) m = fmaxf(m, ms[x * kHeads + warp]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int x = lane; x < nb; x += 32) {
       const int i = x * kHeads + warp;
-      const float w = ls[i] > 0.f ? ex2_approx(ms[i] - m) : 0.f;
-      l += w > 0.f ? w * ls[i] : 0.f;
+      const float w = ls[i] <= 0.f ? 0.f : ex2_approx(ms[i] - m);
+      l += ls[i] <= 0.f ? 0.f : w * ls[i];
       ms[i] = w;
     }
 #pragma unroll
@@ -858,12 +858,12 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
       o[3] += u.w;
     }
     const float l0 = tot_l[n * 8 + 2 * q4], l1 = tot_l[n * 8 + 2 * q4 + 1];
-    write_fragment<FP8>(o, l0 > 0.f ? 1.f / l0 : 0.f, l1 > 0.f ? 1.f / l1 : 0.f, 8 * n + g < nh,
+    write_fragment<FP8>(o, l0 == 0.f ? 0.f : 1.f / l0, l1 == 0.f ? 0.f : 1.f / l1, 8 * n + g < nh,
                         a.out + ((long long)in.r * a.H + h0 + 8 * n + g) * D + 16 * i, q4);
     if (a.lse && i == 0 && lane < 8 && 8 * n + lane < nh) {
       const float l = tot_l[n * 8 + lane];
       a.lse[(long long)in.r * a.H + h0 + 8 * n + lane] =
-          l > 0.f ? (tot_m[n * 8 + lane] + lg2_approx(l)) * kLn2 : -INFINITY;
+          l == 0.f ? -INFINITY : (tot_m[n * 8 + lane] + lg2_approx(l)) * kLn2;
     }
   }
 }

@@ -345,3 +345,22 @@ def test_history_to_sketch_to_heads_and_back():
     for name, w, x in zip(("dX", "dP", "dWk", "dWv", "dQ"), want, (gr["dX"], gr["dP"], gr["dWk"], gr["dWv"], c["dQ"])):
         err = float((x.double() - w).norm() / w.norm())
         assert err <= 1e-2 + 6 * ref.HALF, (name, err)
+
+
+@pytest.mark.parametrize("lq,lk,d", [([3, 200, 7], [40, 700, 20000], 64), ([300, 1], [513, 9000], 128)])
+def test_nan_in_a_kept_row_stays_with_its_user_and_heads(lq, lk, d):
+    """A NaN that is attended to is in out and lse of every head that shares its key head, and nowhere else."""
+    from prototype_sketch_attention_b200 import binding as b
+    H, Hkv = 6, 2
+    Q, K, V, dout = _inputs(lq, lk, H, Hkv, d, seed=801)
+    qo, ko = _offsets(lq), _offsets(lk)
+    clean = b.cross_attention(Q, _dev(qo), K, V, _dev(ko))
+    for u, row in [(x, r) for x in range(len(lq)) for r in (0, lk[x] // 2, lk[x] - 1)]:
+        bad = K.clone()
+        bad[ko[u] + row, 1, 5] = math.nan
+        f = b.cross_attention(Q, _dev(qo), bad, V, _dev(ko))
+        hit = torch.zeros(Q.shape[:2], dtype=torch.bool, device="cuda")
+        hit[qo[u]:qo[u + 1], 3:] = True
+        assert f["out"][hit].isnan().all() and f["lse"][hit].isnan().all()
+        assert torch.equal(f["out"][~hit], clean["out"][~hit]) and torch.equal(f["lse"][~hit], clean["lse"][~hit])
+    assert b.device_status(f["_ws"]) == 0

@@ -341,3 +341,22 @@ def test_attention_fp8_scales_of_many_magnitudes(H, Hkv, d, amp):
     torch.cuda.synchronize()
     assert b.device_status(got["_ws"]) == 0
     _check(Q, cache, table, ln, 32, 0, got)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,H,Hkv,d", [([5, 300, 9000], 4, 2, 64), ([20000], 32, 2, 128)])
+def test_attention_nan_in_reach_stays_with_its_request_and_heads(lens, H, Hkv, d, fp8):
+    from prototype_sketch_attention_b200 import binding as b
+    Q, cache, table, ln = _filled(lens, H, Hkv, d, 16, fp8, seed=901)
+    clean = b.paged_attention(Q, cache, table, ln)
+    K = cache["K"].view(torch.uint8) if fp8 else cache["K"]
+    for r, pos in [(x, p) for x in range(len(lens)) for p in (0, lens[x] // 2, lens[x] - 1)]:
+        at = (int(table[r, pos // 16]), 1, pos % 16, 7)
+        old = K[at].clone()
+        K[at] = 0x7F if fp8 else math.nan
+        got = b.paged_attention(Q, cache, table, ln)
+        K[at] = old
+        hit = torch.zeros(Q.shape[:2], dtype=torch.bool, device="cuda")
+        hit[r, H // Hkv:] = True
+        assert got["out"][hit].isnan().all() and got["lse"][hit].isnan().all()
+        assert torch.equal(got["out"][~hit], clean["out"][~hit]) and torch.equal(got["lse"][~hit], clean["lse"][~hit])
