@@ -135,6 +135,10 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+# The usual calls of the attention with heads, in C++ (csrc/sa_calls.cpp): checks, allocations and
+# the C ABI call in a third of the host time. They return None for any other call, which
+# the functions below then check step by step and make themselves.
+from . import _calls  # noqa: E402
 
 
 # ---------------------------------------------------------------- raw C ABI
@@ -787,6 +791,13 @@ def _check_heads(where: str, name: str, x, n, d, dev, heads=None) -> None:
         _fail(where, f"{name} is on {x.device}, expected {dev}")
 
 
+def _result(res, call: str) -> dict:
+    """What _calls returned: a dictionary, or the status of a refused call."""
+    if type(res) is dict:
+        return res
+    raise SketchAttentionError(res, call)
+
+
 def _scale(scale, d: int) -> float:
     return float(d) ** -0.5 if scale is None else float(scale)
 
@@ -826,6 +837,10 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
     [n_q, H, d] bf16, lse [n_q, H] fp32 and, for the backward, what rounding took from out (rest,
     like out; want_rest=False leaves it away). They are written into `out` ({"out", "lse"} and,
     if wanted, "rest") when given."""
+    if out is None and stream is None:
+        res = _calls.cross_forward(Q, q_offsets, K, V, kv_offsets, key_mask, scale, bool(want_rest), ws)
+        if res is not None:
+            return _result(res, "sa_cross_attn_forward")
     where = "cross_attention"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
                                                               key_mask)
@@ -865,6 +880,11 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     [n_q, H, d] bf16: dQ [n_q, H, d], dK and dV [n_kv, Hkv, d], bf16 (sa_cross_attn_backward),
     written into `out` ({"dQ", "dK", "dV"}) when given. Other arguments as passed to the
     forward."""
+    if out is None and stream is None:
+        res = _calls.cross_backward(Q, q_offsets, K, V, kv_offsets, key_mask, scale, fwd.get("out"),
+                                    fwd.get("lse"), fwd.get("rest"), dout, ws)
+        if res is not None:
+            return _result(res, "sa_cross_attn_backward")
     where = "cross_attention_backward"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
                                                               key_mask)
@@ -947,6 +967,11 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     and new_offsets [R + 1] int64, seq_lens [R] int32, free_used [1] int64. Too few pages and
     the like are latched in the device status (device_status(result["_ws"])) and change
     nothing."""
+    if stream is None:
+        res = _calls.page_tables(cached_lens, new_lens, free_pages, block_table, page_size, n_slots,
+                                 free_used, ws)
+        if res is not None:
+            return _result(res, "sa_page_tables")
     where = "page_tables"
     _require(isinstance(cached_lens, torch.Tensor) and cached_lens.dim() == 1, where,
              "cached_lens must be a 1-D tensor")
@@ -987,6 +1012,13 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
     """Writes rows K, V [n, Hkv, d] bf16 (rows may be strided) into the slots [n] int64 of a
     paged_cache, quantised for an FP8 cache (sa_paged_append). Slots outside the cache, such as
     the -1 of page_tables, are skipped; a slot must not be named twice."""
+    if stream is None and isinstance(cache, dict):
+        res = _calls.paged_append(K, V, slots, cache.get("K"), cache.get("V"), cache.get("k_scales"),
+                                  cache.get("v_scales"))
+        if res == SA_OK:
+            return
+        if res is not None:
+            raise SketchAttentionError(res, "sa_paged_append")
     where = "paged_append"
     _require(isinstance(K, torch.Tensor) and K.dim() == 3, where, "K must be [n, heads, d]")
     dev = K.device
@@ -1011,6 +1043,11 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     positions (0: all) of its seq_lens [R] int32 in a paged_cache, through block_table
     [R, max_pages] int32 (sa_paged_attn). Returns out [R, H, d] bf16 and lse [R, H] fp32. Bad
     lengths and page ids are latched in the device status (device_status(result["_ws"]))."""
+    if stream is None and isinstance(cache, dict):
+        res = _calls.paged_attention(Q, cache.get("K"), cache.get("V"), cache.get("k_scales"),
+                                     cache.get("v_scales"), block_table, seq_lens, window, scale, ws)
+        if res is not None:
+            return _result(res, "sa_paged_attn")
     where = "paged_attention"
     _require(isinstance(Q, torch.Tensor) and Q.dim() == 3, where, "Q must be [n, heads, d]")
     dev, (R, H, d) = Q.device, Q.shape

@@ -5,7 +5,9 @@
 Each .cu file under csrc/ compiles to an object under _build/ (in parallel). The
 objects link into prototype_sketch_attention_b200/libsa_sketch.so. The CUDA runtime
 is linked statically and the driver API is reached through
-cudaGetDriverEntryPoint, so the library needs no -lcuda.
+cudaGetDriverEntryPoint, so the library needs no -lcuda. csrc/sa_calls.cpp, the Python
+extension through which the binding makes its short calls, is compiled with g++ against
+torch into prototype_sketch_attention_b200/_calls.so.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsa_sketch.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["sa_host.cu", "sa_prep.cu", "sa_fwd_sm100.cu", "sa_fwd_simt.cu", "sa_bwd_simt.cu",
            "sa_gemm_sm100.cu", "sa_bwd_tc.cu",
@@ -65,8 +69,31 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def _build_calls(force: bool) -> None:
+    """csrc/sa_calls.cpp against the installed torch, linked to libsa_sketch.so beside it."""
+    src = os.path.join(CSRC, "sa_calls.cpp")
+    if not force and _mtime(CALLS) >= max(_mtime(src), _mtime(os.path.join(INCLUDE, "sa_sketch.h")), _mtime(__file__)):
+        return
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib, tmp = os.path.join(home, "lib"), CALLS + f".tmp{os.getpid()}"
+    includes = [INCLUDE, os.path.join(home, "include"),
+                os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", "-DTORCH_EXTENSION_NAME=_calls",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in includes for x in ("-isystem" if d != INCLUDE else "-I", d)], src, "-o", tmp,
+           "-L", PKG, "-l:libsa_sketch.so", "-Wl,-rpath,$ORIGIN",
+           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for sa_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compiles every CUDA source for sm_100a and links libsa_sketch.so. Returns its path."""
+    """Compiles every CUDA source for sm_100a, links libsa_sketch.so (its path is returned) and
+    builds the extension of the short calls."""
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps_mtime()
     stale = [s for s in SOURCES
@@ -86,6 +113,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_calls(force)
     if verbose_ptxas:
         for src, log in logs.items():
             print(f"== {src}\n{log}")

@@ -187,3 +187,18 @@ def test_reference_tables():
     assert table == [[7, 1, -1], [-1, -1, -1], [3, 4, 5]]
     assert slots == [59, 60, 61, 62, 63, 8, 40, 41, -1, -1]
     assert (off, lens, used) == ([0, 6, 6, 8], [9, 0, 18], 3)
+
+
+def test_short_calls_leave_what_is_not_plain_to_python(b):
+    """_calls returns None, and touches nothing, for whatever is not a plain call on CUDA tensors."""
+    calls = b._calls
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    i, o = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    counts = {"cross_forward": 9, "cross_backward": 12, "page_tables": 8, "paged_append": 7, "paged_attention": 10}
+    for name, n in counts.items():
+        f = getattr(calls, name)
+        for arg in (None, 3, "x", x, i, o, torch.nn.Parameter(x.float())):
+            assert f(*[arg] * n) is None
+        assert f() is None and f(*[x] * (n + 1)) is None
+    assert calls.cross_forward(x, o, x, x, o, None, None, True, None) is None
+    assert calls.paged_attention(x, x, x, None, None, i, i, 0, None, None) is None

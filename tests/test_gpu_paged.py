@@ -360,3 +360,42 @@ def test_attention_nan_in_reach_stays_with_its_request_and_heads(lens, H, Hkv, d
         hit[r, H // Hkv:] = True
         assert got["out"][hit].isnan().all() and got["lse"][hit].isnan().all()
         assert torch.equal(got["out"][~hit], clean["out"][~hit]) and torch.equal(got["lse"][~hit], clean["lse"][~hit])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_short_calls_and_stepwise_calls_agree(fp8):
+    """A call with a stream goes through Python's checks, one without through the extension's."""
+    from prototype_sketch_attention_b200 import binding as b
+    R, H, Hkv, d, page = 5, 4, 2, 128, 16
+    cached, new = [3, 0, 40, 16, 7], [1, 30, 2, 16, 0]
+    g = torch.Generator(device="cuda").manual_seed(950)
+    K, V = (torch.randn(sum(new) + 2, Hkv, d, generator=g, device="cuda").to(BF) for _ in range(2))  # and two of padding
+    Q = torch.randn(R, H, d, generator=g, device="cuda").to(BF)
+    free = _i32(range(20, 60))
+    got = []
+    for stream in (None, torch.cuda.current_stream()):
+        table = _i32(range(R * 6)).view(R, 6) % 20
+        cache = b.paged_cache(64, Hkv, page, d, fmt=b.SA_CODEC_FP8 if fp8 else b.SA_CODEC_BF16)
+        for x in cache.values():
+            if x is not None:
+                x.view(torch.uint8).zero_()
+        t = b.page_tables(_i32(cached), _i32(new), free, table, page, sum(new) + 2, stream=stream)
+        b.paged_append(K, V, t["slots"], cache, stream=stream)
+        a = b.paged_attention(Q, cache, table, t["seq_lens"], window=20, stream=stream)
+        q, k = _i32([0, 1, 2, 3, 4, 5]).long(), _i32([0, 7, 7, 20, 30, 45]).long()
+        f = b.cross_attention(Q, q, K[:45], V[:45], k, stream=stream)
+        r = b.cross_attention_backward(Q, q, K[:45], V[:45], k, f, Q, stream=stream)
+        torch.cuda.synchronize()
+        assert all(b.device_status(x["_ws"]) == 0 for x in (t, a, f, r))
+        got.append([table, *(t[n] for n in ("slots", "new_offsets", "seq_lens", "free_used")), a["out"], a["lse"],
+                    f["out"], f["lse"], f["rest"], r["dQ"], r["dK"], r["dV"]])
+        got[-1] += [x.view(torch.uint8) for x in cache.values() if x is not None]
+    assert len(got[0]) == len(got[1])
+    for x, y in zip(*got):
+        assert x.shape == y.shape and x.dtype == y.dtype and torch.equal(x, y)
+    assert isinstance(b._calls.paged_attention(Q, cache["K"], cache["V"], cache["k_scales"], cache["v_scales"], table,
+                                               t["seq_lens"], 0, None, None), dict)
+    assert b._calls.paged_append(K, V, t["slots"], cache["K"], cache["V"], cache["k_scales"],
+                                 cache["v_scales"]) == 0
+    with pytest.raises(b.SketchAttentionError):  # a status of the C ABI (an uneven workspace)
+        b.paged_attention(Q, cache, table, t["seq_lens"], ws=torch.empty(300, dtype=torch.uint8, device="cuda")[1:])
