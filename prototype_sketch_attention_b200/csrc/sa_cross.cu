@@ -95,21 +95,14 @@ __device__ __forceinline__ void stats_rows(const CrossArgs& a, int pg, long long
     if (i < rows) {
       const uint4 x = reinterpret_cast<const uint4*>(a.dout)[i * LANES + lane];
       const uint4 y = reinterpret_cast<const uint4*>(a.out)[i * LANES + lane];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+      uint4 r = make_uint4(0, 0, 0, 0);
+      if (a.rest) r = reinterpret_cast<const uint4*>(a.rest)[i * LANES + lane];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w}, w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
       for (int z = 0; z < 4; ++z) {
-        s = fmaf(__uint_as_float(u[z] << 16), __uint_as_float(v[z] << 16), s);
-        s = fmaf(__uint_as_float(u[z] & 0xffff0000u), __uint_as_float(v[z] & 0xffff0000u), s);
-      }
-    }
-    if (i < rows && a.rest) {
-      const uint4 x = reinterpret_cast<const uint4*>(a.dout)[i * LANES + lane];
-      const uint4 y = reinterpret_cast<const uint4*>(a.rest)[i * LANES + lane];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        s = fmaf(__uint_as_float(u[z] << 16), __uint_as_float(v[z] << 16), s);
-        s = fmaf(__uint_as_float(u[z] & 0xffff0000u), __uint_as_float(v[z] & 0xffff0000u), s);
+        s = fmaf(__uint_as_float(u[z] << 16), __uint_as_float(v[z] << 16) + __uint_as_float(w[z] << 16), s);
+        s = fmaf(__uint_as_float(u[z] & 0xffff0000u),
+                 __uint_as_float(v[z] & 0xffff0000u) + __uint_as_float(w[z] & 0xffff0000u), s);
       }
     }
 #pragma unroll
@@ -326,6 +319,7 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
     q.costs = take((size_t)(g.pair_tiles + 1) * sizeof(long long));
     q.starts = take((size_t)(g.ctas + 1) * sizeof(cross::Start));
     if (g.cuts) {
+      q.joins = take((size_t)g.ctas * (sizeof(cross::JoinItem) + sizeof(int)));
       q.part_o = take((size_t)2 * g.ctas * 256 * d * sizeof(float));
       q.part_lse = take((size_t)2 * g.ctas * 256 * sizeof(float));
     }

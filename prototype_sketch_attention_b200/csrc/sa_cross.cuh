@@ -205,6 +205,12 @@ struct Start {
   int tile, group, key, pad;
 };
 
+// The item that starts in a CTA of the forward and goes on in later ones: how many CTAs work on
+// it (0: there is none), its rows, its head group.
+struct JoinItem {
+  int parts, t0, t1, group;
+};
+
 // Launch geometry, from the sizes that the host knows (lengths live on the device).
 struct CrossGeo {
   int pg;                // heads packed into a tile

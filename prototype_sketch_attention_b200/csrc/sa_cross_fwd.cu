@@ -98,7 +98,10 @@ struct FwdParams {
   __nv_bfloat16* out;    // [n_q, H, D]
   __nv_bfloat16* rest;   // [n_q, H, D], nullable: out's rounding
   float* lse;            // [n_q, H]
-  float* part_o;         // [2 CTAs][256, D] (null: no boundary cuts an item)
+  JoinItem* joins;       // [CTAs]; null: no boundary cuts an item
+  int* join_ctas;        // [CTAs]: from b on, the CTAs behind CTA b that work on joins[b]
+  int ctas;
+  float* part_o;         // [2 CTAs][256, D]
   float* part_lse;       // [2 CTAs][256], log2 units
   long long budget;
 };
@@ -181,6 +184,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  griddep_launch_dependents();  // the join reads its inputs only after this grid has ended
   griddep_wait();  // the schedule
 
   const int groups = a.H / a.PG, tokens = 128 / a.PG;  // tokens per tile
@@ -387,6 +391,34 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         mbar_arrive(smem_u32(&bars->item_full[s & 1]));
         if (!more) break;
       }
+    }
+    __syncwarp();
+    if (a.joins) {  // what the join has to know, while the others work
+      const int b = blockIdx.x;
+      const Start at = a.starts[b], end = a.starts[b + 1];
+      const bool any = a.hdr->total_tiles > 0, same = at.tile == end.tile && at.group == end.group;
+      JoinItem it = {};
+      if (any && end.key > 0 && !(same && at.key > 0)) {
+        const Tile tl = a.tiles[end.tile];
+        it.t0 = (int)a.qoff[tl.user] + tl.index * 2 * tokens;
+        it.t1 = (int)a.qoff[tl.user + 1];
+        it.group = end.group;
+        it.parts = 1;
+        for (int x0 = b + 1;; x0 += 32) {  // until a boundary lies in another item
+          const int x = x0 + lane;
+          bool in = false, works = false;  // (rounded boundaries leave some CTAs with nothing)
+          if (x < a.ctas) {
+            const Start z = a.starts[x], y = a.starts[x + 1];
+            in = z.tile == end.tile && z.group == end.group;
+            works = in && !(z.tile == y.tile && z.group == y.group && z.key == y.key);
+          }
+          const unsigned w = __ballot_sync(0xffffffffu, works);
+          if (works) a.join_ctas[b + it.parts - 1 + __popc(w & ((1u << lane) - 1))] = x;
+          it.parts += __popc(w);
+          if (!__all_sync(0xffffffffu, in)) break;
+        }
+      }
+      if (lane == 0) a.joins[b] = it;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -648,99 +680,98 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   }
 }
 
-// Items that boundaries cut: block (b, y) joins rows [32 y, 32 y + 32) of the item that starts in CTA b
-// and goes on, from the parts of CTAs b, b + 1, ... in order: out = sum w O, w = 2^(lse2 - total).
-// Bound by the chain of loads, so every load that can be is in flight at once: the boundaries by
-// a warp, all parts' lse2 by the block, four rows' O by a warp. A part that saw no kept key
-// (lse2 = -inf), or whose CTA had nothing to do, left no O.
+// Items that boundaries cut: a warp of block (b, y) joins four rows of the item that starts in CTA b and
+// goes on, from the parts of the CTAs that worked on it, in order: out = sum w O, w = 2^(lse2 - total).
+// Bound by the chain of loads: the item and its CTAs; the parts' lse2 and the first two parts' O;
+// more O. (Looking the item up here and walking every CTA of it made one user's forward 18.6 us in
+// place of 15.3; 64 or 128 rows a block instead of 32 cost the odd batch 4 us.) A part that saw no
+// kept key (lse2 = -inf) left no O.
 template <int D>
-__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdParams a, int ctas) {
-  extern __shared__ float wts[];  // [parts][32]: lse2, then weights
-  __shared__ float total[32];
-  __shared__ int parts_s;
+__global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ FwdParams a) {
+  constexpr int C = D / 32;  // columns a lane
   griddep_wait();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r0 = blockIdx.y * 32;
-  const Start at = a.starts[b], cut = a.starts[b + 1];
-  if (a.hdr->total_tiles == 0 || cut.key == 0 || (at.tile == cut.tile && at.group == cut.group && at.key > 0)) return;
-  const Tile tl = a.tiles[cut.tile];
-  const int t0 = (int)a.qoff[tl.user] + tl.index * (256 / a.PG), t1 = (int)a.qoff[tl.user + 1];
-  if (t0 + r0 / a.PG >= t1) return;
-  if (warp == 0) {  // CTAs b .. b + parts - 1: until a boundary lies in another item
-    int n = 1;
-    while (true) {
-      const int x = b + n + lane;
-      bool same = false;
-      if (x < ctas) {
-        const Start z = a.starts[x];
-        same = z.tile == cut.tile && z.group == cut.group;
-      }
-      const unsigned other = __ballot_sync(0xffffffffu, !same);
-      n += other ? __ffs(other) - 1 : 32;
-      if (other) break;
-    }
-    if (lane == 0) parts_s = n;
-  }
-  __syncthreads();
-  const int parts = parts_s;
-  auto row_of = [&](int x) { return (long long)(x == 0 ? 2 * b + 1 : 2 * (b + x)) * 256 + r0; };
-  for (int i = tid; i < parts * 32; i += 256) {
-    const int x = i >> 5;
-    const Start z = a.starts[b + x], y = a.starts[b + x + 1];
-    const bool none = x > 0 && z.tile == y.tile && z.group == y.group && z.key == y.key;
-    wts[i] = none ? -INFINITY : a.part_lse[row_of(x) + (i & 31)];
-  }
-  __syncthreads();
-  if (tid < 32) {
-    float m = -INFINITY, l = 0.f;
-    for (int x = 0; x < parts; ++x) m = fmaxf(m, wts[x * 32 + tid]);
-    for (int x = 0; x < parts; ++x) {
-      const float ls = wts[x * 32 + tid], w = ls == -INFINITY ? 0.f : ex2_approx(ls - m);
-      l += w;
-      wts[x * 32 + tid] = w;
-    }
-    total[tid] = l == 0.f ? 0.f : 1.f / l;
-    const int t = t0 + (r0 + tid) / a.PG;
-    if (t < t1)
-      a.lse[(long long)t * a.H + cut.group * a.PG + (r0 + tid) % a.PG] =
-          l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kLn2;
-  }
-  __syncthreads();
-  float o[4][D / 32];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int y = 0; y < D / 32; ++y) o[i][y] = 0.f;
-#pragma unroll 2
-  for (int x = 0; x < parts; ++x) {
-    const float* po = a.part_o + (row_of(x) + 4 * warp) * D + lane * (D / 32);
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const JoinItem it = a.joins[b];
+  // lane: the CTA of part lane (and of parts lane + 32, ... where there are more)
+  const int cta0 = lane == 0 ? b : a.join_ctas[min(b + lane - 1, a.ctas - 1)];
+  const int r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * 4;
+  if (it.parts < 2 || it.t0 + r0 / a.PG >= it.t1) return;
+  int cta = cta0;
+  auto load = [&](int x, float (&v)[4][C]) {  // part x of the lanes' 32
+    const int c = __shfl_sync(0xffffffffu, cta, x & 31);
+    const float* po = a.part_o + ((long long)(x == 0 ? 2 * b + 1 : 2 * c) * 256 + r0) * D + lane * C;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float w = wts[x * 32 + 4 * warp + i];
-      if (w != 0.f) {
-        if (D == 128) {
-          const float4 v = *reinterpret_cast<const float4*>(po + i * D);
-          o[i][0] = fmaf(w, v.x, o[i][0]);
-          o[i][1] = fmaf(w, v.y, o[i][1]);
-          o[i][2 % (D / 32)] = fmaf(w, v.z, o[i][2 % (D / 32)]);
-          o[i][3 % (D / 32)] = fmaf(w, v.w, o[i][3 % (D / 32)]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(po + i * D);
-          o[i][0] = fmaf(w, v.x, o[i][0]);
-          o[i][1] = fmaf(w, v.y, o[i][1]);
-        }
+      if (D == 128) {
+        const float4 f = *reinterpret_cast<const float4*>(po + i * D);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
+        v[i][2 % C] = f.z;
+        v[i][3 % C] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(po + i * D);
+        v[i][0] = f.x;
+        v[i][1] = f.y;
       }
+    }
+  };
+  auto turn = [&](int x) {  // the lanes' CTAs for parts x .. x + 31
+    if (it.parts > 32) cta = x == 0 ? cta0 : a.join_ctas[min(b + x + lane - 1, a.ctas - 1)];
+  };
+  // lane: row lane mod 4 of part x + lane / 4
+  auto lse2 = [&](int x) {
+    const int k = x + (lane >> 2), c = __shfl_sync(0xffffffffu, cta, k & 31);
+    return k < it.parts ? a.part_lse[(long long)(k == 0 ? 2 * b + 1 : 2 * c) * 256 + r0 + (lane & 3)] : -INFINITY;
+  };
+  float v[2][4][C], o[4][C] = {};
+  load(0, v[0]);
+  load(1, v[1]);
+  float m = -INFINITY, l = 0.f;
+  for (int x = 0; x < it.parts; x += 8) {
+    if ((x & 31) == 0) turn(x);
+    m = fmaxf(m, lse2(x));
+  }
+#pragma unroll
+  for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+  for (int x0 = 0; x0 < it.parts; x0 += 8) {
+    if ((x0 & 31) == 0) turn(x0);
+    const float ls = lse2(x0), w = ls == -INFINITY ? 0.f : ex2_approx(ls - m);
+    l += w;
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {
+      if (x0 + x >= it.parts) break;
+      if (x0 + x > 0) {
+        load(x0 + x, v[0]);
+        if (x0 + x + 1 < it.parts) load(x0 + x + 1, v[1]);
+      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = __shfl_sync(0xffffffffu, w, 4 * (x + z) + i);
+          if (f != 0.f) {
+#pragma unroll
+            for (int y = 0; y < C; ++y) o[i][y] = fmaf(f, v[z][i][y], o[i][y]);
+          }
+        }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * warp + i, t = t0 + r / a.PG;
-    if (t >= t1) continue;
-    const float inv = total[4 * warp + i];
-    const long long at = (((long long)t * a.H + cut.group * a.PG + r % a.PG) * D + lane * (D / 32)) / 2;
+  for (int y = 4; y < 32; y <<= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int mine = r0 + (lane & 3), tm = it.t0 + mine / a.PG;
+  if (lane < 4 && tm < it.t1)
+    a.lse[(long long)tm * a.H + it.group * a.PG + mine % a.PG] = l == 0.f ? -INFINITY : (m + lg2_approx(l)) * kLn2;
 #pragma unroll
-    for (int y = 0; y < D / 64; ++y) {
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i, t = it.t0 + r / a.PG;
+    const float f = __shfl_sync(0xffffffffu, inv, i);
+    if (t >= it.t1) continue;
+    const long long at = (((long long)t * a.H + it.group * a.PG + r % a.PG) * D + lane * C) / 2;
+#pragma unroll
+    for (int y = 0; y < C / 2; ++y) {
       uint32_t rest;
-      reinterpret_cast<uint32_t*>(a.out)[at + y] = round_pair(o[i][2 * y] * inv, o[i][2 * y + 1] * inv, rest);
+      reinterpret_cast<uint32_t*>(a.out)[at + y] = round_pair(o[i][2 * y] * f, o[i][2 * y + 1] * f, rest);
       if (a.rest) reinterpret_cast<uint32_t*>(a.rest)[at + y] = rest;
     }
   }
@@ -768,6 +799,9 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.rest = static_cast<__nv_bfloat16*>(a.rest);
   p.lse = a.lse;
+  p.joins = geo.cuts ? reinterpret_cast<JoinItem*>(ws + a.plan.joins) : nullptr;
+  p.join_ctas = reinterpret_cast<int*>(p.joins + geo.ctas);
+  p.ctas = geo.ctas;
   p.part_o = reinterpret_cast<float*>(ws + a.plan.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + a.plan.part_lse);
   p.budget = kDefaultWaitBudget;
@@ -780,8 +814,7 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
                             p)) != cudaSuccess)
     return e;
   if (!geo.cuts) return cudaSuccess;
-  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256),
-                          (size_t)geo.ctas * 32 * sizeof(float), s, p, geo.ctas);
+  return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256), 0, s, p);
 }
 
 }  // namespace

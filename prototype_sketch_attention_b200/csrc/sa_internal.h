@@ -305,7 +305,7 @@ cudaError_t launch_sketch_unpack(const void* codes, const float* scales, long lo
 
 // ---- multi-head cross attention (sa_cross.cu)
 struct CrossPlan {  // workspace layout (byte offsets, 256-aligned)
-  size_t hdr = 0, qtiles = 0, ktiles = 0, costs = 0, starts = 0, part_o = 0, part_lse = 0, stats = 0, total = 0;
+  size_t hdr = 0, qtiles = 0, ktiles = 0, costs = 0, starts = 0, joins = 0, part_o = 0, part_lse = 0, stats = 0, total = 0;
 };
 size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, bool backward,
                   int sms, CrossPlan* p);
