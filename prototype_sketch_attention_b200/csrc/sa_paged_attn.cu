@@ -800,6 +800,15 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
   auto part_of = [&](int x) {  // the first CTA's last part, then the others' first parts
     return a.parts + ((long long)a.ctas * kMaxWarps * 2 + (b0 + x) * 2 + (x == 0 ? 1 : 0)) * Part<D, NT>::kStride;
   };
+  // thread t of a group holds float4 t: n-tile (t / 32) mod NT, heads 2 (t mod 4) + e; a group's first
+  // parts are loaded ahead of the weights
+  const int grp = tid / kV, t = tid % kV, hh = (t >> 5) % NT * 8 + 2 * (t & 3);
+  auto load = [&](int x) { return (reinterpret_cast<const float4*>(part_of(x)) + ci * kV)[t]; };
+  constexpr int kAhead = 4;
+  float4 ahead[kAhead];
+#pragma unroll
+  for (int y = 0; y < kAhead; ++y)
+    if (grp + y * kGroups < nb) ahead[y] = load(grp + y * kGroups);
   float* ms = ml;
   float* ls = ml + a.ctas * kHeads;
   for (int i = tid; i < nb * kHeads; i += 512) {
@@ -830,19 +839,20 @@ paged_join_kernel(const __grid_constant__ PagedParams a) {
     }
   }
   __syncthreads();
-  // thread t of a group holds float4 t: n-tile (t / 32) mod NT, heads 2 (t mod 4) + e
-  const int grp = tid / kV, t = tid % kV, hh = (t >> 5) % NT * 8 + 2 * (t & 3);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int x = grp; x < nb; x += kGroups) {
-    const float4* p = reinterpret_cast<const float4*>(part_of(x)) + ci * kV;
-    const float4 v = ls[x * kHeads] < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : p[t];
+  auto add = [&](int x, const float4& v) {
+    if (ls[x * kHeads] < 0.f) return;  // a CTA without tiles left nothing
     const float2 w = *reinterpret_cast<const float2*>(ms + x * kHeads + hh);
     acc.x = fmaf(v.x, w.x, acc.x);
     acc.y = fmaf(v.y, w.y, acc.y);
     acc.z = fmaf(v.z, w.x, acc.z);
     acc.w = fmaf(v.w, w.y, acc.w);
-  }
+  };
+#pragma unroll
+  for (int y = 0; y < kAhead; ++y)
+    if (grp + y * kGroups < nb) add(grp + y * kGroups, ahead[y]);
+#pragma unroll 4
+  for (int x = grp + kAhead * kGroups; x < nb; x += kGroups) add(x, load(x));
   acc_s[grp][t] = acc;
   __syncthreads();
   if (warp < kFrags) {  // a warp per fragment writes, as the main kernel's warps do
