@@ -84,7 +84,7 @@ def _build_calls(force: bool) -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in includes for x in ("-isystem" if d != INCLUDE else "-I", d)], src, "-o", tmp,
            "-L", PKG, "-l:libsa_sketch.so", "-Wl,-rpath,$ORIGIN",
-           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for sa_calls.cpp:\n{r.stdout}\n{r.stderr}")
