@@ -364,3 +364,27 @@ def test_nan_in_a_kept_row_stays_with_its_user_and_heads(lq, lk, d):
         assert f["out"][hit].isnan().all() and f["lse"][hit].isnan().all()
         assert torch.equal(f["out"][~hit], clean["out"][~hit]) and torch.equal(f["lse"][~hit], clean["lse"][~hit])
     assert b.device_status(f["_ws"]) == 0
+
+
+def test_short_calls_follow_the_current_stream_and_take_parameters():
+    """The extension's calls run on the stream that is current; nn.Parameter inputs give the same results."""
+    from prototype_sketch_attention_b200 import binding as b
+    Q, K, V, dout = _inputs([70, 3], [300, 40], 4, 2, 64, seed=990)
+    qo, ko = _dev(_offsets([70, 3])), _dev(_offsets([300, 40]))
+    base = _run(Q, [0, 70, 73], K, V, [0, 300, 340], dout)
+    s, gate = torch.cuda.Stream(), torch.cuda.Event()
+    late = torch.empty_like(K)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):  # K is written on this stream first: another one would read it too early
+        torch.cuda._sleep(20_000_000)
+        late.copy_(K)
+        f = b.cross_attention(Q, qo, late, V, ko)
+        g = b.cross_attention_backward(Q, qo, late, V, ko, f, dout)
+        gate.record()
+    gate.synchronize()
+    assert all(torch.equal({**f, **g}[n], base[n]) for n in NAMES)
+    P = [torch.nn.Parameter(x) for x in (Q, K, V)]
+    f = b.cross_attention(P[0], qo, P[1], P[2], ko)
+    g = b.cross_attention_backward(P[0], qo, P[1], P[2], ko, f, dout)
+    torch.cuda.synchronize()
+    assert all(torch.equal({**f, **g}[n], base[n]) and not {**f, **g}[n].requires_grad for n in NAMES)
