@@ -261,14 +261,15 @@ def sketch_pack(S: torch.Tensor, fmt: int = SA_CODEC_FP8, stream=None) -> dict:
     _check_tensor(where, "S", S, tuple(S.shape), torch.float32, S.device)
     _check_cuda(where, S)
     dt = torch.uint8 if fmt == SA_CODEC_FP8 else torch.bfloat16
-    out = {"codes": torch.empty(S.shape, dtype=dt, device=S.device),
-           "scales": (torch.empty(S.shape[:-1], dtype=torch.float32, device=S.device)
-                      if fmt == SA_CODEC_FP8 else None), "format": fmt}
-    with torch.cuda.device(S.device):
+    with _on(where, S.device, stream):
+        out = {"codes": torch.empty(S.shape, dtype=dt, device=S.device),
+               "scales": (torch.empty(S.shape[:-1], dtype=torch.float32, device=S.device)
+                          if fmt == SA_CODEC_FP8 else None), "format": fmt}
         st = sa_sketch_pack(_ptr(S), rows, d, fmt, _ptr(out["codes"]), _ptr(out["scales"]),
                             _stream(stream, S.device))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_pack")
+    _used_on(stream, S.device, S, out)
     return out
 
 
@@ -276,12 +277,13 @@ def sketch_unpack(packed: dict, stream=None) -> torch.Tensor:
     """The fp32 sketches back from sketch_pack's output."""
     codes, fmt = packed["codes"], packed["format"]
     d = codes.shape[-1]
-    S = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-    with torch.cuda.device(codes.device):
+    with _on("sketch_unpack", codes.device, stream):
+        S = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
         st = sa_sketch_unpack(_ptr(codes), _ptr(packed.get("scales")), codes.numel() // d, d, fmt,
                               _ptr(S), _stream(stream, codes.device))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_unpack")
+    _used_on(stream, codes.device, packed, S)
     return S
 
 
@@ -380,13 +382,19 @@ def _stream(stream, device=None) -> int:
     return s.cuda_stream
 
 
-def _used_on(stream, out: dict) -> None:
-    """A result that is dropped early stays allocated until the given stream has passed this call:
-    its tensors may come from another stream's pool."""
-    if stream is not None:
-        for t in out.values():
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
+def _used_on(stream, dev, *args) -> None:
+    """For a call on a given stream: its tensors (in tuples and dictionaries too) that are dropped
+    early stay allocated until that stream has passed the call, and its results, which come from
+    that stream's pool, until the caller's stream has passed what it does with them."""
+    if stream is None:
+        return
+    here = torch.cuda.current_stream(dev)
+    for x in args:
+        if isinstance(x, torch.Tensor):
+            x.record_stream(stream)  # (nothing, for a tensor of the stream's own pool)
+            x.record_stream(here)
+        elif isinstance(x, (tuple, list, dict)):
+            _used_on(stream, dev, *(x.values() if isinstance(x, dict) else x))
 
 
 def _fail(where: str, what: str):
@@ -404,6 +412,20 @@ _HERE = contextlib.nullcontext()
 def _device(dev: torch.device):
     """Makes `dev` current for a call; nothing to do when it is (the guard costs microseconds)."""
     return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+@contextlib.contextmanager
+def _on(where: str, dev: torch.device, stream):
+    """The device and, if one is given, the stream of a call, current while it allocates and launches.
+    A block of another stream's pool may still be in use by work queued there, which the given
+    stream does not wait for."""
+    if stream is None:
+        with _device(dev):
+            yield
+        return
+    _require(stream.device == dev, where, f"stream is on {stream.device}, the inputs on {dev}")
+    with torch.cuda.stream(stream):
+        yield
 
 
 def _check_tensor(where: str, name: str, t: torch.Tensor | None, shape: tuple, dtype,
@@ -473,20 +495,21 @@ def forward(X: torch.Tensor, offsets: torch.Tensor, P: torch.Tensor, Wk: torch.T
     R = offsets.shape[0] - 1
     dt = _dt(X)
     dev = X.device
-    if out is None:
-        out = {"sketch": torch.empty(R, k, d, device=dev, dtype=torch.float32),
-               "mass": torch.empty(R, k, device=dev, dtype=torch.float32)}
-        if want_lse:
-            out["lse"] = torch.empty(n_total, device=dev, dtype=torch.float32)
-        if want_xsketch:
-            out["xsketch"] = torch.empty(R, k, d, device=dev, dtype=torch.float32)
     f32 = torch.float32
-    _check_tensor(where, "sketch", out.get("sketch"), (R, k, d), f32, dev)
-    _check_tensor(where, "mass", out.get("mass"), (R, k), f32, dev)
-    _check_tensor(where, "lse", out.get("lse"), (n_total,), f32, dev, optional=True)
-    _check_tensor(where, "xsketch", out.get("xsketch"), (R, k, d), f32, dev, optional=True)
+    if out is not None:
+        _check_tensor(where, "sketch", out.get("sketch"), (R, k, d), f32, dev)
+        _check_tensor(where, "mass", out.get("mass"), (R, k), f32, dev)
+        _check_tensor(where, "lse", out.get("lse"), (n_total,), f32, dev, optional=True)
+        _check_tensor(where, "xsketch", out.get("xsketch"), (R, k, d), f32, dev, optional=True)
     _check_cuda(where, X)
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        if out is None:
+            out = {"sketch": torch.empty(R, k, d, device=dev, dtype=f32),
+                   "mass": torch.empty(R, k, device=dev, dtype=f32)}
+            if want_lse:
+                out["lse"] = torch.empty(n_total, device=dev, dtype=f32)
+            if want_xsketch:
+                out["xsketch"] = torch.empty(R, k, d, device=dev, dtype=f32)
         if ws is None:
             ws = workspace(R, n_total, k, d, X.dtype, False, dev)
         _require(ws.device == dev and ws.is_contiguous(), where,
@@ -498,6 +521,7 @@ def forward(X: torch.Tensor, offsets: torch.Tensor, P: torch.Tensor, Wk: torch.T
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_forward")
     out["_ws"] = ws
+    _used_on(stream, dev, X, offsets, P, Wk, Wv, out)
     return out
 
 
@@ -522,11 +546,11 @@ def backward(X, offsets, P, Wk, Wv, fwd: dict, dsketch: torch.Tensor, dmass=None
     _check_tensor(where, "dsketch", dsketch, (R, k, d), f32, dev)
     _check_tensor(where, "dmass", dmass, (R, k), f32, dev, optional=True)
     _check_cuda(where, X)
-    out = {"dX": torch.empty(n_total, d, device=dev, dtype=f32),
-           "dP": torch.empty(k, d, device=dev, dtype=f32),
-           "dWk": torch.empty(d, d, device=dev, dtype=f32),
-           "dWv": torch.empty(d, d, device=dev, dtype=f32)}
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        out = {"dX": torch.empty(n_total, d, device=dev, dtype=f32),
+               "dP": torch.empty(k, d, device=dev, dtype=f32),
+               "dWk": torch.empty(d, d, device=dev, dtype=f32),
+               "dWv": torch.empty(d, d, device=dev, dtype=f32)}
         if ws is None:
             ws = workspace(R, n_total, k, d, X.dtype, True, dev)
         _require(ws.device == dev and ws.is_contiguous(), where,
@@ -539,6 +563,7 @@ def backward(X, offsets, P, Wk, Wv, fwd: dict, dsketch: torch.Tensor, dmass=None
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_backward")
     out["_ws"] = ws
+    _used_on(stream, dev, X, offsets, P, Wk, Wv, fwd, dsketch, dmass, out)
     return out
 
 
@@ -558,15 +583,16 @@ def combine(xsketch: torch.Tensor, mass: torch.Tensor, Wv: torch.Tensor, *,
     _require(isinstance(Wv, torch.Tensor), where, "Wv must be a tensor")
     _check_tensor(where, "Wv", Wv, (d, d), Wv.dtype, dev)
     dt = _dt(Wv)
-    if out is None:
-        out = torch.empty(R, k, d, device=dev, dtype=f32)
-    _check_tensor(where, "out", out, (R, k, d), f32, dev)
+    _check_tensor(where, "out", out, (R, k, d), f32, dev, optional=True)
     _check_cuda(where, xsketch)
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        if out is None:
+            out = torch.empty(R, k, d, device=dev, dtype=f32)
         st = sa_sketch_combine(_ptr(xsketch), _ptr(mass), R, k, d, _ptr(Wv), dt, _ptr(out),
                                _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_combine")
+    _used_on(stream, dev, xsketch, mass, Wv, out)
     return out
 
 
@@ -592,10 +618,10 @@ def stca_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, W
     for name, W in (("Wq", Wq), ("WK", WK), ("WV", WV)):
         _check_tensor(where, name, W, (d, d), bf, dev)
     _check_cuda(where, Q)
-    out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
-    if want_lse:
-        out["lse"] = torch.empty(n_cand, device=dev, dtype=torch.float32)
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
+        if want_lse:
+            out["lse"] = torch.empty(n_cand, device=dev, dtype=torch.float32)
         if ws is None:
             nb = sa_stca_workspace_size(R, n_cand, k, d, 0)
             if nb == 0:
@@ -607,6 +633,7 @@ def stca_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, W
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_forward")
     out["_ws"] = ws
+    _used_on(stream, dev, Q, cand_offsets, S, Wq, WK, WV, out)
     return out
 
 
@@ -640,12 +667,12 @@ def stca_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, 
         _check_tensor(where, "cand_offsets_host", cand_offsets_host, (R + 1,), torch.int64,
                       torch.device("cpu"))
         coff_h = cand_offsets_host
-    out = {"dQ": torch.empty(n_cand, d, device=dev, dtype=f32),
-           "dS": torch.empty(R, k, d, device=dev, dtype=f32),
-           "dWq": torch.empty(d, d, device=dev, dtype=f32),
-           "dWK": torch.empty(d, d, device=dev, dtype=f32),
-           "dWV": torch.empty(d, d, device=dev, dtype=f32)}
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        out = {"dQ": torch.empty(n_cand, d, device=dev, dtype=f32),
+               "dS": torch.empty(R, k, d, device=dev, dtype=f32),
+               "dWq": torch.empty(d, d, device=dev, dtype=f32),
+               "dWK": torch.empty(d, d, device=dev, dtype=f32),
+               "dWV": torch.empty(d, d, device=dev, dtype=f32)}
         if ws is None:
             nb = sa_stca_workspace_size(R, n_cand, k, d, 1)
             if nb == 0:
@@ -658,6 +685,7 @@ def stca_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, 
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_backward")
     out["_ws"] = ws
+    _used_on(stream, dev, Q, cand_offsets, S, Wq, WK, WV, dout, out)
     return out
 
 
@@ -671,13 +699,14 @@ def recent_ranges(offsets: torch.Tensor, L: int, *, stream=None) -> tuple[torch.
     dev = offsets.device
     _check_tensor(where, "offsets", offsets, (R + 1,), torch.int64, dev)
     _check_cuda(where, offsets)
-    kb = torch.empty(R, dtype=torch.int64, device=dev)
-    ke = torch.empty(R, dtype=torch.int64, device=dev)
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        kb = torch.empty(R, dtype=torch.int64, device=dev)
+        ke = torch.empty(R, dtype=torch.int64, device=dev)
         st = sa_stca_recent_ranges(_ptr(offsets), R, int(L), _ptr(kb), _ptr(ke),
                                    _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_recent_ranges")
+    _used_on(stream, dev, offsets, kb, ke)
     return kb, ke
 
 
@@ -713,10 +742,10 @@ def stca_keys_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Ten
     where = "stca_keys_forward"
     n_cand, d, R, n_keys, dev = _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end,
                                                    Wq, WK, WV)
-    out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
-    if want_lse:
-        out["lse"] = torch.empty(n_cand, device=dev, dtype=torch.float32)
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
+        if want_lse:
+            out["lse"] = torch.empty(n_cand, device=dev, dtype=torch.float32)
         if ws is None:
             nb = sa_stca_keys_workspace_size(R, n_cand, d, 0)
             if nb == 0:
@@ -729,6 +758,7 @@ def stca_keys_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Ten
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_keys_forward")
     out["_ws"] = ws
+    _used_on(stream, dev, Q, cand_offsets, Kx, key_begin, key_end, Wq, WK, WV, out)
     return out
 
 
@@ -748,12 +778,12 @@ def stca_keys_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Te
     _check_tensor(where, "dout", dout, (n_cand, d), f32, dev)
     _check_tensor(where, "dKx", dKx, (n_keys, d), f32, dev, optional=True)
     accumulate = dKx is not None
-    out = {"dQ": torch.empty(n_cand, d, device=dev, dtype=f32),
-           "dKx": dKx if accumulate else torch.empty(n_keys, d, device=dev, dtype=f32),
-           "dWq": torch.empty(d, d, device=dev, dtype=f32),
-           "dWK": torch.empty(d, d, device=dev, dtype=f32),
-           "dWV": torch.empty(d, d, device=dev, dtype=f32)}
-    with torch.cuda.device(dev):
+    with _on(where, dev, stream):
+        out = {"dQ": torch.empty(n_cand, d, device=dev, dtype=f32),
+               "dKx": dKx if accumulate else torch.empty(n_keys, d, device=dev, dtype=f32),
+               "dWq": torch.empty(d, d, device=dev, dtype=f32),
+               "dWK": torch.empty(d, d, device=dev, dtype=f32),
+               "dWV": torch.empty(d, d, device=dev, dtype=f32)}
         if ws is None:
             nb = sa_stca_keys_workspace_size(R, n_cand, d, 1)
             if nb == 0:
@@ -767,6 +797,7 @@ def stca_keys_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Te
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_stca_keys_backward")
     out["_ws"] = ws
+    _used_on(stream, dev, Q, cand_offsets, Kx, key_begin, key_end, Wq, WK, WV, dout, out)
     return out
 
 
@@ -844,17 +875,17 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
     where = "cross_attention"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
                                                               key_mask)
-    if out is None:
-        out = {"out": torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16),
-               "lse": torch.empty(n_q, H, device=dev, dtype=torch.float32)}
-        if want_rest:
-            out["rest"] = torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16)
-    else:
+    if out is not None:
         out = dict(out)
         _check_tensor(where, "out", out.get("out"), (n_q, H, d), torch.bfloat16, dev)
         _check_tensor(where, "rest", out.get("rest"), (n_q, H, d), torch.bfloat16, dev, optional=True)
         _check_tensor(where, "lse", out.get("lse"), (n_q, H), torch.float32, dev)
-    with _device(dev):
+    with _on(where, dev, stream):
+        if out is None:
+            out = {"out": torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16),
+                   "lse": torch.empty(n_q, H, device=dev, dtype=torch.float32)}
+            if want_rest:
+                out["rest"] = torch.empty(n_q, H, d, device=dev, dtype=torch.bfloat16)
         if ws is None:
             nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 0)
             if nb == 0:
@@ -867,7 +898,7 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_forward")
     out["_ws"] = ws
-    _used_on(stream, out)
+    _used_on(stream, dev, Q, q_offsets, K, V, kv_offsets, key_mask, out)
     return out
 
 
@@ -893,16 +924,16 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     _check_tensor(where, "lse", fwd.get("lse"), (n_q, H), torch.float32, dev)
     _check_tensor(where, "rest", fwd.get("rest"), (n_q, H, d), bf, dev, optional=True)
     _check_tensor(where, "dout", dout, (n_q, H, d), bf, dev)
-    if out is None:
-        out = {"dQ": torch.empty(n_q, H, d, device=dev, dtype=bf),
-               "dK": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf),
-               "dV": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf)}
-    else:
+    if out is not None:
         out = dict(out)
         _check_tensor(where, "dQ", out.get("dQ"), (n_q, H, d), bf, dev)
         _check_tensor(where, "dK", out.get("dK"), (n_kv, Hkv, d), bf, dev)
         _check_tensor(where, "dV", out.get("dV"), (n_kv, Hkv, d), bf, dev)
-    with _device(dev):
+    with _on(where, dev, stream):
+        if out is None:
+            out = {"dQ": torch.empty(n_q, H, d, device=dev, dtype=bf),
+                   "dK": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf),
+                   "dV": torch.empty(n_kv, Hkv, d, device=dev, dtype=bf)}
         if ws is None:
             nb = sa_cross_attn_workspace_size(R, n_q, n_kv, H, Hkv, d, 1)
             if nb == 0:
@@ -916,7 +947,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_cross_attn_backward")
     out["_ws"] = ws
-    _used_on(stream, out)
+    _used_on(stream, dev, Q, q_offsets, K, V, kv_offsets, key_mask, fwd, dout, out)
     return out
 
 
@@ -988,13 +1019,13 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     _check_tensor(where, "free_used", free_used, (1,), i64, dev, optional=True)
     _check_cuda(where, cached_lens)
     _require(int(n_slots) >= 0, where, "n_slots must not be negative")
-    out = {"slots": torch.empty(int(n_slots), dtype=i64, device=dev),
-           "new_offsets": torch.empty(R + 1, dtype=i64, device=dev),
-           "seq_lens": torch.empty(R, dtype=i32, device=dev),
-           "free_used": torch.empty(1, dtype=i64, device=dev)}
-    if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=dev)
-    with _device(dev):
+    with _on(where, dev, stream):
+        out = {"slots": torch.empty(int(n_slots), dtype=i64, device=dev),
+               "new_offsets": torch.empty(R + 1, dtype=i64, device=dev),
+               "seq_lens": torch.empty(R, dtype=i32, device=dev),
+               "free_used": torch.empty(1, dtype=i64, device=dev)}
+        if ws is None:
+            ws = torch.empty(256, dtype=torch.uint8, device=dev)
         st = sa_page_tables(_ptr(cached_lens), _ptr(new_lens), R, int(page_size), _ptr(free_pages),
                             free_pages.numel(), _ptr(free_used), _ptr(block_table),
                             block_table.shape[1], int(n_slots), _ptr(out["slots"]),
@@ -1003,7 +1034,7 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_page_tables")
     out["_ws"] = ws
-    _used_on(stream, out)
+    _used_on(stream, dev, cached_lens, new_lens, free_pages, block_table, free_used, out)
     return out
 
 
@@ -1028,12 +1059,13 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
     _check_tensor(where, "slots", slots, (K.shape[0],), torch.int64, dev)
     _check_cuda(where, K)
     ks, vs = _rows_stride(where, "K", K, Hkv, d), _rows_stride(where, "V", V, Hkv, d)
-    with _device(dev):
+    with _on(where, dev, stream):
         st = sa_paged_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), K.shape[0], Hkv, d, fmt,
                              _ptr(cache["K"]), _ptr(cache["V"]), _ptr(cache["k_scales"]),
                              _ptr(cache["v_scales"]), n_pages, page_size, _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_paged_append")
+    _used_on(stream, dev, K, V, slots, cache)
 
 
 def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
@@ -1061,9 +1093,9 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     _check_tensor(where, "seq_lens", seq_lens, (R,), torch.int32, dev)
     _check_cuda(where, Q)
     qs = _rows_stride(where, "Q", Q, H, d)
-    out = {"out": torch.empty(R, H, d, device=dev, dtype=torch.bfloat16),
-           "lse": torch.empty(R, H, device=dev, dtype=torch.float32)}
-    with _device(dev):
+    with _on(where, dev, stream):
+        out = {"out": torch.empty(R, H, d, device=dev, dtype=torch.bfloat16),
+               "lse": torch.empty(R, H, device=dev, dtype=torch.float32)}
         if ws is None:
             nb = sa_paged_attn_workspace_size(R, H, Hkv, d)
             if nb == 0:
@@ -1077,7 +1109,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_paged_attn")
     out["_ws"] = ws
-    _used_on(stream, out)
+    _used_on(stream, dev, Q, cache, block_table, seq_lens, out)
     return out
 
 
