@@ -453,6 +453,13 @@ def _check_cuda(where: str, X: torch.Tensor) -> None:
         _fail(where, f"inputs are on {X.device}; the library runs on CUDA devices only")
 
 
+def _check_ws(where: str, ws, dev) -> None:
+    """A workspace that the caller gives: the library sees its pointer and its size, so those bytes
+    have to be there, on the inputs' device (their number is the library's to check)."""
+    if ws is not None and not (isinstance(ws, torch.Tensor) and ws.device == dev and ws.is_contiguous()):
+        _fail(where, f"ws must be a contiguous tensor on {dev}")
+
+
 def _check_forward_inputs(where, X, offsets, P, Wk, Wv):
     _require(isinstance(X, torch.Tensor) and X.dim() == 2, where, "X must be a 2-D tensor")
     _require(isinstance(P, torch.Tensor) and P.dim() == 2, where, "P must be a 2-D tensor")
@@ -496,6 +503,7 @@ def forward(X: torch.Tensor, offsets: torch.Tensor, P: torch.Tensor, Wk: torch.T
     dt = _dt(X)
     dev = X.device
     f32 = torch.float32
+    _check_ws(where, ws, dev)
     if out is not None:
         _check_tensor(where, "sketch", out.get("sketch"), (R, k, d), f32, dev)
         _check_tensor(where, "mass", out.get("mass"), (R, k), f32, dev)
@@ -512,8 +520,6 @@ def forward(X: torch.Tensor, offsets: torch.Tensor, P: torch.Tensor, Wk: torch.T
                 out["xsketch"] = torch.empty(R, k, d, device=dev, dtype=f32)
         if ws is None:
             ws = workspace(R, n_total, k, d, X.dtype, False, dev)
-        _require(ws.device == dev and ws.is_contiguous(), where,
-                 "ws must be contiguous on X's device")
         st = sa_sketch_forward(_ptr(X), _ptr(offsets), R, n_total, d, _ptr(P), k, _ptr(Wk),
                                _ptr(Wv), dt, _ptr(out["sketch"]), _ptr(out["mass"]),
                                _ptr(out.get("lse")), _ptr(out.get("xsketch")), _ptr(ws),
@@ -545,6 +551,7 @@ def backward(X, offsets, P, Wk, Wv, fwd: dict, dsketch: torch.Tensor, dmass=None
     _check_tensor(where, "lse", fwd.get("lse"), (n_total,), f32, dev, optional=True)
     _check_tensor(where, "dsketch", dsketch, (R, k, d), f32, dev)
     _check_tensor(where, "dmass", dmass, (R, k), f32, dev, optional=True)
+    _check_ws(where, ws, dev)
     _check_cuda(where, X)
     with _on(where, dev, stream):
         out = {"dX": torch.empty(n_total, d, device=dev, dtype=f32),
@@ -553,8 +560,6 @@ def backward(X, offsets, P, Wk, Wv, fwd: dict, dsketch: torch.Tensor, dmass=None
                "dWv": torch.empty(d, d, device=dev, dtype=f32)}
         if ws is None:
             ws = workspace(R, n_total, k, d, X.dtype, True, dev)
-        _require(ws.device == dev and ws.is_contiguous(), where,
-                 "ws must be contiguous on X's device")
         st = sa_sketch_backward(_ptr(X), _ptr(offsets), R, n_total, d, _ptr(P), k, _ptr(Wk),
                                 _ptr(Wv), dt, _ptr(fwd["sketch"]), _ptr(fwd["mass"]),
                                 _ptr(fwd.get("lse")), _ptr(fwd["xsketch"]), _ptr(dsketch),
@@ -617,6 +622,7 @@ def stca_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, W
     _check_tensor(where, "S", S, (R, k, d), torch.float32, dev)
     for name, W in (("Wq", Wq), ("WK", WK), ("WV", WV)):
         _check_tensor(where, name, W, (d, d), bf, dev)
+    _check_ws(where, ws, dev)
     _check_cuda(where, Q)
     with _on(where, dev, stream):
         out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
@@ -660,6 +666,7 @@ def stca_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, S: torch.Tensor, 
     for name, W in (("Wq", Wq), ("WK", WK), ("WV", WV)):
         _check_tensor(where, name, W, (d, d), bf, dev)
     _check_tensor(where, "dout", dout, (n_cand, d), f32, dev)
+    _check_ws(where, ws, dev)
     _check_cuda(where, Q)
     if cand_offsets_host is None:
         coff_h = cand_offsets.cpu().contiguous()
@@ -710,7 +717,7 @@ def recent_ranges(offsets: torch.Tensor, L: int, *, stream=None) -> tuple[torch.
     return kb, ke
 
 
-def _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end, Wq, WK, WV):
+def _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end, Wq, WK, WV, ws):
     _require(isinstance(Q, torch.Tensor) and Q.dim() == 2, where, "Q must be a 2-D tensor")
     _require(isinstance(Kx, torch.Tensor) and Kx.dim() == 2, where, "Kx must be a 2-D tensor")
     _require(isinstance(cand_offsets, torch.Tensor) and cand_offsets.dim() == 1
@@ -726,6 +733,7 @@ def _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end, Wq, WK, W
     _check_tensor(where, "key_end", key_end, (R,), torch.int64, dev)
     for name, W in (("Wq", Wq), ("WK", WK), ("WV", WV)):
         _check_tensor(where, name, W, (d, d), bf, dev)
+    _check_ws(where, ws, dev)
     _check_cuda(where, Q)
     return n_cand, d, R, Kx.shape[0], dev
 
@@ -741,7 +749,7 @@ def stca_keys_forward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Ten
     lse [n_cand])."""
     where = "stca_keys_forward"
     n_cand, d, R, n_keys, dev = _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end,
-                                                   Wq, WK, WV)
+                                                   Wq, WK, WV, ws)
     with _on(where, dev, stream):
         out = {"out": torch.empty(n_cand, d, device=dev, dtype=torch.float32)}
         if want_lse:
@@ -773,7 +781,7 @@ def stca_keys_backward(Q: torch.Tensor, cand_offsets: torch.Tensor, Kx: torch.Te
     (for the recent branch: into the history gradient)."""
     where = "stca_keys_backward"
     n_cand, d, R, n_keys, dev = _check_keys_inputs(where, Q, cand_offsets, Kx, key_begin, key_end,
-                                                   Wq, WK, WV)
+                                                   Wq, WK, WV, ws)
     f32 = torch.float32
     _check_tensor(where, "dout", dout, (n_cand, d), f32, dev)
     _check_tensor(where, "dKx", dKx, (n_keys, d), f32, dev, optional=True)
@@ -833,7 +841,7 @@ def _scale(scale, d: int) -> float:
     return float(d) ** -0.5 if scale is None else float(scale)
 
 
-def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
+def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask, ws):
     _require(isinstance(Q, torch.Tensor) and Q.dim() == 3, where, "Q must be [n, heads, d]")
     _require(isinstance(K, torch.Tensor) and K.dim() == 3, where, "K must be [n, heads, d]")
     dev, (n_q, H, d), (n_kv, Hkv, _) = Q.device, Q.shape, K.shape
@@ -851,6 +859,7 @@ def _check_cross(where, Q, q_offsets, K, V, kv_offsets, key_mask):
         _require(isinstance(key_mask, torch.Tensor) and key_mask.dtype in (torch.bool, torch.uint8),
                  where, "key_mask must be a bool or uint8 tensor")
         _check_tensor(where, "key_mask", key_mask, (n_kv,), key_mask.dtype, dev)
+    _check_ws(where, ws, dev)
     _check_cuda(where, Q)
     strides = (_rows_stride(where, "Q", Q, H, d), _rows_stride(where, "K", K, Hkv, d),
                _rows_stride(where, "V", V, Hkv, d))
@@ -874,7 +883,7 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
             return _result(res, "sa_cross_attn_forward")
     where = "cross_attention"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
-                                                              key_mask)
+                                                              key_mask, ws)
     if out is not None:
         out = dict(out)
         _check_tensor(where, "out", out.get("out"), (n_q, H, d), torch.bfloat16, dev)
@@ -918,7 +927,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
             return _result(res, "sa_cross_attn_backward")
     where = "cross_attention_backward"
     R, n_q, H, d, n_kv, Hkv, dev, (qs, ks, vs) = _check_cross(where, Q, q_offsets, K, V, kv_offsets,
-                                                              key_mask)
+                                                              key_mask, ws)
     bf = torch.bfloat16
     _check_tensor(where, "out", fwd.get("out"), (n_q, H, d), bf, dev)
     _check_tensor(where, "lse", fwd.get("lse"), (n_q, H), torch.float32, dev)
@@ -1017,6 +1026,7 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
              "block_table must be [R, max_pages]")
     _check_tensor(where, "block_table", block_table, (R, block_table.shape[1]), i32, dev)
     _check_tensor(where, "free_used", free_used, (1,), i64, dev, optional=True)
+    _check_ws(where, ws, dev)
     _check_cuda(where, cached_lens)
     _require(int(n_slots) >= 0, where, "n_slots must not be negative")
     with _on(where, dev, stream):
@@ -1091,6 +1101,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
              "block_table must be [R, max_pages]")
     _check_tensor(where, "block_table", block_table, (R, block_table.shape[1]), torch.int32, dev)
     _check_tensor(where, "seq_lens", seq_lens, (R,), torch.int32, dev)
+    _check_ws(where, ws, dev)
     _check_cuda(where, Q)
     qs = _rows_stride(where, "Q", Q, H, d)
     with _on(where, dev, stream):

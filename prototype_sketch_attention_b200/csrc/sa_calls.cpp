@@ -98,7 +98,7 @@ PyObject *kOut, *kLse, *kRest, *kWs, *kDQ, *kDK, *kDV, *kSlots, *kNewOffsets, *k
 bool workspace(Args& a, int i, size_t bytes, Tensor* ws) {
   if (!a.none(i)) {
     const Tensor* t = a.tensor(i);
-    if (!t || !a.need(t->is_cuda() && t->device() == a.dev)) return false;
+    if (!t || !a.need(t->device() == a.dev && t->is_contiguous())) return false;  // (nbytes of them are there)
     *ws = *t;
     return true;
   }
