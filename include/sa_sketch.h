@@ -589,8 +589,8 @@ int sa_paged_append(const void* K, int64_t k_stride, const void* V, int64_t v_st
  * max_pages page_size <= INT32_MAX - 256; R <= SA_MAX_USERS. Precision as for the forward
  * above. FP8: the codes are exact in fp16, Q is as well but for what lies 2^-33 under a
  * head's largest value, K's scales enter in fp32, and a weight times its row's v_scale is
- * rounded to fp16 (2^-12 of its value; below 2^-14 of the largest v_scale of the positions
- * read, 2^-25 of that). Workspace: sa_paged_attn_workspace_size(...) bytes, 256-aligned.
+ * rounded to fp16: by 2^-11 of its value, or by 2^-24 of the head's largest such product where it
+ * is below 2^-13 of that. Workspace: sa_paged_attn_workspace_size(...) bytes, 256-aligned.
  */
 size_t sa_paged_attn_workspace_size(int R, int H, int Hkv, int d);
 int sa_paged_attn(const void* Q, int64_t q_stride, int R, int H, int d, const void* k_cache,

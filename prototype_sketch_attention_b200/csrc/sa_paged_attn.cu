@@ -18,15 +18,18 @@
 //
 // FP8 codes go to fp16 exactly (one conversion instruction a pair), and the products run in fp16.
 // A head's query is brought to [2^8, 2^9) by a power of two, which costs nothing that fp32 sums
-// would keep (what falls below fp16's steps is 2^-33 of the largest value); the weights are
-// p v_scale / 2^e with 2^e the power of two above the largest v_scale so far, so they stay
-// below 2^8 and are rounded to 2^-12 of their value, or to 2^-25 where they are below 2^-14 (so what
-// rows with a scale below 2^-14 of the largest give loses digits). The same steps through bf16 took
+// would keep (what falls below fp16's steps is 2^-33 of the largest value). The second product's weights are
+// p v_scale in a unit of each head's own, from its largest p v_scale so far: a value row's scale alone says
+// little (the append gives a row of zeros the scale 1 among any neighbours: in a unit from the scales,
+// neighbours of 1e-4 would lose all digits). The largest is at 1/2 to 2^8, and weights are rounded by 2^-11
+// of their value, or by 2^-25 where they are below 2^-14. The same steps through bf16 took
 // 9 integer instructions a word in place of 2 or 3. A key's scale multiplies its scores in fp32.
 // Measured (of the 6,568 GB/s of a copy): 40 requests x 10K positions, 12 heads over 4, bf16: 0.141 ms
-// (0.88); 300 x 1K-100K, 8 heads over 1, FP8: 0.300 ms (0.93; through bf16 0.393); 16 heads over one
-// in FP8: 0.69, and 0.53 at d = 64, where the products' issue is the bound; one request of 1,900
-// positions 10.6 us, one of 100,000 24 us.
+// (0.88); 300 x 1K-100K, 8 heads over 1, FP8: 0.300 ms (0.93; through bf16 0.393); 16 heads over 1 on
+// such requests: 0.32 ms (0.82), and 0.19 to 0.20 at d = 64 (0.66 to 0.72; 0.19 with one unit for all
+// heads), where the products' issue is the bound; one request of 1,900 positions 10.6 us, one of
+// 100,000 24 us. The unit of the weights is decided with the maximum, by one vote, from log2 of the scales: a
+// vote of its own on the products, after the exponentials, cost 140 us in place of 132 at 16 heads and d = 64.
 #include <cmath>
 
 #include "sa_cross.cuh"
@@ -36,7 +39,8 @@ namespace {
 
 using cross::kLn2;
 using cross::kLog2e;
-constexpr float kRaise = 8.f;  // raise the running maximum only when passed by this (log2 units)
+constexpr float kRaise = 8.f;  // raise a running maximum only when passed by this (log2 units)
+constexpr float kUnits = 126.f;  // FP8: 2^m and the unit of o are at most this far apart
 constexpr int kMaxWarps = 12;
 
 template <int D, bool FP8, int NT>
@@ -229,26 +233,31 @@ struct Part {
 template <int D, int NT>
 struct State {
   float o[D / 16][NT][4];
-  int ve;  // FP8: o is in units of 2^ve
+  float r[NT][2], u[NT][2];  // FP8: o is in units of 2^r; u = 2^(m - r)
   float m[NT][2], l[NT][2];  // heads 8 nt + 2 (lane mod 4) and the next; l summed over this lane's keys
   __device__ void clear() {
-    ve = -126;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      r[n][0] = r[n][1] = -INFINITY;
+      u[n][0] = u[n][1] = 1.f;
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
   }
-  __device__ void plain_units() {
-    const float f = pow2i(ve);
+  __device__ void scale_o(int n, float f0, float f1) {  // of the two heads
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int i = 0; i < D / 16; ++i) {
+      o[i][n][0] *= f0;
+      o[i][n][1] *= f1;
+      o[i][n][2] *= f0;
+      o[i][n][3] *= f1;
+    }
+  }
+  __device__ void plain_units() {  // 2^m, as l
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[i][n][x] *= f;
+    for (int n = 0; n < NT; ++n) scale_o(n, 1.f / u[n][0], 1.f / u[n][1]);
   }
   __device__ void sum_l() {  // over the lanes that hold other keys of the same head
 #pragma unroll
@@ -571,55 +580,52 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
           for (int mt = 1; mt < MT; ++mt) mx[n][e] = fmax3(mx[n][e], s[mt][n][e], s[mt][n][2 + e]);
         }
-      bool raise = false;
-      float fv = 1.f;  // FP8: the change of o's unit
+      float mw[NT][2];  // FP8: the maximum of log2(p v_scale) + m
       if (FP8) {
-        uint32_t top = 0;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          const float v0 = lg2_approx(fabsf(ksc[T + mt * 16 + g])), v1 = lg2_approx(fabsf(ksc[T + mt * 16 + g + 8]));
 #pragma unroll
-          for (int hi = 0; hi < 2; ++hi)
-            top = max(top, __float_as_uint(ksc[T + mt * 16 + g + 8 * hi]) & 0x7fffffffu);
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const int e = min((int)(top >> 23) - 126, 126);  // 2^e is above every scale
-        if (e > st.ve) {
-          fv = pow2i(max(st.ve - e, -126));
-          st.ve = e;
-          raise = true;
+            for (int e = 0; e < 2; ++e) {
+              const float w0 = s[mt][n][e] + v0, w1 = s[mt][n][2 + e] + v1;
+              mw[n][e] = mt == 0 ? fmaxf(w0, w1) : fmax3(mw[n][e], w0, w1);
+            }
         }
       }
+      bool raise = false;  // (the vote goes over the lanes: their maxima are only needed behind it)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], x));
-          raise = raise || mx[n][e] - st.m[n][e] > kRaise;
-        }
+        for (int e = 0; e < 2; ++e)
+          raise = raise || mx[n][e] - st.m[n][e] > kRaise || (FP8 && mw[n][e] - st.r[n][e] > kRaise);
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], x));
             const float mm = fmaxf(st.m[n][e], mx[n][e]);
             f[e] = st.m[n][e] > -INFINITY ? ex2_approx(st.m[n][e] - mm) : 0.f;
             st.m[n][e] = mm;
             st.l[n][e] *= f[e];
-            if (FP8) f[e] *= fv;
-          }
+            if (FP8) {
 #pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            st.o[y][n][0] *= f[0];
-            st.o[y][n][1] *= f[1];
-            st.o[y][n][2] *= f[0];
-            st.o[y][n][3] *= f[1];
+              for (int x = 4; x < 32; x <<= 1) mw[n][e] = fmaxf(mw[n][e], __shfl_xor_sync(0xffffffffu, mw[n][e], x));
+              float r = mw[n][e] - st.r[n][e] > kRaise ? ceilf(mw[n][e]) : st.r[n][e];
+              r = fmaxf(fminf(r, mm + kUnits), mm - kUnits);  // (u and 1 / u are normal numbers)
+              f[e] = st.r[n][e] > -INFINITY ? ex2_approx(st.r[n][e] - r) : 0.f;
+              st.r[n][e] = r;
+              st.u[n][e] = mm > -INFINITY ? ex2_approx(mm - r) : 1.f;
+            }
           }
+          st.scale_o(n, f[0], f[1]);
         }
       }
       uint32_t pf[MT][NT][2];
-      const float vdown = FP8 ? pow2i(-st.ve) : 1.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0 = st.m[n][0] == -INFINITY ? 0.f : st.m[n][0];
@@ -632,9 +638,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             st.l[n][0] += e0;
             st.l[n][1] += e1;
             if (FP8) {
-              const float vs = ksc[T + mt * 16 + g + 8 * hi] * vdown;
-              e0 *= vs;
-              e1 *= vs;
+              const float vs = ksc[T + mt * 16 + g + 8 * hi];
+              e0 = e0 * vs * st.u[n][0];
+              e1 = e1 * vs * st.u[n][1];
             }
             pf[mt][n][hi] = transpose8(FP8 ? cvt_f16x2(e0, e1) : cvt_bf16x2(e0, e1));
           }
