@@ -12,9 +12,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
+import warnings
 
 import torch
+
+from .build import calls_path
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsa_sketch.so")
 
@@ -135,10 +140,28 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
-# The usual calls of the attention with heads, in C++ (csrc/sa_calls.cpp): checks, allocations and
-# the C ABI call in a third of the host time. They return None for any other call, which
-# the functions below then check step by step and make themselves.
-from . import _calls  # noqa: E402
+
+
+def _load_calls():
+    """The usual calls of the attention with heads, in C++ (csrc/sa_calls.cpp): checks, allocations
+    and the C ABI call in a third of the host time. They return None for any other call, which
+    the functions below then check step by step and make themselves, as they make all of them
+    where the extension is missing (None)."""
+    path, name = calls_path(), f"{__package__}._calls"
+    try:
+        spec = importlib.util.spec_from_file_location(
+            name, path, loader=importlib.machinery.ExtensionFileLoader(name, path))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        if torch.version.cuda is not None:
+            warnings.warn(f"no extension for the short calls ({e}): they take longer on the host; "
+                          "run python -m prototype_sketch_attention_b200.build", RuntimeWarning)
+        return None
+
+
+_calls = _load_calls()
 
 
 # ---------------------------------------------------------------- raw C ABI
@@ -877,7 +900,7 @@ def cross_attention(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.Tensor, V
     [n_q, H, d] bf16, lse [n_q, H] fp32 and, for the backward, what rounding took from out (rest,
     like out; want_rest=False leaves it away). They are written into `out` ({"out", "lse"} and,
     if wanted, "rest") when given."""
-    if out is None and stream is None:
+    if _calls is not None and out is None and stream is None:
         res = _calls.cross_forward(Q, q_offsets, K, V, kv_offsets, key_mask, scale, bool(want_rest), ws)
         if res is not None:
             return _result(res, "sa_cross_attn_forward")
@@ -920,7 +943,7 @@ def cross_attention_backward(Q: torch.Tensor, q_offsets: torch.Tensor, K: torch.
     [n_q, H, d] bf16: dQ [n_q, H, d], dK and dV [n_kv, Hkv, d], bf16 (sa_cross_attn_backward),
     written into `out` ({"dQ", "dK", "dV"}) when given. Other arguments as passed to the
     forward."""
-    if out is None and stream is None:
+    if _calls is not None and out is None and stream is None:
         res = _calls.cross_backward(Q, q_offsets, K, V, kv_offsets, key_mask, scale, fwd.get("out"),
                                     fwd.get("lse"), fwd.get("rest"), dout, ws)
         if res is not None:
@@ -1007,7 +1030,7 @@ def page_tables(cached_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: t
     and new_offsets [R + 1] int64, seq_lens [R] int32, free_used [1] int64. Too few pages and
     the like are latched in the device status (device_status(result["_ws"])) and change
     nothing."""
-    if stream is None:
+    if _calls is not None and stream is None:
         res = _calls.page_tables(cached_lens, new_lens, free_pages, block_table, page_size, n_slots,
                                  free_used, ws)
         if res is not None:
@@ -1053,7 +1076,7 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
     """Writes rows K, V [n, Hkv, d] bf16 (rows may be strided) into the slots [n] int64 of a
     paged_cache, quantised for an FP8 cache (sa_paged_append). Slots outside the cache, such as
     the -1 of page_tables, are skipped; a slot must not be named twice."""
-    if stream is None and isinstance(cache, dict):
+    if _calls is not None and stream is None and isinstance(cache, dict):
         res = _calls.paged_append(K, V, slots, cache.get("K"), cache.get("V"), cache.get("k_scales"),
                                   cache.get("v_scales"))
         if res == SA_OK:
@@ -1085,7 +1108,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
     positions (0: all) of its seq_lens [R] int32 in a paged_cache, through block_table
     [R, max_pages] int32 (sa_paged_attn). Returns out [R, H, d] bf16 and lse [R, H] fp32. Bad
     lengths and page ids are latched in the device status (device_status(result["_ws"]))."""
-    if stream is None and isinstance(cache, dict):
+    if _calls is not None and stream is None and isinstance(cache, dict):
         res = _calls.paged_attention(Q, cache.get("K"), cache.get("V"), cache.get("k_scales"),
                                      cache.get("v_scales"), block_table, seq_lens, window, scale, ws)
         if res is not None:

@@ -7,7 +7,8 @@ objects link into prototype_sketch_attention_b200/libsa_sketch.so. The CUDA runt
 is linked statically and the driver API is reached through
 cudaGetDriverEntryPoint, so the library needs no -lcuda. csrc/sa_calls.cpp, the Python
 extension through which the binding makes its short calls, is compiled with g++ against
-torch into prototype_sketch_attention_b200/_calls.so.
+torch into prototype_sketch_attention_b200/_calls.<Python>.torch-<version>.so (not where torch
+has no CUDA: the binding works without it).
 """
 from __future__ import annotations
 
@@ -25,7 +26,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsa_sketch.so")
-CALLS = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["sa_host.cu", "sa_prep.cu", "sa_fwd_sm100.cu", "sa_fwd_simt.cu", "sa_bwd_simt.cu",
            "sa_gemm_sm100.cu", "sa_bwd_tc.cu",
@@ -69,14 +69,23 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def calls_path() -> str:
+    """The extension of the short calls, named after the Python and the torch that it is compiled
+    against: under others it is not found, rather than loaded."""
+    import torch
+    return os.path.join(PKG, f"_calls.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
 def _build_calls(force: bool) -> None:
     """csrc/sa_calls.cpp against the installed torch, linked to libsa_sketch.so beside it."""
-    src = os.path.join(CSRC, "sa_calls.cpp")
-    if not force and _mtime(CALLS) >= max(_mtime(src), _mtime(os.path.join(INCLUDE, "sa_sketch.h")), _mtime(__file__)):
-        return
     import torch
+    src, to = os.path.join(CSRC, "sa_calls.cpp"), calls_path()
+    if torch.version.cuda is None:  # nothing to link it to
+        return
+    if not force and _mtime(to) >= max(_mtime(src), _mtime(os.path.join(INCLUDE, "sa_sketch.h")), _mtime(__file__)):
+        return
     home = os.path.dirname(torch.__file__)
-    lib, tmp = os.path.join(home, "lib"), CALLS + f".tmp{os.getpid()}"
+    lib, tmp = os.path.join(home, "lib"), to + f".tmp{os.getpid()}"
     includes = [INCLUDE, os.path.join(home, "include"),
                 os.path.join(home, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
@@ -88,7 +97,7 @@ def _build_calls(force: bool) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for sa_calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, to)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
