@@ -1094,8 +1094,8 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cache: d
     ks, vs = _rows_stride(where, "K", K, Hkv, d), _rows_stride(where, "V", V, Hkv, d)
     with _on(where, dev, stream):
         st = sa_paged_append(_ptr(K), ks, _ptr(V), vs, _ptr(slots), K.shape[0], Hkv, d, fmt,
-                             _ptr(cache["K"]), _ptr(cache["V"]), _ptr(cache["k_scales"]),
-                             _ptr(cache["v_scales"]), n_pages, page_size, _stream(stream, dev))
+                             _ptr(cache["K"]), _ptr(cache["V"]), _ptr(cache.get("k_scales")),
+                             _ptr(cache.get("v_scales")), n_pages, page_size, _stream(stream, dev))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_paged_append")
     _used_on(stream, dev, K, V, slots, cache)
@@ -1136,7 +1136,7 @@ def paged_attention(Q: torch.Tensor, cache: dict, block_table: torch.Tensor,
                 raise SketchAttentionError(SA_ERR_UNSUPPORTED, "sa_paged_attn_workspace_size")
             ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         st = sa_paged_attn(_ptr(Q), qs, R, H, d, _ptr(cache["K"]), _ptr(cache["V"]),
-                           _ptr(cache["k_scales"]), _ptr(cache["v_scales"]), fmt, n_pages,
+                           _ptr(cache.get("k_scales")), _ptr(cache.get("v_scales")), fmt, n_pages,
                            page_size, Hkv, _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
                            int(window), _scale(scale, d), _ptr(out["out"]), _ptr(out["lse"]),
                            _ptr(ws), ws.nbytes, _stream(stream, dev))
