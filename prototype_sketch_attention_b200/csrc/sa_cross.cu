@@ -120,10 +120,12 @@ __device__ __forceinline__ void stats_rows(const CrossArgs& a, int pg, long long
 // The forward's schedule, one block. An item is a query tile of one head group; its cost in
 // half steps is 2 per key tile (1 when the rows fit in one 128-row tile) and a constant for
 // its start and end. CTA b starts where the items' costs, in order, reach b / CTAs of their sum,
-// rounded to an even key tile, or (cuts = false) to the nearer end of the item.
+// rounded to an even key tile. (Boundaries rounded to whole items, with nothing to join, took 6 % less time
+// with 8 items a CTA, 1 % less with 16 to 32, and three times as long with one user of 50,000 keys among 160
+// of 200: 305 against 105 us at d = 64.)
 __global__ void __launch_bounds__(1024)
 cross_schedule_kernel(const int64_t* __restrict__ qoff, const int64_t* __restrict__ koff, int R, long long n_q,
-                      long long n_kv, int tokens, int groups, int ctas, bool cuts, WsHeader* hdr,
+                      long long n_kv, int tokens, int groups, int ctas, WsHeader* hdr,
                       cross::Tile* __restrict__ tiles, long long* __restrict__ costs,
                       cross::Start* __restrict__ starts) {
   griddep_launch_dependents();
@@ -226,13 +228,8 @@ cross_schedule_kernel(const int64_t* __restrict__ qoff, const int64_t* __restric
     const long long in = at - costs[lo] * groups;
     cross::Start s{lo, (int)(in / c), (int)(in % c), 0};
     s.key = max(0, two ? (s.key - 4) / 2 : s.key - 3);
-    if (cuts) {
-      s.key = (s.key + 1) / 2 * 2;
-      if (s.key > nkt - 2) s.key = nkt;
-    } else {
-      s.key = 2 * s.key >= nkt ? nkt : 0;
-    }
-    if (s.key >= nkt) {  // the next item
+    s.key = (s.key + 1) / 2 * 2;
+    if (s.key > nkt - 2) {  // the next item
       s.key = 0;
       if (++s.group == groups) {
         s.group = 0;
@@ -280,7 +277,6 @@ cross::CrossGeo geometry(int R, long long n_q, long long n_kv, int H, int Hkv, i
   if (s > most) s = most;
   g.splits = s < 1 ? 1 : (int)s;
   g.ctas = sms;
-  g.cuts = ctas < 8LL * sms;  // with more items a CTA than that, whole ones are even enough
   return g;
 }
 
@@ -318,11 +314,9 @@ size_t cross_plan(int R, long long n_q, long long n_kv, int H, int Hkv, int d, b
   } else {
     q.costs = take((size_t)(g.pair_tiles + 1) * sizeof(long long));
     q.starts = take((size_t)(g.ctas + 1) * sizeof(cross::Start));
-    if (g.cuts) {
-      q.joins = take((size_t)g.ctas * (sizeof(cross::JoinItem) + sizeof(int)));
-      q.part_o = take((size_t)2 * g.ctas * 256 * d * sizeof(float));
-      q.part_lse = take((size_t)2 * g.ctas * 256 * sizeof(float));
-    }
+    q.joins = take((size_t)g.ctas * (sizeof(cross::JoinItem) + sizeof(int)));
+    q.part_o = take((size_t)2 * g.ctas * 256 * d * sizeof(float));
+    q.part_lse = take((size_t)2 * g.ctas * 256 * sizeof(float));
   }
   q.total = o;
   if (p) *p = q;
@@ -333,7 +327,7 @@ cudaError_t launch_cross_forward(const CrossArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const cross::CrossGeo g = geometry(a.R, a.n_q, a.n_kv, a.H, a.Hkv, a.sms);
   cross_schedule_kernel<<<1, 1024, 0, s>>>(
-      a.qoff, a.koff, a.R, a.n_q, a.n_kv, 128 / g.pg, a.H / g.pg, g.ctas, g.cuts,
+      a.qoff, a.koff, a.R, a.n_q, a.n_kv, 128 / g.pg, a.H / g.pg, g.ctas,
       reinterpret_cast<WsHeader*>(ws + a.plan.hdr), reinterpret_cast<cross::Tile*>(ws + a.plan.qtiles),
       reinterpret_cast<long long*>(ws + a.plan.costs), reinterpret_cast<cross::Start*>(ws + a.plan.starts));
   const cudaError_t e = cudaGetLastError();

@@ -217,8 +217,7 @@ struct CrossGeo {
   long long pair_tiles;  // bound on the 256-row query tiles of all users
   long long key_tiles;   // bound on the 128-row key tiles of all users
   int splits;            // backward: CTAs that share a query tile's keys
-  int ctas;              // forward: CTAs, and whether their boundaries may cut an item
-  bool cuts;
+  int ctas;              // forward: CTAs
 };
 
 // 3-D tensor map over bf16 rows of heads [n, heads, d], rows `stride` elements apart: boxes of

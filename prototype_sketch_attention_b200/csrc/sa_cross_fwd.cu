@@ -98,7 +98,7 @@ struct FwdParams {
   __nv_bfloat16* out;    // [n_q, H, D]
   __nv_bfloat16* rest;   // [n_q, H, D], nullable: out's rounding
   float* lse;            // [n_q, H]
-  JoinItem* joins;       // [CTAs]; null: no boundary cuts an item
+  JoinItem* joins;       // [CTAs]
   int* join_ctas;        // [CTAs]: from b on, the CTAs behind CTA b that work on joins[b]
   int ctas;
   float* part_o;         // [2 CTAs][256, D]
@@ -393,7 +393,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       }
     }
     __syncwarp();
-    if (a.joins) {  // what the join has to know, while the others work
+    {  // what the join has to know, while the others work
       const int b = blockIdx.x;
       const Start at = a.starts[b], end = a.starts[b + 1];
       const bool any = a.hdr->total_tiles > 0, same = at.tile == end.tile && at.group == end.group;
@@ -799,7 +799,7 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.rest = static_cast<__nv_bfloat16*>(a.rest);
   p.lse = a.lse;
-  p.joins = geo.cuts ? reinterpret_cast<JoinItem*>(ws + a.plan.joins) : nullptr;
+  p.joins = reinterpret_cast<JoinItem*>(ws + a.plan.joins);
   p.join_ctas = reinterpret_cast<int*>(p.joins + geo.ctas);
   p.ctas = geo.ctas;
   p.part_o = reinterpret_cast<float*>(ws + a.plan.part_o);
@@ -813,7 +813,6 @@ cudaError_t launch_t(const CrossArgs& a, const CrossGeo& geo, cudaStream_t s) {
   if ((e = launch_dependent(cross_fwd_kernel<D>, dim3((unsigned)geo.ctas), dim3(kThreads), smem, s, tq, tk, tv,
                             p)) != cudaSuccess)
     return e;
-  if (!geo.cuts) return cudaSuccess;
   return launch_dependent(cross_join_kernel<D>, dim3((unsigned)geo.ctas, 8), dim3(256), 0, s, p);
 }
 

@@ -1,6 +1,6 @@
-"""The cross attention's forward with so many items that its blocks' boundaries fall between them (8 items
-a multiprocessor and more: no item is cut, none joined), and just below that, against the 64-bit
-reference: several key tiles and head groups, masks, the output's rest, users without queries or keys."""
+"""The cross attention with many items a block (8 a multiprocessor and more, and just below that), one very
+long user among short ones with them, against the 64-bit reference: several key tiles and head
+groups, masks, the output's rest, users without queries or keys."""
 import pytest
 import torch
 
@@ -28,7 +28,7 @@ CASES = [
     (130, 60, 300, 12, 4, 0),
     (160, 300, 400, 16, 4, 0),
     (320, 5, 513, 4, 4, 20000),
-    (110, 40, 700, 8, 8, 0),  # below: items are cut
+    (110, 40, 700, 8, 8, 0),  # below
 ]
 
 
@@ -39,7 +39,7 @@ def test_against_reference(users, q, k, H, Hkv, longest, masked, d):
     lq, lk = _lengths(users, q, k)
     lq[3], lk[users // 2] = 0, longest or lk[users // 2]
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    assert (_items(lq, H, Hkv) >= 8 * sms) == (users != 110)  # (the host's count, by user and head group, is about this)
+    assert (_items(lq, H, Hkv) >= 8 * sms) == (users != 110)
     Q, K, V, dout = _inputs(lq, lk, H, Hkv, d, seed=1000 + users)
     qo, ko = _offsets(lq), _offsets(lk)
     mask = None
