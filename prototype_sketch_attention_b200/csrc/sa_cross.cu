@@ -268,8 +268,11 @@ cross::CrossGeo geometry(int R, long long n_q, long long n_kv, int H, int Hkv, i
   const long long pair = 256 / g.pg, some = R < n_q ? R : n_q;
   g.pair_tiles = n_q / pair + some;
   g.key_tiles = n_kv / 128 + (R < n_kv ? R : n_kv);
-  // With fewer CTAs than SMs (about one per user and head group, or per full tile), the
-  // keys are split so that the SMs fill up, down to four key tiles a split.
+  // With fewer CTAs than SMs (about one per user and head group, or per full tile), the keys of the
+  // backward's dQ items are split so that the SMs fill up, down to four key tiles a split. Measured at
+  // d = 128, by the rule and with one split: a user's 40 queries, 8 heads over 2, 10K keys: 31 and 100 us; 1
+  // query, 30K keys: 47 and 283; 4 users x 40 queries, 5K keys: 43 and 66; 8 users, 4 heads over 4, 3K
+  // keys: 53 and 65; 2 users x 300 queries, 8 over 8, 2K keys: 44 and 41.
   const long long full = (n_q + pair - 1) / pair;
   const long long ctas = (full > some ? full : some) * (H / g.pg);
   long long s = ctas > 0 ? sms / ctas : 1;

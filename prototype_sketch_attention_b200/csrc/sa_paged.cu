@@ -299,6 +299,8 @@ void append_t(const PagedAppendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t s) {
+  // eight slots a thread once one a thread fills all threads (1 and 8, us: 300 slots 4.3 and 12.4; 90,000 6.3
+  // and 6.3; 300,000 8.3 and 6.3; 6 M 43 and 16.5)
   const int v = a.n_slots > 2LL * a.sms * kUsers ? 8 : 1;
   long long g = (a.n_slots + v * kUsers - 1) / (v * kUsers);  // at most one pass of the threads each
   if (g < 1) g = 1;
