@@ -28,7 +28,7 @@
 // Bound: at d = 128 a tile costs 1,024 tensor clocks and 1,024 clocks of exponentials (16 a
 // clock and SM); at d = 64 the exponentials bound it. Measured (4 d H a pair): 4 x 4096 queries and
 // keys, 8 heads of 128: 255 us, 1,077 TFLOP/s (265 with the rest); 40 x 300 over 10K keys, 8 heads over
-// 2: 510 us, 960 TFLOP/s; 8 heads of 64 over 1,024 keys of their own: 90 us, where the last 44
+// 2: 510 us, 960 TFLOP/s; 8 heads of 64 over 1,024 keys of their own: 92 us, where the last 44
 // rows of each user's 300 fill a third of a tile and an item has 8 steps a tile.
 #include <cmath>
 
@@ -41,6 +41,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRaise = 8.f;
+constexpr uint32_t kRest = 32;  // one-tile items: a half of P's rest lies this many columns behind it
 // The softmax warpgroups keep a row's 128 scores in registers. setmaxnreg.inc draws on the
 // launch's 384 x 168 registers, so the split stays within them, and the launch refuses a build
 // compiled to fewer.
@@ -256,6 +257,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int s = 0; ok && get_item(bars, items, s, lane, status, a.budget, &it); ++s) {
       const bool two = broadcast(it.two);
       const int n = broadcast(it.n), steps = two ? 2 * n : n;
+      const bool wide = n == 1;  // P's rest, too (an item that is cut leaves pieces of two tiles at least)
       if (n == 0) continue;
       wait(bar(bars->q_full), (uint32_t)(nq & 1));
       ++nq;
@@ -292,13 +294,22 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           else mma_ts<1>(o, p, b, kDescHi, id_o);
 #pragma unroll
           for (int ks = 1; ks < 4; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          if (wide) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma_ts<1>(o, p + kRest + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          }
         }
         __syncwarp();
         if (!wait(pf + 8, pb.ph)) break;
         tc_fence_after();
         if (elect_one()) {
+          const uint32_t p1 = p + 32 + (wide ? kRest : 0);
 #pragma unroll
-          for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p + 8 * ks, b + mn_step(ks), kDescHi, id_o);
+          for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p1 + 8 * (ks - 4), b + mn_step(ks), kDescHi, id_o);
+          if (wide) {
+#pragma unroll
+            for (int ks = 4; ks < 8; ++ks) mma_ts<1>(o, p1 + kRest + 8 * (ks - 4), b + mn_step(ks), kDescHi, id_o);
+          }
           tc_commit(bar(bars->o_done[0]) + 8 * w);
           if (q + 2 >= steps) tc_commit(bar(bars->o_last[0]) + 8 * w);
           if (last_use) tc_commit(bar(bars->empty[0]) + 8 * vpos.st);
@@ -451,7 +462,66 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     for (int q = (two ? 2 * nkt : nkt) % (2 * kNB); q > 0; --q) base.next();
     MaskBytes mb;
     if (first < nkt) mb.load(a.mask, k0 + 128 * first, k1, lane);
-    for (int j = first; j < nkt; j += step, ++n, par ^= kCnt) {
+    if (nkt == 1 && first == 0) {
+      // At most 128 keys: P enters the product as two bf16, its value and what that rounding took. Of few keys
+      // P's rounding does not average out, and the gradients' delta = dout . out inherits it: dQ and dK were off
+      // by up to 1.52 times what fp32 sums and one rounding give (3 keys), and are by 1.43, of which dS's
+      // rounding makes 1.41. Half of the scores at a time, to 32 columns of P and 32 of its rest in their
+      // place. In this block of its own, with short loops: in the loop below the values that the rest needs
+      // cost long items 4 to 7 %; so 40 x 300 over 1,024 keys take 2 % more, 100 x 300 over 128 keys 5 %.
+      uint32_t keep[4];
+      const bool drop = mb.vote(a.mask, k0, k1, lane, keep);
+      ok = mbar_wait_warp(smem_u32(&bars->s_full[sb.st]), sb.ph, status, a.budget);
+      const uint32_t st = tmem + lane_off + 128 * sb.st;
+      tc_fence_after();
+      auto scores = [&](int i, uint32_t (&x)[32]) {
+        tmem_ld32_raw(st + 32 * i, x);
+        tmem_wait_tie(x);
+        if (drop) {
+          const uint32_t kw = i == 0 ? keep[0] : i == 1 ? keep[1] : i == 2 ? keep[2] : keep[3];
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            if (!((kw >> y) & 1u)) x[y] = 0xff800000u;  // -inf
+        }
+      };
+      if (ok) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[32];
+          scores(i, x);
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) m = fmax3(m, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t x[32];
+            scores(2 * h + i, x);
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              const float z0 = ex2_approx(fmaf(__uint_as_float(x[y]), c, -mc));
+              const float z1 = ex2_approx(fmaf(__uint_as_float(x[y + 1]), c, -mc));
+              sum[0] += z0;
+              sum[1] += z1;
+              hi[16 * i + y / 2] = round_pair(z0, z1, lo[16 * i + y / 2]);
+            }
+          }
+          tmem_st32(st + 2 * kRest * h, hi);
+          tmem_st32(st + 2 * kRest * h + kRest, lo);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[sb.st][h]));
+        }
+        l = sum[0] + sum[1];
+        n = 1;
+        par ^= kCnt;
+      }
+    } else for (int j = first; j < nkt; j += step, ++n, par ^= kCnt) {
       uint32_t keep[4];
       const bool drop = mb.vote(a.mask, k0 + 128 * j, k1, lane, keep);
       if (j + step < nkt) mb.load(a.mask, k0 + 128 * (j + step), k1, lane);
