@@ -256,7 +256,8 @@ __device__ __forceinline__ uint2 quantise(uint4 w, unsigned mask, float* scale) 
 }
 
 // One (new position, key head) per LANES = d / 8 lanes, 16 bytes of K and of V each. Bound by
-// reading the rows and writing the cache once; IDX is 32 bits where the rows fit (a 64-bit
+// reading the rows and writing the cache once in bf16 (300,001 rows of 2 heads of 128: 100 us, 0.94 of a copy's
+// rate); in FP8 (140 us, 0.51) a lane makes 16 divisions for its 48 bytes. IDX is 32 bits where the rows fit (a 64-bit
 // division a row costs more than its bytes).
 template <int LANES, bool FP8, typename IDX>
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedAppendArgs a) {
