@@ -298,15 +298,25 @@ def sketch_pack(S: torch.Tensor, fmt: int = SA_CODEC_FP8, stream=None) -> dict:
 
 def sketch_unpack(packed: dict, stream=None) -> torch.Tensor:
     """The fp32 sketches back from sketch_pack's output."""
+    where = "sketch_unpack"
     codes, fmt = packed["codes"], packed["format"]
-    d = codes.shape[-1]
-    with _on("sketch_unpack", codes.device, stream):
+    _require(fmt in (SA_CODEC_BF16, SA_CODEC_FP8), where, f"unknown format {fmt}")
+    _require(isinstance(codes, torch.Tensor) and codes.dim() >= 2 and codes.shape[-1] > 0, where,
+             "codes must be [..., d]")
+    d, size = codes.shape[-1], 1 if fmt == SA_CODEC_FP8 else 2
+    _require(codes.element_size() == size, where, f"{codes.dtype} codes; format {fmt} has {size} bytes a code")
+    _check_tensor(where, "codes", codes, tuple(codes.shape), codes.dtype)
+    scales = packed.get("scales") if fmt == SA_CODEC_FP8 else None
+    if fmt == SA_CODEC_FP8:
+        _check_tensor(where, "scales", scales, tuple(codes.shape[:-1]), torch.float32, codes.device)
+    _check_cuda(where, codes)
+    with _on(where, codes.device, stream):
         S = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-        st = sa_sketch_unpack(_ptr(codes), _ptr(packed.get("scales")), codes.numel() // d, d, fmt,
-                              _ptr(S), _stream(stream, codes.device))
+        st = sa_sketch_unpack(_ptr(codes), _ptr(scales), codes.numel() // d, d, fmt, _ptr(S),
+                              _stream(stream, codes.device))
     if st != SA_OK:
         raise SketchAttentionError(st, "sa_sketch_unpack")
-    _used_on(stream, codes.device, packed, S)
+    _used_on(stream, codes.device, codes, scales, S)
     return S
 
 
